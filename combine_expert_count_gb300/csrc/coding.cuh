@@ -1,0 +1,45 @@
+// coding.cuh -- the block-128 e4m3 coding of fp32 values, as the dispatch
+// codes its rows: scale = amax / 448 (fp32 division), code = e4m3 round to
+// nearest even of v / scale (fp32 division), saturating; a block of zeros has
+// scale 0 and zero bytes.  A NaN makes its block's scale and codes NaN (the
+// dispatch leaves NaN out of amax, so a block of nothing but NaN is coded as
+// zeros there; a norm or a product should not lose it).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+// |v| as bits: their order as unsigned integers is that of the magnitudes,
+// with NaN above infinity, so an integer maximum finds amax and keeps NaN.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    return m;
+}
+
+__device__ __forceinline__ float block_scale(uint32_t amax) {
+    return __fdiv_rn(__uint_as_float(amax), 448.0f);
+}
+
+// Four values to four codes, the first in the low byte.
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float scale) {
+    const uint32_t lo = (uint32_t)__nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = (uint32_t)__nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(c, scale), __fdiv_rn(d, scale)), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// Eight values of a block whose scale is known (0: a block of zeros).
+__device__ __forceinline__ uint2 code8(const float (&v)[8], float scale) {
+    if (scale == 0.0f) return make_uint2(0u, 0u);
+    return make_uint2(code4(v[0], v[1], v[2], v[3], scale), code4(v[4], v[5], v[6], v[7], scale));
+}
+
+}  // namespace moe

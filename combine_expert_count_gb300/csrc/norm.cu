@@ -1,0 +1,112 @@
+// norm.cu -- moe_rmsnorm: residual addition, RMS norm and block-128 e4m3
+// coding of the rows of x in one pass.
+#include <cmath>
+
+#include "bf16.cuh"
+#include "check.h"
+#include "coding.cuh"
+#include "launch.h"
+#include "trace.h"
+
+namespace moe {
+
+__device__ __forceinline__ void unpack8(float (&v)[8], const uint4 &w) {
+    v[0] = bf16_lo(w.x);
+    v[1] = bf16_hi(w.x);
+    v[2] = bf16_lo(w.y);
+    v[3] = bf16_hi(w.y);
+    v[4] = bf16_lo(w.z);
+    v[5] = bf16_hi(w.z);
+    v[6] = bf16_lo(w.w);
+    v[7] = bf16_hi(w.w);
+}
+
+// One CTA per row.  A thread holds V chunks of eight elements in registers
+// from the load to the last store, chunk tid + i * blockDim.x, so a row is
+// read once; blockDim.x is a multiple of 32, so the sixteen chunks of a block
+// of 128 are sixteen neighbouring lanes.
+template <int V>
+__global__ void __launch_bounds__(V == 8 ? 1024 : 256) k_rmsnorm(int H, float eps, const uint16_t *x, const uint16_t *res,
+                          const uint16_t *__restrict__ gamma, uint16_t *res_out, uint16_t *y,
+                          uint8_t *__restrict__ q, float *__restrict__ s) {
+    __shared__ float wsum[32];
+    const int tid = threadIdx.x, nthr = blockDim.x, nch = H >> 3;
+    const size_t row = blockIdx.x, base = row * (size_t)H;
+    float v[V][8], acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nthr;
+        if (c >= nch) continue;
+        unpack8(v[i], *reinterpret_cast<const uint4 *>(x + base + c * 8));
+        if (res) add8(v[i], *reinterpret_cast<const uint4 *>(res + base + c * 8));
+        if (res_out) *reinterpret_cast<uint4 *>(res_out + base + c * 8) = pack_bf16x8(v[i]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) acc = __fmaf_rn(v[i][u], v[i][u], acc);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(kFull, acc, d);
+    if ((tid & 31) == 0) wsum[tid >> 5] = acc;
+    __syncthreads();
+    float sum = 0.0f;
+    for (int w = 0; w < (nthr >> 5); ++w) sum += wsum[w];
+    const float rstd = __frsqrt_rn(sum / (float)H + eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nthr;
+        const bool in = c < nch;
+        uint32_t amax = 0;
+        if (in) {
+            float g[8];
+            unpack8(g, __ldg(reinterpret_cast<const uint4 *>(gamma + c * 8)));
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * g[u];
+            if (y) *reinterpret_cast<uint4 *>(y + base + c * 8) = pack_bf16x8(v[i]);
+            amax = amax8(v[i]);
+        }
+        if (q) {
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, d));
+            if (in) {
+                const float scale = block_scale(amax);
+                *reinterpret_cast<uint2 *>(q + base + c * 8) = code8(v[i], scale);
+                if ((c & 15) == 0) s[row * (size_t)(H >> 7) + (c >> 4)] = scale;
+            }
+        }
+    }
+}
+
+static cudaError_t launch_rmsnorm(const moe_shape &sh, float eps, const uint16_t *x,
+                                  const uint16_t *res, const uint16_t *gamma, uint16_t *res_out,
+                                  uint16_t *y, uint8_t *q, float *s, cudaStream_t st) {
+    const long long rows = (long long)sh.N * sh.T;
+    const int nch = sh.H >> 3;
+    int V = 1;
+    while (V < 8 && nch > 256 * V) V *= 2;
+    const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
+    const auto kern = V == 1 ? k_rmsnorm<1> : V == 2 ? k_rmsnorm<2> : V == 4 ? k_rmsnorm<4> : k_rmsnorm<8>;
+    return launch_kernel(kern, dim3((unsigned)rows), dim3(nthr), 0, st, sh.H, eps, x, res, gamma,
+                         res_out, y, q, s);
+}
+
+}  // namespace moe
+
+extern "C" int moe_rmsnorm(const moe_shape *sh, float eps, const uint16_t *x, const uint16_t *res,
+                           const uint16_t *gamma, uint16_t *res_out, uint16_t *y, uint8_t *q,
+                           float *s, void *stream) {
+    MOE_TRACE_CALL();
+    moe_sizes z;
+    int rc = moe_sizes_query(sh, &z);
+    if (rc != MOE_OK) return rc;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return MOE_EINVAL;
+    if ((int64_t)sh->N * sh->T == 0) return MOE_OK;
+    if ((q == nullptr) != (s == nullptr) || (!res_out && !y && !q)) return MOE_EINVAL;
+    if (!moe::ok_buffer(x, z.bytes_x) || !moe::ok_buffer(gamma, 2 * sh->H) ||
+        !moe::ok_optional(res) || !moe::ok_optional(res_out) || !moe::ok_optional(y) ||
+        !moe::ok_optional(q) || !moe::ok_optional(s))
+        return MOE_EINVAL;
+    if ((int64_t)sh->N * sh->T >= ((int64_t)1 << 31)) return MOE_ENOTSUP;
+    return moe::launch_rmsnorm(*sh, eps, x, res, gamma, res_out, y, q, s,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ECUDA;
+}

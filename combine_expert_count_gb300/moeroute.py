@@ -38,6 +38,7 @@ EXPORTS = ("moe_sizes_query", "moe_route_count", "moe_exchange", "moe_route", "m
            "moe_combine", "moe_combine_partial_send", "moe_combine_partial_recv",
            "moe_combine_partial", "moe_expert_standin",
            "moe_e4m3_encode", "moe_dispatch_ll", "moe_expert_standin_ll", "moe_combine_ll",
+           "moe_rmsnorm", "moe_expert_gemm", "moe_expert_gemm_swiglu", "moe_layer_few",
            "moe_strerror", "moe_version")
 
 
@@ -109,6 +110,10 @@ def lib() -> ctypes.CDLL:
             h.moe_dispatch_ll.argtypes = [sp] + [V] * 8 + [V]
             h.moe_expert_standin_ll.argtypes = [sp, I] + [V] * 4 + [V]
             h.moe_combine_ll.argtypes = [sp] + [V] * 5 + [V]
+            h.moe_rmsnorm.argtypes = [sp, ctypes.c_float] + [V] * 7 + [V]
+            h.moe_expert_gemm.argtypes = [sp, I, I] + [V] * 6 + [V]
+            h.moe_expert_gemm_swiglu.argtypes = [sp, I, I] + [V] * 7 + [V]
+            h.moe_layer_few.argtypes = [sp, I] + [V] * 11 + [V]
             h.moe_strerror.argtypes = [I]
             h.moe_strerror.restype = ctypes.c_char_p
             h.moe_version.argtypes = []
@@ -418,6 +423,73 @@ def moe_combine_ll(shape, y_ll, topk_w, ll_row, out, status, stream=None) -> Non
         _p(ll_row, z.bytes_topk_idx, "ll_row"), _p(out, z.bytes_x, "out"),
         _p(status, 4, "status"), _s(stream)),
         "moe_combine_ll")
+
+
+def _maybe(t, nbytes: int, name: str):
+    return None if t is None else _p(t, nbytes, name)
+
+
+def moe_rmsnorm(shape, x, gamma, eps: float, y=None, q=None, s=None, res=None, res_out=None,
+                stream=None) -> None:
+    """RMS norm of the N*T rows of ``x`` (plus ``res``) times ``gamma``: the
+    bf16 rows ``y``, their block-128 e4m3 coding (``q``, ``s``) and the sum
+    ``res_out``, each where a buffer is given."""
+    sh, z = _as_shape(shape), sizes_query(shape)
+    nq = z.bytes_x // 2
+    _check(lib().moe_rmsnorm(
+        ctypes.byref(sh), float(eps), _p(x, z.bytes_x, "x"), _maybe(res, z.bytes_x, "res"),
+        _p(gamma, 2 * sh.H, "gamma"), _maybe(res_out, z.bytes_x, "res_out"),
+        _maybe(y, z.bytes_x, "y"), _maybe(q, nq, "q"), _maybe(s, nq // 32, "s"), _s(stream)),
+        "moe_rmsnorm")
+
+
+def _product_sizes(sh: moe_shape, z: moe_sizes, n: int, k: int) -> tuple[int, int, int, int]:
+    """Bytes of a_q, a_s, w_q and w_s of a product with n outputs of k inputs."""
+    rows = sh.N * z.cap
+    return rows * k, rows * (k // 128) * 4, sh.E * n * k, sh.E * (n // 128) * (k // 128) * 4
+
+
+def moe_expert_gemm(shape, n: int, k: int, a_q, a_s, grp_off, w_q, w_s, y, stream=None) -> None:
+    """y = the grouped 8-bit rows (``a_q``, ``a_s``) times their experts' weights
+    [E][n][k]; ``grp_off`` None where every rank has one expert (E == N)."""
+    sh, z = _as_shape(shape), sizes_query(shape)
+    ba, bs, bw, bt = _product_sizes(sh, z, n, k)
+    _check(lib().moe_expert_gemm(
+        ctypes.byref(sh), int(n), int(k), _p(a_q, ba, "a_q"), _p(a_s, bs, "a_s"),
+        _maybe(grp_off, z.bytes_grp_off, "grp_off"), _p(w_q, bw, "w_q"), _p(w_s, bt, "w_s"),
+        _p(y, sh.N * z.cap * n * 2, "y"), _s(stream)),
+        "moe_expert_gemm")
+
+
+def moe_expert_gemm_swiglu(shape, inter: int, k: int, a_q, a_s, grp_off, w13_q, w13_s, h_q, h_s,
+                           stream=None) -> None:
+    """The gate and up product [E][2*inter][k], silu(gate) * up and its block-128
+    e4m3 coding (``h_q``, ``h_s``): the rows of the second product."""
+    sh, z = _as_shape(shape), sizes_query(shape)
+    ba, bs, bw, bt = _product_sizes(sh, z, 2 * inter, k)
+    rows = sh.N * z.cap
+    _check(lib().moe_expert_gemm_swiglu(
+        ctypes.byref(sh), int(inter), int(k), _p(a_q, ba, "a_q"), _p(a_s, bs, "a_s"),
+        _maybe(grp_off, z.bytes_grp_off, "grp_off"), _p(w13_q, bw, "w13_q"),
+        _p(w13_s, bt, "w13_s"), _p(h_q, rows * inter, "h_q"),
+        _p(h_s, rows * (inter // 128) * 4, "h_s"), _s(stream)),
+        "moe_expert_gemm_swiglu")
+
+
+def moe_layer_few(shape, inter: int, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, h_q, h_s, out,
+                  status, stream=None) -> None:
+    """A whole expert layer for at most MOE_FEW_MAX_TOKENS tokens; ``h_q``
+    [N][T][R][inter] and ``h_s`` [N][T][R][inter/128] are scratch."""
+    sh, z = _as_shape(shape), sizes_query(shape)
+    A, E, H = sh.N * sh.T * sh.R, sh.E, sh.H
+    nw, ns = E * inter * H, E * (inter // 128) * (H // 128) * 4
+    _check(lib().moe_layer_few(
+        ctypes.byref(sh), int(inter), _p(x, z.bytes_x, "x"),
+        _p(topk_idx, z.bytes_topk_idx, "topk_idx"), _p(topk_w, z.bytes_topk_idx, "topk_w"),
+        _p(w13_q, 2 * nw, "w13_q"), _p(w13_s, 2 * ns, "w13_s"), _p(w2_q, nw, "w2_q"),
+        _p(w2_s, ns, "w2_s"), _p(h_q, A * inter, "h_q"), _p(h_s, A * (inter // 128) * 4, "h_s"),
+        _p(out, z.bytes_x, "out"), _p(status, 4, "status"), _s(stream)),
+        "moe_layer_few")
 
 
 class MoeLLBuffers:

@@ -436,6 +436,79 @@ int moe_expert_standin_ll(const moe_shape *shape, int mode, const uint8_t *ll_q,
 int moe_combine_ll(const moe_shape *shape, const uint16_t *y_ll, const float *topk_w,
                    const int32_t *ll_row, uint16_t *out_bf16, int32_t *status, void *stream);
 
+/* ---------------------------------------------------------------- norm
+ * The norm that makes a layer's input x, with the residual's addition before
+ * it and the 8-bit coding after it, in one pass over the rows of x.  For each
+ * of the N*T rows (shape's N, T, H; E, R and cap are only checked):
+ *   v       = x + res                   fp32; v = x where res is NULL
+ *   res_out = bf16_rn(v)                the residual stream after the addition
+ *   y       = bf16_rn((v * rstd) * gamma),  rstd = 1 / sqrt(mean(v^2) + eps)
+ *   s, q    = the dispatch's block-128 coding (moe_dispatch_send) of the fp32
+ *             values (v * rstd) * gamma: one rounding, not that of y again
+ * gamma is bf16 [H].  Sums are fp32.  res, res_out, y and the pair (q, s) may
+ * each be NULL; q and s go together, and at least one output is needed.  y is
+ * the x of moe_dispatch; (q, s) feed a product with 8-bit rows directly (a
+ * shared expert).  res_out may be x or res itself (each element is read
+ * before it is written, by the same thread), likewise y; other overlaps of
+ * outputs with inputs are not allowed.  eps must be finite and >= 0. */
+int moe_rmsnorm(const moe_shape *shape, float eps, const uint16_t *x_bf16,
+                const uint16_t *res_bf16, const uint16_t *gamma_bf16, uint16_t *res_out_bf16,
+                uint16_t *y_bf16, uint8_t *q, float *s, void *stream);
+
+/* ---------------------------------------------------------------- experts
+ * The experts' products over the grouped rows: what stands between the two
+ * halves.  Weights are e4m3 with one fp32 scale per 128 x 128 block, row-major
+ * over the outputs, as 8-bit checkpoints hold them:
+ *   w_q  u8    [E][n][k]          w_s  float [E][n/128][k/128]
+ * n and k are multiples of 128 up to 65536.  Row i of rank r belongs to local
+ * expert j (e = r*Er + j) when grp_off[r][j] <= i < grp_off[r][j+1], offsets
+ * being read on the device and clipped to [0, cap]; rows of no expert, and
+ * those at or beyond cap, are left untouched.  grp_off may be NULL when E = N:
+ * each rank's cap rows are then all its one expert's (N = E = 1 is a dense
+ * product of cap rows).  Products of e4m3 values are exact; each block of 128
+ * along k is summed in fp32 by the tensor cores and added, times its two
+ * scales, to an fp32 sum over the blocks:
+ *   p[i][c] = sum_b (a_s[i][b] * w_s[e][c/128][b]) * sum_{kk in b} a_q[i][kk] * w_q[e][c][kk]
+ * Only N, E and cap of the shape matter here (the others are checked). */
+
+/* y[i][c] = bf16_rn(p[i][c]).
+ *   a_q u8 [N][cap][k], a_s float [N][cap][k/128], y bf16 [N][cap][n] */
+int moe_expert_gemm(const moe_shape *shape, int n, int k, const uint8_t *a_q, const float *a_s,
+                    const int32_t *grp_off, const uint8_t *w_q, const float *w_s,
+                    uint16_t *y_bf16, void *stream);
+
+/* The gate and up product with the activation and the coding of its result:
+ * the weights' first `inter` outputs are the gate g, the next `inter` the up u
+ * (n = 2 * inter),
+ *   h = (g / (1 + exp(-g))) * u   fp32, then the dispatch's block-128 coding:
+ *   h_q u8 [N][cap][inter], h_s float [N][cap][inter/128]
+ * the row operand of the second moe_expert_gemm. */
+int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8_t *a_q,
+                           const float *a_s, const int32_t *grp_off, const uint8_t *w13_q,
+                           const float *w13_s, uint8_t *h_q, float *h_s, void *stream);
+
+/* ---------------------------------------------------------------- a few tokens
+ * A whole expert layer for a few tokens, in two kernels and without a
+ * dispatch or combine: only the weights of the experts that some token chose
+ * are read, once.  Per token t of rank s, with the coding and the products
+ * defined above:
+ *   xq      = coding of x[s][t]                      (as moe_dispatch)
+ *   h_k     = coding of silu(g) * u, [g; u] = w13[e_k] xq   (as ..._swiglu)
+ *   out     = bf16_rn(sum_k topk_w[s][t][k] * (w2[e_k] h_k))
+ * The same steps as moe_dispatch, moe_expert_gemm_swiglu, moe_expert_gemm and
+ * moe_combine, except that an expert's output is not rounded to bf16 before
+ * the weighted sum.  Ids outside [0, E) are skipped (MOE_ST_BAD_EXPERT);
+ * *status is cleared first.  N*T <= MOE_FEW_MAX_TOKENS (MOE_ENOTSUP beyond).
+ *   w13_q u8 [E][2*inter][H], w13_s float [E][2*inter/128][H/128]
+ *   w2_q  u8 [E][H][inter],   w2_s  float [E][H/128][inter/128]
+ *   h_q u8 [N][T][R][inter], h_s float [N][T][R][inter/128]: scratch that the
+ *     call writes before it reads (rows of skipped ids stay untouched) */
+#define MOE_FEW_MAX_TOKENS 64
+int moe_layer_few(const moe_shape *shape, int inter, const uint16_t *x_bf16,
+                  const int32_t *topk_idx, const float *topk_w, const uint8_t *w13_q,
+                  const float *w13_s, const uint8_t *w2_q, const float *w2_s, uint8_t *h_q,
+                  float *h_s, uint16_t *out_bf16, int32_t *status, void *stream);
+
 /* Static description of an error code or status bit set. */
 const char *moe_strerror(int code);
 
