@@ -1,24 +1,52 @@
 // experts.cu -- the experts' products over the grouped rows: moe_expert_gemm
 // and moe_expert_gemm_swiglu.
+//
+// p[i][c] = sum over blocks b of 128 along k of
+//           (a_s[i][b] * w_s[e][c/128][b]) * sum_{kk in b} a_q[i][kk] * w_q[e][c][kk]
+//
+// One persistent CTA per SM works through tiles of 128 rows of one expert by
+// two column blocks of 128 (two neighbours of the plain product; the gate
+// block and the up block of the same activations of the other).  One warp
+// loads the operands' 128-byte-wide k blocks by TMA into a ring of four
+// stages; one thread issues the tcgen05 products of a block into one of two
+// 256-column accumulators in tensor memory; eight warps take each finished
+// block out of there and add it, times its two scales, to fp32 sums that stay
+// in registers over the whole of k.  The fp32 scales of a block are why the
+// sums leave tensor memory at every block: the tensor cores can only apply
+// power-of-two scales by themselves.  A thread holds one row, so its row's
+// scale is one number for all its columns and the gate, the up value and half
+// of the block maximum of an activation meet in one thread.
+#include <mutex>
+
 #include "bf16.cuh"
 #include "check.h"
 #include "coding.cuh"
 #include "launch.h"
 #include "mma8.cuh"
+#include "tc.cuh"
 #include "trace.h"
 
 namespace moe {
 
+constexpr int kTileRows = 128;               // rows of a tile: the lanes of tensor memory
+constexpr int kBlk = 128;                    // k block, scale block, half of a tile's columns
+constexpr int kBoxRows = 32;                 // rows of one TMA load of a: a group's last tile
+                                             // loads no more than it has, rounded up to 32
+constexpr int kStages = 4;
+constexpr int kStageBytes = 3 * kTileRows * kBlk;  // a, first and second weight block
+constexpr int kSumWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kProductThreads = 32 * 10;
+constexpr int kStageOut = 32 * 64;           // a sum warp's output staging: 32 rows of 64 bytes
+
 struct Product {
     int N, E, cap, n, k;
-    const uint8_t *a_q;
     const float *a_s;
     const int32_t *grp_off;
-    const uint8_t *w_q;
     const float *w_s;
     uint16_t *y;
     uint8_t *h_q;
     float *h_s;
+    int32_t *status;
 };
 
 // First row and row count of expert e within its rank's rows, clipped.
@@ -30,119 +58,368 @@ __device__ __forceinline__ int2 group_rows(const Product &p, int e) {
     return make_int2(b, t - b);
 }
 
-// One CTA: 16 rows of one expert by 128 outputs (kSwiglu: 128 of the gate and
-// the same 128 of the up), warp w taking 16 of each.
+struct Tile {
+    int e, rows;      // expert; rows of the tile, 1 .. 128
+    long long row0;   // first row, over all ranks
+    int blk0, blk1;   // column blocks of 128; blk1 < 0: there is none
+};
+
+// Shared memory behind the stages and the output staging.
+struct ProductShared {
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int stop, total;
+    int wsum[32];
+    uint32_t peak[2][kTileRows];
+    int first[MOE_MAX_EXPERTS + 1];  // tiles of rows before each expert
+};
+
+constexpr size_t kProductSmem =
+    1024 + (size_t)kStages * kStageBytes + (size_t)kSumWarps * kStageOut + sizeof(ProductShared);
+static_assert(kProductSmem <= 232448, "a CTA's shared memory");
+
+// Tiles run row tile first within runs of kRun row tiles, so that the CTAs at
+// work at one time share weights and rows in L2.
+constexpr int kRun = 16;
+
 template <bool kSwiglu>
-__global__ void __launch_bounds__(256) k_product_simple(const Product p) {
-    __shared__ uint32_t wmax[8][16];
-    const int e = blockIdx.z, Er = p.E / p.N;
-    const int2 g = group_rows(p, e);
-    const int r0 = blockIdx.x * 16;
-    if (r0 >= g.y) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, t4 = lane & 3;
-    const size_t row0 = (size_t)(e / Er) * p.cap + g.x + r0;
-    const int Kb = p.k >> 7, nb = p.n >> 7;
-    constexpr int kHalves = kSwiglu ? 2 : 1;
-    float acc[kHalves][2][4] = {};
-    for (int b = 0; b < Kb; ++b) {
-        uint32_t a[4][4];
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int rr = gid + (i & 1) * 8;
-                a[kk][i] = r0 + rr < g.y
-                               ? *reinterpret_cast<const uint32_t *>(
-                                     p.a_q + (row0 + rr) * p.k + b * 128 + kk * 32 + t4 * 4 + (i >> 1) * 16)
-                               : 0u;
-            }
-        const float s0 = r0 + gid < g.y ? __ldg(p.a_s + (row0 + gid) * Kb + b) : 0.0f;
-        const float s1 = r0 + gid + 8 < g.y ? __ldg(p.a_s + (row0 + gid + 8) * Kb + b) : 0.0f;
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-            const int blk = blockIdx.y + h * (nb / 2);
-            const float ws = __ldg(p.w_s + ((size_t)e * nb + blk) * Kb + b);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint8_t *w = p.w_q + ((size_t)e * p.n + blk * 128 + warp * 16 + j * 8 + gid) * p.k + b * 128 + t4 * 4;
-                float c[4] = {};
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_e4m3(c, a[kk], *reinterpret_cast<const uint32_t *>(w + kk * 32),
-                             *reinterpret_cast<const uint32_t *>(w + kk * 32 + 16));
-                acc[h][j][0] = __fmaf_rn(s0 * ws, c[0], acc[h][j][0]);
-                acc[h][j][1] = __fmaf_rn(s0 * ws, c[1], acc[h][j][1]);
-                acc[h][j][2] = __fmaf_rn(s1 * ws, c[2], acc[h][j][2]);
-                acc[h][j][3] = __fmaf_rn(s1 * ws, c[3], acc[h][j][3]);
-            }
-        }
+__device__ __forceinline__ Tile tile_at(const Product &p, const int *first, int ntn, int t) {
+    int lo = 0, hi = p.E;  // first[lo] * ntn <= t < first[hi] * ntn
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] * ntn <= t)
+            lo = mid;
+        else
+            hi = mid;
     }
-    if constexpr (!kSwiglu) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (r0 + gid + i * 8 < g.y)
-                    *reinterpret_cast<uint32_t *>(p.y + (row0 + gid + i * 8) * p.n + blockIdx.y * 128 +
-                                                  warp * 16 + j * 8 + t4 * 2) =
-                        pack_bf16x2(acc[0][j][i * 2], acc[0][j][i * 2 + 1]);
+    const int mt = first[lo + 1] - first[lo], u = t - first[lo] * ntn;
+    const int run = u / (kRun * ntn), width = min(kRun, mt - run * kRun);
+    const int v = u - run * kRun * ntn, ni = v / width, mi = run * kRun + v - ni * width;
+    const int2 g = group_rows(p, lo);
+    Tile tile;
+    tile.e = lo;
+    tile.rows = min(kTileRows, g.y - mi * kTileRows);
+    tile.row0 = (long long)(lo / (p.E / p.N)) * p.cap + g.x + mi * kTileRows;
+    const int nb = p.n >> 7;
+    if (kSwiglu) {
+        tile.blk0 = ni;
+        tile.blk1 = ni + (nb >> 1);
     } else {
-        float h[2][4];
-        uint32_t m[2] = {0, 0};
+        tile.blk0 = 2 * ni;
+        tile.blk1 = 2 * ni + 1 < nb ? 2 * ni + 1 : -1;
+    }
+    return tile;
+}
+
+// Writes 64 bytes of each of the warp's 32 rows (v: a lane's own row) to
+// dst + row * pitch, rows < rows only: through shared memory, so that four
+// lanes write a row's 64 bytes together.
+__device__ __forceinline__ void store_rows64(uint8_t *stage, const uint32_t (&v)[16], uint8_t *dst,
+                                             size_t pitch, int rows) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j)  // 16-byte chunk j of row `lane`, swizzled by row
+        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((j ^ (lane >> 1)) & 3) * 16) =
+            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[j][i] = silu_mul(acc[0][j][i], acc[kHalves - 1][j][i]);
-                m[i >> 1] = max(m[i >> 1], abs_bits(h[j][i]));
-            }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            m[i] = max(m[i], __shfl_xor_sync(kFull, m[i], 1));
-            m[i] = max(m[i], __shfl_xor_sync(kFull, m[i], 2));
-            if (t4 == 0) wmax[warp][gid + i * 8] = m[i];
-        }
-        __syncthreads();
-        const int I = p.n >> 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t am = 0;
-            for (int w = 0; w < 8; ++w) am = max(am, wmax[w][gid + i * 8]);
-            const float scale = block_scale(am);
-            if (r0 + gid + i * 8 >= g.y) continue;
-            const size_t row = row0 + gid + i * 8;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t c = scale == 0.0f ? 0u : code4(h[j][i * 2], h[j][i * 2 + 1], 0.0f, 0.0f, scale);
-                *reinterpret_cast<uint16_t *>(p.h_q + row * I + blockIdx.y * 128 + warp * 16 + j * 8 + t4 * 2) = (uint16_t)c;
-            }
-            if (warp == 0 && t4 == 0) p.h_s[row * (I >> 7) + blockIdx.y] = scale;
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), j = lane & 3;
+        if (r < rows)
+            *reinterpret_cast<uint4 *>(dst + (size_t)r * pitch + j * 16) =
+                *reinterpret_cast<const uint4 *>(stage + r * 64 + ((j ^ (r >> 1)) & 3) * 16);
     }
 }
 
-static cudaError_t launch_product(const Product &p, cudaStream_t st) {
-    if (p.cap == 0) return cudaSuccess;
-    const unsigned tiles = (unsigned)((p.cap + 15) / 16);
-    if (p.y)
-        return launch_kernel(k_product_simple<false>, dim3(tiles, p.n >> 7, p.E), dim3(256), 0, st, p);
-    return launch_kernel(k_product_simple<true>, dim3(tiles, p.n >> 8, p.E), dim3(256), 0, st, p);
+template <bool kSwiglu>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    k_product(const Product p, const __grid_constant__ CUtensorMap map_a,
+              const __grid_constant__ CUtensorMap map_w) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *stages = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *staging = stages + kStages * kStageBytes;
+    ProductShared &s = *reinterpret_cast<ProductShared *>(staging + kSumWarps * kStageOut);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.tfull[i], 1);
+            mbar_init(&s.tempty[i], kSumWarps);
+        }
+        mbar_init(&s.drain, 1);
+        s.stop = 0;
+        s.first[0] = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tc_alloc_all(&s.tmem);
+    if (warp == kTmaWarp && lane == 0) {
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_w);
+    }
+    __syncthreads();
+    // row tiles before each expert
+    int before = 0;
+    for (int e0 = 0; e0 < p.E; e0 += kProductThreads) {
+        const int e = e0 + tid;
+        const int mt = e < p.E ? (group_rows(p, e).y + kTileRows - 1) / kTileRows : 0;
+        const int upto = block_inclusive_scan(mt, s.wsum, &s.total);
+        if (e < p.E) s.first[e + 1] = before + upto;
+        before += s.total;
+        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    volatile int *stop = &s.stop;
+    const int nb = p.n >> 7, ntn = kSwiglu ? nb >> 1 : (nb + 1) >> 1;
+    const int tiles = before * ntn, Kb = p.k >> 7;
+
+    int issued = 0;  // k blocks whose loads are under way (TMA warp)
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
+                const int boxes = (tile.rows + kBoxRows - 1) / kBoxRows;
+                const uint32_t bytes =
+                    boxes * kBoxRows * kBlk + (tile.blk1 >= 0 ? 2 : 1) * kBlk * kBlk;
+                const int w0 = tile.e * p.n + tile.blk0 * kBlk, w1 = tile.e * p.n + tile.blk1 * kBlk;
+                for (int b = 0; b < Kb; ++b, ++issued) {
+                    const int st = issued % kStages;
+                    if (issued >= kStages &&
+                        !(ok = wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop)))
+                        break;
+                    uint8_t *a = stages + st * kStageBytes, *w = a + kTileRows * kBlk;
+                    mbar_arrive_expect_tx(&s.full[st], bytes);
+                    tma_tile(w, &map_w, b * kBlk, w0, &s.full[st]);
+                    if (tile.blk1 >= 0) tma_tile(w + kBlk * kBlk, &map_w, b * kBlk, w1, &s.full[st]);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_tile(a + i * kBoxRows * kBlk, &map_a, b * kBlk,
+                                 (int)tile.row0 + i * kBoxRows, &s.full[st]);
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            bool ok = true;
+            int it = 0;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
+                const uint32_t idesc =
+                    tile.blk1 >= 0 ? tc_e4m3_f32(kTileRows, 256) : tc_e4m3_f32(kTileRows, 128);
+                for (int b = 0; b < Kb; ++b, ++it) {
+                    const int st = it % kStages, ac = it & 1;
+                    if (it >= 2 && !(ok = wait_or_stop(&s.tempty[ac], (it / 2 - 1) & 1, stop))) break;
+                    if (!(ok = wait_or_stop(&s.full[st], (it / kStages) & 1, stop))) break;
+                    tc_fence_after();
+                    const uint64_t a = tc_operand(stages + st * kStageBytes);
+                    const uint64_t w = tc_operand(stages + st * kStageBytes + kTileRows * kBlk);
+#pragma unroll
+                    for (int kk = 0; kk < kBlk / 32; ++kk)  // 32 bytes along k: 2 address units
+                        tc_mma(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0);
+                    tc_commit(&s.empty[st]);
+                    tc_commit(&s.tfull[ac]);
+                }
+            }
+        }
+    } else {
+        const int quad = warp & 3, wg = warp >> 2;  // lanes 32 quad ..; columns 64 wg .. of each half
+        const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + wg * 64;
+        uint8_t *stage = staging + warp * kStageOut;
+        bool ok = true;
+        int it = 0;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
+            const int r = quad * 32 + lane;
+            const bool two = tile.blk1 >= 0;
+            // rows past the group's last read its scale; they are not stored
+            const float *as = p.a_s + (size_t)(tile.row0 + min(r, tile.rows - 1)) * Kb;
+            const float *ws0 = p.w_s + ((size_t)tile.e * nb + tile.blk0) * Kb;
+            const float *ws1 = p.w_s + ((size_t)tile.e * nb + (two ? tile.blk1 : tile.blk0)) * Kb;
+            uint64_t acc[2][32] = {};
+            // scales two blocks ahead
+            float sa = __ldg(as), s0 = __ldg(ws0), s1 = __ldg(ws1);
+            const int o1 = min(1, Kb - 1);
+            float sa1 = __ldg(as + o1), s01 = __ldg(ws0 + o1), s11 = __ldg(ws1 + o1);
+            for (int b = 0; b < Kb; ++b, ++it) {
+                const int ac = it & 1, o2 = min(b + 2, Kb - 1);
+                const float sa2 = __ldg(as + o2), s02 = __ldg(ws0 + o2), s12 = __ldg(ws1 + o2);
+                ok = __all_sync(kFull, wait_or_stop(&s.tfull[ac], (it / 2) & 1, stop));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && !two) break;
+                    const float f = sa * (h ? s1 : s0);
+                    const uint64_t ff = pack2(__float_as_uint(f), __float_as_uint(f));
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t v[32];
+                        tc_ld32(v, mine + ac * 256 + h * 128 + q * 32);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[h][q * 16 + i] =
+                                fma2(pack2(v[2 * i], v[2 * i + 1]), ff, acc[h][q * 16 + i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.tempty[ac]);
+                sa = sa1;
+                s0 = s01;
+                s1 = s11;
+                sa1 = sa2;
+                s01 = s02;
+                s11 = s12;
+            }
+            // either every sum warp has its sums or none goes on: the barriers
+            // below are met by all
+            ok = bar_named_all(1, kSumWarps * 32, ok);
+            if (!ok) break;
+            const int rows = tile.rows - quad * 32;  // of this warp
+            if constexpr (!kSwiglu) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && !two) break;
+                    const int blk = h ? tile.blk1 : tile.blk0;
+                    uint16_t *y = p.y + (size_t)(tile.row0 + quad * 32) * p.n + blk * 128 + wg * 64;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 f = unpack2(acc[h][q * 16 + i]);
+                            o[i] = pack_bf16x2(f.x, f.y);
+                        }
+                        store_rows64(stage, o, reinterpret_cast<uint8_t *>(y + q * 32),
+                                     (size_t)p.n * 2, rows);
+                    }
+                }
+            } else {
+                uint32_t am = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float2 g = unpack2(acc[0][i]), u = unpack2(acc[1][i]);
+                    const float h0 = silu_mul(g.x, u.x), h1 = silu_mul(g.y, u.y);
+                    am = max(am, max(abs_bits(h0), abs_bits(h1)));
+                    acc[0][i] = pack2(__float_as_uint(h0), __float_as_uint(h1));
+                }
+                // the other 64 columns of the row's block are the other group's
+                s.peak[wg][r] = am;
+                bar_named(1, kSumWarps * 32);
+                const float scale = block_scale(max(s.peak[0][r], s.peak[1][r]));
+                bar_named(1, kSumWarps * 32);
+                uint32_t o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 v0 = unpack2(acc[0][2 * i]), v1 = unpack2(acc[0][2 * i + 1]);
+                    o[i] = scale == 0.0f ? 0u : code4(v0.x, v0.y, v1.x, v1.y, scale);
+                }
+                const int I = p.n >> 1;
+                store_rows64(stage, o,
+                             p.h_q + (size_t)(tile.row0 + quad * 32) * I + tile.blk0 * 128 + wg * 64,
+                             (size_t)I, rows);
+                if (wg == 0 && lane < rows)
+                    p.h_s[(size_t)(tile.row0 + r) * (I >> 7) + tile.blk0] = scale;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (s.stop) {  // a kernel that gave up leaves no copy and no product in flight
+        if (warp == kTmaWarp && lane == 0)
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
+        if (warp == kMmaWarp && lane == 0) {
+            tc_commit(&s.drain);
+            mbar_wait(&s.drain, 0);
+        }
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kMmaWarp) tc_free_all(tmem);
+    if (tid == 0 && s.stop && p.status) flag(p.status, MOE_ST_TIMEOUT);
+}
+
+// ------------------------------------------------------------ host
+
+// cuTensorMapEncodeTiled through the runtime (the library links no driver).
+static cudaError_t tile_map(CUtensorMap *map, const void *base, int64_t rows, int k, int box_rows) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = nullptr;
+    static std::mutex mu;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!encode) {
+            void *fn = nullptr;
+            cudaDriverEntryPointQueryResult found;
+            const cudaError_t err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn,
+                                                                     12000, cudaEnableDefault, &found);
+            if (err != cudaSuccess) return err;
+            if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+            encode = reinterpret_cast<Encode>(fn);
+        }
+    }
+    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)k};
+    const cuuint32_t box[2] = {kBlk, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    const CUresult rc =
+        encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return rc == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const uint8_t *w_q,
+                                  cudaStream_t st) {
+    CUtensorMap map_a, map_w;
+    cudaError_t err = tile_map(&map_a, a_q, (int64_t)p.N * p.cap, p.k, kBoxRows);
+    if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kBlk);
+    if (err != cudaSuccess) return err;
+    const bool swiglu = p.h_q != nullptr;
+    const auto kern = swiglu ? k_product<true> : k_product<false>;
+    static LaunchMemo memo;
+    int done = 0;
+    err = memo.get(swiglu, &done, [&](int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kProductSmem);
+    });
+    if (err != cudaSuccess) return err;
+    // as many CTAs as there can be tiles: every expert's last tile may be part full
+    const int64_t nb = p.n >> 7, ntn = swiglu ? nb >> 1 : (nb + 1) >> 1;
+    const int64_t rows = (int64_t)p.N * p.cap;
+    const int64_t most = (rows / kTileRows + (rows < p.E ? rows : p.E)) * ntn;
+    const int grid = (int)(most < sm_count() ? most : sm_count());
+    return launch_kernel(kern, dim3(grid), dim3(kProductThreads), kProductSmem, st, p, map_a, map_w);
 }
 
 // The checks that both products share; fills *p.
 static int check_product(const moe_shape *sh, int64_t n, int k, const uint8_t *a_q,
                          const float *a_s, const int32_t *grp_off, const uint8_t *w_q,
-                         const float *w_s, Product *p) {
+                         const float *w_s, int32_t *status, Product *p) {
     moe_sizes z;
     int rc = moe_sizes_query(sh, &z);
     if (rc != MOE_OK) return rc;
     if ((rc = check_width(n)) != MOE_OK || (rc = check_width(k)) != MOE_OK) return rc;
     const int64_t rows = (int64_t)sh->N * z.cap;
     if (!ok_buffer(a_q, rows * k) || !ok_buffer(a_s, rows * (k / 128) * 4) ||
-        !ok_buffer(w_q, sh->E * n * k) || !ok_buffer(w_s, 4) || !ok_optional(grp_off))
+        !ok_buffer(w_q, sh->E * n * k) || !ok_buffer(w_s, 4) || !ok_optional(grp_off) ||
+        !ok_optional(status))
         return MOE_EINVAL;
     if (!grp_off && sh->E != sh->N) return MOE_EINVAL;
-    *p = Product{sh->N, sh->E, (int)z.cap, (int)n, k, a_q, a_s, grp_off, w_q, w_s, nullptr, nullptr, nullptr};
+    *p = Product{sh->N, sh->E, (int)z.cap, (int)n, k,       a_s,
+                 grp_off, w_s, nullptr,    nullptr, nullptr, status};
     return MOE_OK;
 }
 
@@ -150,27 +427,28 @@ static int check_product(const moe_shape *sh, int64_t n, int k, const uint8_t *a
 
 extern "C" int moe_expert_gemm(const moe_shape *sh, int n, int k, const uint8_t *a_q,
                                const float *a_s, const int32_t *grp_off, const uint8_t *w_q,
-                               const float *w_s, uint16_t *y, void *stream) {
+                               const float *w_s, uint16_t *y, int32_t *status, void *stream) {
     MOE_TRACE_CALL();
     moe::Product p;
-    const int rc = moe::check_product(sh, n, k, a_q, a_s, grp_off, w_q, w_s, &p);
+    const int rc = moe::check_product(sh, n, k, a_q, a_s, grp_off, w_q, w_s, status, &p);
     if (rc != MOE_OK) return rc;
     if (!moe::ok_buffer(y, (int64_t)p.N * p.cap * n * 2)) return MOE_EINVAL;
     if (p.cap == 0) return MOE_OK;
     p.y = y;
-    return moe::launch_product(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
-                                                                                       : MOE_ECUDA;
+    return moe::launch_product(p, a_q, w_q, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ECUDA;
 }
 
 extern "C" int moe_expert_gemm_swiglu(const moe_shape *sh, int inter, int k, const uint8_t *a_q,
                                       const float *a_s, const int32_t *grp_off,
                                       const uint8_t *w13_q, const float *w13_s, uint8_t *h_q,
-                                      float *h_s, void *stream) {
+                                      float *h_s, int32_t *status, void *stream) {
     MOE_TRACE_CALL();
     moe::Product p;
     int rc = moe::check_width(inter);
     if (rc != MOE_OK) return rc;
-    rc = moe::check_product(sh, 2 * (int64_t)inter, k, a_q, a_s, grp_off, w13_q, w13_s, &p);
+    rc = moe::check_product(sh, 2 * (int64_t)inter, k, a_q, a_s, grp_off, w13_q, w13_s, status, &p);
     if (rc != MOE_OK) return rc;
     const int64_t rows = (int64_t)p.N * p.cap;
     if (!moe::ok_buffer(h_q, rows * inter) || !moe::ok_buffer(h_s, rows * (inter / 128) * 4))
@@ -178,6 +456,7 @@ extern "C" int moe_expert_gemm_swiglu(const moe_shape *sh, int inter, int k, con
     if (p.cap == 0) return MOE_OK;
     p.h_q = h_q;
     p.h_s = h_s;
-    return moe::launch_product(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
-                                                                                       : MOE_ECUDA;
+    return moe::launch_product(p, a_q, w13_q, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ECUDA;
 }

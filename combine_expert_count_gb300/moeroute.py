@@ -111,8 +111,8 @@ def lib() -> ctypes.CDLL:
             h.moe_expert_standin_ll.argtypes = [sp, I] + [V] * 4 + [V]
             h.moe_combine_ll.argtypes = [sp] + [V] * 5 + [V]
             h.moe_rmsnorm.argtypes = [sp, ctypes.c_float] + [V] * 7 + [V]
-            h.moe_expert_gemm.argtypes = [sp, I, I] + [V] * 6 + [V]
-            h.moe_expert_gemm_swiglu.argtypes = [sp, I, I] + [V] * 7 + [V]
+            h.moe_expert_gemm.argtypes = [sp, I, I] + [V] * 7 + [V]
+            h.moe_expert_gemm_swiglu.argtypes = [sp, I, I] + [V] * 8 + [V]
             h.moe_layer_few.argtypes = [sp, I] + [V] * 11 + [V]
             h.moe_strerror.argtypes = [I]
             h.moe_strerror.restype = ctypes.c_char_p
@@ -449,7 +449,8 @@ def _product_sizes(sh: moe_shape, z: moe_sizes, n: int, k: int) -> tuple[int, in
     return rows * k, rows * (k // 128) * 4, sh.E * n * k, sh.E * (n // 128) * (k // 128) * 4
 
 
-def moe_expert_gemm(shape, n: int, k: int, a_q, a_s, grp_off, w_q, w_s, y, stream=None) -> None:
+def moe_expert_gemm(shape, n: int, k: int, a_q, a_s, grp_off, w_q, w_s, y, status=None,
+                    stream=None) -> None:
     """y = the grouped 8-bit rows (``a_q``, ``a_s``) times their experts' weights
     [E][n][k]; ``grp_off`` None where every rank has one expert (E == N)."""
     sh, z = _as_shape(shape), sizes_query(shape)
@@ -457,12 +458,12 @@ def moe_expert_gemm(shape, n: int, k: int, a_q, a_s, grp_off, w_q, w_s, y, strea
     _check(lib().moe_expert_gemm(
         ctypes.byref(sh), int(n), int(k), _p(a_q, ba, "a_q"), _p(a_s, bs, "a_s"),
         _maybe(grp_off, z.bytes_grp_off, "grp_off"), _p(w_q, bw, "w_q"), _p(w_s, bt, "w_s"),
-        _p(y, sh.N * z.cap * n * 2, "y"), _s(stream)),
+        _p(y, sh.N * z.cap * n * 2, "y"), _maybe(status, 4, "status"), _s(stream)),
         "moe_expert_gemm")
 
 
 def moe_expert_gemm_swiglu(shape, inter: int, k: int, a_q, a_s, grp_off, w13_q, w13_s, h_q, h_s,
-                           stream=None) -> None:
+                           status=None, stream=None) -> None:
     """The gate and up product [E][2*inter][k], silu(gate) * up and its block-128
     e4m3 coding (``h_q``, ``h_s``): the rows of the second product."""
     sh, z = _as_shape(shape), sizes_query(shape)
@@ -472,7 +473,7 @@ def moe_expert_gemm_swiglu(shape, inter: int, k: int, a_q, a_s, grp_off, w13_q, 
         ctypes.byref(sh), int(inter), int(k), _p(a_q, ba, "a_q"), _p(a_s, bs, "a_s"),
         _maybe(grp_off, z.bytes_grp_off, "grp_off"), _p(w13_q, bw, "w13_q"),
         _p(w13_s, bt, "w13_s"), _p(h_q, rows * inter, "h_q"),
-        _p(h_s, rows * (inter // 128) * 4, "h_s"), _s(stream)),
+        _p(h_s, rows * (inter // 128) * 4, "h_s"), _maybe(status, 4, "status"), _s(stream)),
         "moe_expert_gemm_swiglu")
 
 

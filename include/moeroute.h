@@ -469,13 +469,16 @@ int moe_rmsnorm(const moe_shape *shape, float eps, const uint16_t *x_bf16,
  * along k is summed in fp32 by the tensor cores and added, times its two
  * scales, to an fp32 sum over the blocks:
  *   p[i][c] = sum_b (a_s[i][b] * w_s[e][c/128][b]) * sum_{kk in b} a_q[i][kk] * w_q[e][c][kk]
- * Only N, E and cap of the shape matter here (the others are checked). */
+ * Only N, E and cap of the shape decide what is computed (T and R, with which
+ * the rows of an expert are estimated, only how).  status may be NULL; a
+ * kernel whose bounded waits run out sets MOE_ST_TIMEOUT there (it is not
+ * cleared) and leaves outputs unwritten. */
 
 /* y[i][c] = bf16_rn(p[i][c]).
  *   a_q u8 [N][cap][k], a_s float [N][cap][k/128], y bf16 [N][cap][n] */
 int moe_expert_gemm(const moe_shape *shape, int n, int k, const uint8_t *a_q, const float *a_s,
                     const int32_t *grp_off, const uint8_t *w_q, const float *w_s,
-                    uint16_t *y_bf16, void *stream);
+                    uint16_t *y_bf16, int32_t *status, void *stream);
 
 /* The gate and up product with the activation and the coding of its result:
  * the weights' first `inter` outputs are the gate g, the next `inter` the up u
@@ -485,7 +488,8 @@ int moe_expert_gemm(const moe_shape *shape, int n, int k, const uint8_t *a_q, co
  * the row operand of the second moe_expert_gemm. */
 int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8_t *a_q,
                            const float *a_s, const int32_t *grp_off, const uint8_t *w13_q,
-                           const float *w13_s, uint8_t *h_q, float *h_s, void *stream);
+                           const float *w13_s, uint8_t *h_q, float *h_s, int32_t *status,
+                           void *stream);
 
 /* ---------------------------------------------------------------- a few tokens
  * A whole expert layer for a few tokens, in two kernels and without a

@@ -45,8 +45,8 @@ def test_norm_refusals(lib):
 
 def test_product_refusals(lib):
     sh = ctypes.byref(m.moe_shape(2, 4, 8, 2, 256, 0))
-    for f, n in ((lib.moe_expert_gemm, 6), (lib.moe_expert_gemm_swiglu, 7)):
-        each_pointer(f, (sh, 256, 256), n)  # grp_off too: E != N
+    for f, n in ((lib.moe_expert_gemm, 7), (lib.moe_expert_gemm_swiglu, 8)):
+        each_pointer(f, (sh, 256, 256), n, optional=(n - 1,))  # grp_off has to be: E != N
         for width, code in ((0, m.MOE_EINVAL), (-128, m.MOE_EINVAL), (100, m.MOE_EINVAL),
                             (65536 + 128, m.MOE_ENOTSUP)):
             assert f(sh, width, 256, *[GOOD] * n, None) == code
@@ -60,7 +60,7 @@ def test_product_refusals(lib):
         args[2], args[3], args[4] = GOOD, GOOD, GOOD  # offsets and weights
         assert f(none, 256, 256, *args, None) == m.MOE_OK
     # the up weights make 2 * inter outputs: 65536 of them at most
-    assert lib.moe_expert_gemm_swiglu(sh, 32768 + 128, 256, *[GOOD] * 7, None) == m.MOE_ENOTSUP
+    assert lib.moe_expert_gemm_swiglu(sh, 32768 + 128, 256, *[GOOD] * 8, None) == m.MOE_ENOTSUP
 
 
 def test_few_refusals(lib):
