@@ -35,7 +35,11 @@ constexpr int kBoxRows = 32;                 // rows of one TMA load of a: a gro
 constexpr int kStages = 4;
 constexpr int kStageBytes = 3 * kTileRows * kBlk;  // a, first and second weight block
 constexpr int kSumWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kProductThreads = 32 * 10;
+// Twelve warps are launched with 168 registers a thread; the sum warps, which
+// hold 128 sums each thread, then take 232 and the others keep 40: the same
+// total, 384 * 168 = 256 * 232 + 128 * 40.
+constexpr int kProductThreads = 32 * 12;
+constexpr int kSumRegs = 232, kOtherRegs = 40;
 constexpr int kStageOut = 32 * 64;           // a sum warp's output staging: 32 rows of 64 bytes
 
 struct Product {
@@ -182,8 +186,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int tiles = before * ntn, Kb = p.k >> 7;
 
     int issued = 0;  // k blocks whose loads are under way (TMA warp)
-    if (warp == kTmaWarp) {
-        if (lane == 0) {
+    if (warp >= kSumWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kTmaWarp && lane == 0) {
             bool ok = true;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
@@ -206,8 +211,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
             }
         }
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) {
+        if (warp == kMmaWarp && lane == 0) {
             bool ok = true;
             int it = 0;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -230,6 +234,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         const int quad = warp & 3, wg = warp >> 2;  // lanes 32 quad ..; columns 64 wg .. of each half
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + wg * 64;
         uint8_t *stage = staging + warp * kStageOut;
