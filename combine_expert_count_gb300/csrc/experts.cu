@@ -322,11 +322,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 bar_named(1, kSumWarps * 32);
                 const float scale = block_scale(max(s.peak[0][r], s.peak[1][r]));
                 bar_named(1, kSumWarps * 32);
+                float inv = __frcp_rn(scale);
+                if (scale < kTinyScale) {
+                    const uint64_t up = pack2(__float_as_uint(kTinyUp), __float_as_uint(kTinyUp));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[0][i] = fma2(acc[0][i], up, 0);
+                    inv = scale == 0.0f ? 0.0f : __frcp_rn(scale * kTinyUp);
+                }
                 uint32_t o[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 v0 = unpack2(acc[0][2 * i]), v1 = unpack2(acc[0][2 * i + 1]);
-                    o[i] = scale == 0.0f ? 0u : code4(v0.x, v0.y, v1.x, v1.y, scale);
+                    o[i] = code4_by(v0.x, v0.y, v1.x, v1.y, inv);
                 }
                 const int I = p.n >> 1;
                 store_rows64(stage, o,
