@@ -16,14 +16,14 @@
 // power-of-two scales by themselves.  A thread holds one row, so its row's
 // scale is one number for all its columns and the gate, the up value and half
 // of the block maximum of an activation meet in one thread.
-#include <mutex>
-
 #include "bf16.cuh"
 #include "check.h"
 #include "coding.cuh"
 #include "launch.h"
 #include "mma8.cuh"
 #include "tc.cuh"
+#include "thin.h"
+#include "tilemap.h"
 #include "trace.h"
 
 namespace moe {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         s.first[0] = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tc_alloc_all(&s.tmem);
+    if (warp == kMmaWarp) tc_alloc<512>(&s.tmem);
     if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_w);
@@ -357,43 +357,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         __syncthreads();
     }
     tc_fence_after();
-    if (warp == kMmaWarp) tc_free_all(tmem);
+    if (warp == kMmaWarp) tc_free<512>(tmem);
     if (tid == 0 && s.stop && p.status) flag(p.status, MOE_ST_TIMEOUT);
 }
 
 // ------------------------------------------------------------ host
 
-// cuTensorMapEncodeTiled through the runtime (the library links no driver).
-static cudaError_t tile_map(CUtensorMap *map, const void *base, int64_t rows, int k, int box_rows) {
-    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static Encode encode = nullptr;
-    static std::mutex mu;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!encode) {
-            void *fn = nullptr;
-            cudaDriverEntryPointQueryResult found;
-            const cudaError_t err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn,
-                                                                     12000, cudaEnableDefault, &found);
-            if (err != cudaSuccess) return err;
-            if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-            encode = reinterpret_cast<Encode>(fn);
-        }
-    }
-    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)k};
-    const cuuint32_t box[2] = {kBlk, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    const CUresult rc =
-        encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
-               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return rc == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const uint8_t *w_q,
                                   cudaStream_t st) {
+    if ((int64_t)p.N * p.cap <= kThinRows)
+        return launch_thin_product(p.N, p.E, p.cap, p.n, p.k, a_q, p.a_s, p.grp_off, w_q, p.w_s, p.y,
+                                   p.h_q, p.h_s, p.status, st);
     CUtensorMap map_a, map_w;
     cudaError_t err = tile_map(&map_a, a_q, (int64_t)p.N * p.cap, p.k, kBoxRows);
     if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kBlk);

@@ -1,0 +1,705 @@
+// thin.cu -- products of the experts' weights with few rows: the two kernels of
+// moe_layer_few, and moe_expert_gemm / moe_expert_gemm_swiglu for a few rows in
+// all.  They are bound by reading the weights once.
+//
+// The weights are the 128-row operand of the tensor cores and the rows of x (or
+// h) the narrow one of 16 columns: a product costs what its real rows cost,
+// and a lane of tensor memory is an output feature.  A CTA owns one block of
+// 128 outputs of one expert (its gate and its up block; or one block over a run
+// of experts) and streams the weights' 16 KB tiles by TMA through a ring of
+// shared memory.  Four warps put the rows' 128-byte pieces beside them: coded
+// from x on the way, or copied from coded rows.  One thread issues the products
+// of a k block; four warps add it, times its scales, to fp32 sums.  Two CTAs
+// fit an SM, so one streams while the other starts or ends; together they keep
+// about 200 KB of weights on the way, and nothing but the ring's TMA copies has
+// to wait for HBM.  Weights are read with plain loads nowhere.
+#include <cooperative_groups.h>
+
+#include "bf16.cuh"
+#include "check.h"
+#include "coding.cuh"
+#include "launch.h"
+#include "mma8.cuh"
+#include "tc.cuh"
+#include "thin.h"
+#include "tilemap.h"
+#include "trace.h"
+
+namespace moe {
+
+namespace cg = cooperative_groups;
+
+// What a kernel multiplies and what becomes of it:
+//   kUp    rows coded from x, gate and up, activation coded to h     (few tokens)
+//   kDown  rows of h, an output block of every token over all experts (few tokens)
+//   kGemm, kSwiglu  grouped coded rows, as the entry points say
+enum class Thin { kUp, kDown, kGemm, kSwiglu };
+
+constexpr int kThinWarps = 10, kThinThreads = 32 * kThinWarps;
+constexpr int kRowWarp = 4, kRowWarps = 4, kThinTma = 8, kThinMma = 9;  // warps 0-3: sums
+constexpr int kTileBytes = 128 * 128;
+
+struct ThinArgs {
+    // few tokens
+    int ntok, E, R, H, inter;
+    bool by_expert;  // k_thin<kUp>: units are experts, not assignments
+    int passes;      // units of 16 rows that an expert may need
+    const uint16_t *x;
+    const int32_t *idx;
+    const float *topk_w;
+    uint8_t *h_q;
+    float *h_s;
+    uint16_t *out;
+    // grouped rows
+    int N, cap;
+    const int32_t *grp_off;
+    const uint8_t *a_q;
+    const float *a_s;
+    uint16_t *y;
+    // both
+    int n, k;  // outputs and inputs of the product
+    const float *w_s;
+    int32_t *status;
+};
+
+__host__ __device__ constexpr bool thin_pair(Thin m) { return m == Thin::kUp || m == Thin::kSwiglu; }
+
+// Columns of a product: rows of one expert that meet its weights at a time.  A
+// unit with more is several units, whose reads of the weights meet in L2.
+constexpr int kThinRowsAt = 16;
+
+// Ring stages for which two CTAs fit an SM.
+__host__ __device__ constexpr int thin_stages(Thin m) { return thin_pair(m) ? 3 : 5; }
+__host__ __device__ constexpr int thin_stage_bytes(Thin m) {
+    return (thin_pair(m) ? 2 : 1) * kTileBytes + kThinRowsAt * 128;
+}
+
+template <Thin kMode>
+struct alignas(16) ThinShared {
+    static constexpr int kStages = thin_stages(kMode);
+    float scale[kStages][kThinRowsAt];  // of the rows' pieces in each stage
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int stop, total, unit[3];
+    unsigned chosen[2];
+    int wsum[32];
+    uint32_t peak[4][kThinRowsAt];
+    int list[MOE_FEW_MAX_TOKENS];  // kUp: the expert's assignments, one a token
+};
+
+template <Thin kMode>
+constexpr size_t thin_fixed_smem() {
+    return 1024 + (size_t)thin_stages(kMode) * thin_stage_bytes(kMode) + sizeof(ThinShared<kMode>);
+}
+
+// kDown's lists behind that: the sums [ntok][128]; ids; the lists' assignments
+// and weights; for each expert its tokens as 64 bits and its first list place;
+// the entries (an expert and up to 16 of
+// its tokens): their experts and where their lists start.
+__host__ __device__ constexpr int thin_entries(int A, int E) { return E + A / kThinRowsAt + 1; }
+__host__ __device__ constexpr size_t thin_lists_smem(int ntok, int E, int R) {
+    return (size_t)ntok * 512 + (size_t)ntok * R * 12 +
+           ((size_t)3 * E + 2 * thin_entries(ntok * R, E)) * 4;
+}
+
+// Where byte 16 c of row r of a 128-byte-swizzled tile is.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+    return (uint32_t)r * 128 + (uint32_t)((c ^ (r & 7)) << 4);
+}
+
+template <Thin kMode>
+__global__ void __launch_bounds__(kThinThreads, 2)
+    k_thin(const ThinArgs p, const __grid_constant__ CUtensorMap map_w) {
+    constexpr bool kPair = thin_pair(kMode);
+    constexpr int kHalves = kPair ? 2 : 1;
+    constexpr int kStages = thin_stages(kMode), kBytes = thin_stage_bytes(kMode);
+    constexpr int NMAX = kThinRowsAt;
+    constexpr int kCols = 2 * kHalves * NMAX;  // two accumulators
+    using Shared = ThinShared<kMode>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    Shared &s = *reinterpret_cast<Shared *>(ring + kStages * kBytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int blk = blockIdx.x, Kb = p.k >> 7, nb = p.n >> 7;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+
+    // ---------------------------------------------------------------- the unit
+    // kDown: the whole list of experts; else one expert and its m rows
+    int e = 0, m = 0;
+    long long row0 = 0;
+    float *sums = reinterpret_cast<float *>(&s + 1);  // kDown, [ntok][128]
+    int *ids = reinterpret_cast<int *>(sums + (kMode == Thin::kDown ? p.ntok * 128 : 0));
+    const int A = p.ntok * p.R;
+    int *slot = ids + A;  // lists of assignments
+    float *weight = reinterpret_cast<float *>(slot + A);
+    unsigned *who = reinterpret_cast<unsigned *>(weight + A);  // [E][2]
+    int *place = reinterpret_cast<int *>(who + 2 * p.E), *start = place + p.E;
+    int *experts = start + thin_entries(A, p.E);
+    const int unit = kMode == Thin::kDown ? 0 : blockIdx.y / p.passes;
+    const int r0 = kMode == Thin::kDown ? 0 : (blockIdx.y - unit * p.passes) * NMAX;
+    int U = 0;  // kDown: entries
+    if constexpr (kMode == Thin::kUp) {
+        ids = reinterpret_cast<int *>(ring);  // the ring is not in use yet
+        int bad = 0;
+        for (int i = tid; i < A; i += kThinThreads) {
+            ids[i] = __ldg(p.idx + i);
+            bad |= (unsigned)ids[i] >= (unsigned)p.E;
+        }
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (blockIdx.x == 0 && blockIdx.y == 0 && part == 0) {
+            bad = __syncthreads_or(bad);
+            if (tid == 0) *p.status = bad ? MOE_ST_BAD_EXPERT : 0;
+        }
+        __syncthreads();
+        e = p.by_expert ? unit : ids[unit];
+        if ((unsigned)e >= (unsigned)p.E) return;
+        // thread t < 64: token t's first assignment to the expert
+        int k = -1;
+        if (tid < MOE_FEW_MAX_TOKENS) {
+            if (tid < p.ntok)
+                for (int i = p.R - 1; i >= 0; --i)
+                    if (ids[tid * p.R + i] == e) k = i;
+            const unsigned got = __ballot_sync(kFull, k >= 0);
+            if (lane == 0) s.chosen[warp] = got;
+        }
+        __syncthreads();
+        const unsigned lo = s.chosen[0], hi = s.chosen[1];
+        m = __popc(lo) + __popc(hi);
+        if (k >= 0) {
+            const unsigned below = (1u << lane) - 1u;
+            const int at = warp == 0 ? __popc(lo & below) : __popc(lo) + __popc(hi & below);
+            s.list[at] = tid * p.R + k;
+        }
+        __syncthreads();
+        if (m <= r0 || (!p.by_expert && s.list[0] != unit)) return;
+        m = min(m - r0, NMAX);
+    } else if constexpr (kMode == Thin::kDown) {
+        for (int i = tid; i < 2 * p.E; i += kThinThreads) who[i] = 0;
+        for (int i = tid; i < p.ntok * 128; i += kThinThreads) sums[i] = 0.0f;
+        for (int i = tid; i < A; i += kThinThreads) ids[i] = __ldg(p.idx + i);
+        __syncthreads();
+        for (int i = tid; i < A; i += kThinThreads) {
+            const int t = i / p.R;
+            if ((unsigned)ids[i] < (unsigned)p.E)
+                atomicOr(who + 2 * ids[i] + (t >> 5), 1u << (t & 31));
+        }
+        __syncthreads();
+        int L = 0;
+        for (int e0 = 0; e0 < p.E; e0 += kThinThreads) {
+            // entries and list places before each expert's, in one scan
+            const int x = e0 + tid;
+            const int c = x < p.E ? __popc(who[2 * x]) + __popc(who[2 * x + 1]) : 0;
+            const int both = ((c + NMAX - 1) / NMAX << 16) + c;
+            const int upto = block_inclusive_scan(both, s.wsum, &s.total) - both;
+            const int u = U + (upto >> 16), l = L + (upto & 0xffff);
+            for (int i = 0; i * NMAX < c; ++i) {
+                experts[u + i] = x;
+                start[u + i] = l + i * NMAX;
+            }
+            if (c > 0) place[x] = l;
+            U += s.total >> 16;
+            L += s.total & 0xffff;
+            __syncthreads();
+        }
+        if (tid == 0) start[U] = L;
+        // an expert's tokens in their order: the parts of a cluster make the same lists
+        for (int i = tid; i < A; i += kThinThreads) {
+            const int x = ids[i], t = i / p.R;
+            if ((unsigned)x >= (unsigned)p.E) continue;
+            bool again = false;  // an earlier slot of the token has this expert
+            for (int q = t * p.R; q < i; ++q) again |= ids[q] == x;
+            if (again) continue;
+            float w = 0.0f;
+            for (int q = i; q < t * p.R + p.R; ++q)
+                if (ids[q] == x) w += __ldg(p.topk_w + q);
+            const unsigned below = (1u << (t & 31)) - 1u;
+            const int at = place[x] + (t < 32 ? __popc(who[2 * x] & below)
+                                              : __popc(who[2 * x]) + __popc(who[2 * x + 1] & below));
+            slot[at] = i;
+            weight[at] = w;
+        }
+    } else {
+        // the unit-th expert that has rows
+        if (tid == 0) s.unit[0] = -1;
+        __syncthreads();
+        int seen = 0;
+        const int Er = p.E / p.N;
+        for (int e0 = 0; e0 < p.E; e0 += kThinThreads) {
+            const int x = e0 + tid;
+            int b = 0, c = 0;
+            if (x < p.E && p.grp_off) {
+                const int32_t *off = p.grp_off + (size_t)(x / Er) * (Er + 1) + x % Er;
+                b = min(max(__ldg(off), 0), p.cap);
+                c = min(max(__ldg(off + 1), b), p.cap) - b;
+            } else if (x < p.E) {
+                c = p.cap;
+            }
+            const int at = seen + block_inclusive_scan(c > 0, s.wsum, &s.total);
+            if (c > 0 && at == unit + 1) {
+                s.unit[0] = x;
+                s.unit[1] = b;
+                s.unit[2] = c;
+            }
+            seen += s.total;
+            __syncthreads();
+        }
+        e = s.unit[0];
+        if (e < 0 || s.unit[2] <= r0) return;
+        m = min(s.unit[2] - r0, NMAX);
+        row0 = (long long)(e / Er) * p.cap + s.unit[1] + r0;
+    }
+
+    // ---------------------------------------------------------------- set-up
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 1 + kRowWarps);
+            mbar_init(&s.empty[i], 1 + 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.tfull[i], 1);
+            mbar_init(&s.tempty[i], 4);
+        }
+        mbar_init(&s.drain, 1);
+        s.stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == kThinMma) tc_alloc<kCols>(&s.tmem);
+    fence_async_smem();  // kUp's ids lay where the ring is
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    volatile int *stop = &s.stop;
+
+    // The CTA's items, in order: k blocks b of (expert, rows).  kDown: a run of
+    // all experts' blocks; else a run of the one expert's.
+    const int all = kMode == Thin::kDown ? U * Kb : Kb;
+    const int i0 = (int)((long long)all * part / parts);
+    const int i1 = (int)((long long)all * (part + 1) / parts);
+    int issued = 0;  // items whose loads are under way (TMA warp)
+
+    float acc[kHalves][NMAX];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int j = 0; j < NMAX; ++j) acc[h][j] = 0.0f;
+
+    if (warp == kThinTma) {
+        if (lane == 0) {
+            for (int item = i0; item < i1; ++item, ++issued) {
+                const int u = kMode == Thin::kDown ? item / Kb : 0, b = item - u * Kb;
+                const int ex = kMode == Thin::kDown ? experts[u] : e, st = issued % kStages;
+                if (issued >= kStages &&
+                    !wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop))
+                    break;
+                uint8_t *w = ring + st * kBytes;
+                mbar_arrive_expect_tx(&s.full[st], kHalves * kTileBytes);
+                tma_tile(w, &map_w, b * 128, ex * p.n + blk * 128, &s.full[st]);
+                if (kPair)
+                    tma_tile(w + kTileBytes, &map_w, b * 128, ex * p.n + (p.n >> 1) + blk * 128,
+                             &s.full[st]);
+            }
+        }
+    } else if (warp == kThinMma) {
+        if (lane == 0) {
+            int it = 0;
+            for (int item = i0; item < i1; ++item, ++it) {
+                const int st = it % kStages, ac = it & 1;
+                const uint32_t idesc = tc_e4m3_f32(128, NMAX);
+                if (it >= 2 && !wait_or_stop(&s.tempty[ac], (it / 2 - 1) & 1, stop)) break;
+                if (!wait_or_stop(&s.full[st], (it / kStages) & 1, stop)) break;
+                tc_fence_after();
+                const uint8_t *w = ring + st * kBytes;
+                const uint64_t rows = tc_operand(w + kHalves * kTileBytes);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    const uint64_t wd = tc_operand(w + h * kTileBytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // 32 bytes along k: 2 address units
+                        tc_mma(tmem + (ac * kHalves + h) * NMAX, wd + kk * 2, rows + kk * 2, idesc,
+                               kk > 0);
+                }
+                tc_commit(&s.empty[st]);
+                tc_commit(&s.tfull[ac]);
+            }
+        }
+    } else if (warp >= kRowWarp) {
+        // A piece: kUp one row's block of x; else four rows' 128 bytes.  Pieces
+        // go round the four warps, each loading its next one while it works.
+        const int rw = warp - kRowWarp;
+        if constexpr (kMode == Thin::kDown)
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // h is k_thin<kUp>'s
+        constexpr int kPer = kMode == Thin::kUp ? 1 : 4;
+        const auto rows_of = [&](int item) {
+            return kMode == Thin::kDown ? start[item / Kb + 1] - start[item / Kb] : m;
+        };
+        int item = i0, first = 0;       // first piece of the item, counted over all items
+        int ni = i0, nfirst = 0, nq = rw;  // this warp's next piece to load: of item ni
+        uint4 v = make_uint4(0, 0, 0, 0);
+        float sc = 0.0f;
+        const auto load_next = [&]() {
+            while (ni < i1) {
+                const int pieces = (rows_of(ni) + kPer - 1) / kPer;
+                if (nq < nfirst + pieces) break;
+                nfirst += pieces;
+                ++ni;
+            }
+            if (ni >= i1) return;
+            const int q = nq - nfirst;
+            if constexpr (kMode == Thin::kUp) {
+                const int tok = s.list[r0 + q] / p.R;
+                const uint2 w = *reinterpret_cast<const uint2 *>(p.x + (size_t)tok * p.H + ni * 128 +
+                                                                 lane * 4);
+                v.x = w.x;
+                v.y = w.y;
+            } else {
+                const int u = kMode == Thin::kDown ? ni / Kb : 0, b = ni - u * Kb;
+                const int r = min(q * 4 + (lane >> 3), rows_of(ni) - 1);
+                const size_t row = kMode == Thin::kDown ? (size_t)slot[start[u] + r] : row0 + r;
+                const uint8_t *rq = kMode == Thin::kDown ? p.h_q : p.a_q;
+                const float *rs = kMode == Thin::kDown ? p.h_s : p.a_s;
+                v = *reinterpret_cast<const uint4 *>(rq + row * p.k + b * 128 + (lane & 7) * 16);
+                sc = rs[row * Kb + b];
+            }
+            nq += kRowWarps;
+        };
+        load_next();
+        int mine = rw;  // this warp's next piece to put in place
+        for (int it = 0; item < i1; ++item, ++it) {
+            const int st = it % kStages;
+            const bool ok = it < kStages ||
+                            __all_sync(kFull, wait_or_stop(&s.empty[st], (it / kStages - 1) & 1, stop));
+            if (!ok) break;
+            const int mm = rows_of(item), pieces = (mm + kPer - 1) / kPer;
+            uint8_t *rows = ring + st * kBytes + kHalves * kTileBytes;
+            for (; mine < first + pieces; mine += kRowWarps) {
+                const int q = mine - first;
+                const uint4 cur = v;
+                const float cs = sc;
+                load_next();
+                if constexpr (kMode == Thin::kUp) {
+                    const float f0 = bf16_lo(cur.x), f1 = bf16_hi(cur.x), f2 = bf16_lo(cur.y),
+                                f3 = bf16_hi(cur.y);
+                    const uint32_t am = __reduce_max_sync(
+                        kFull, max(max(abs_bits(f0), abs_bits(f1)), max(abs_bits(f2), abs_bits(f3))));
+                    const float scale = block_scale(am);
+                    *reinterpret_cast<uint32_t *>(rows + swizzled(q, lane >> 2) + (lane & 3) * 4) =
+                        scale == 0.0f ? 0u : code4(f0, f1, f2, f3, scale);
+                    if (lane == 0) s.scale[st][q] = scale;
+                } else {
+                    const int r = q * 4 + (lane >> 3);
+                    if (r < mm) {
+                        *reinterpret_cast<uint4 *>(rows + swizzled(r, lane & 7)) = cur;
+                        if ((lane & 7) == 0) s.scale[st][r] = cs;
+                    }
+                }
+            }
+            first += pieces;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.full[st]);
+        }
+    } else {
+        // sums: lane = output 32 warp + lane of the block, column = row of x or h
+        const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
+        int it = 0;
+        for (int item = i0; item < i1;) {
+            const int u = kMode == Thin::kDown ? item / Kb : 0, b0 = item - u * Kb;
+            const int end = min(i1, (u + 1) * Kb), ex = kMode == Thin::kDown ? experts[u] : e;
+            if (kMode == Thin::kDown) m = start[u + 1] - start[u];
+            const float *ws = p.w_s + ((size_t)ex * nb + blk) * Kb + b0;
+            const float *wu = ws + (size_t)(kPair ? nb >> 1 : 0) * Kb;
+            const int nblk = end - item;
+            // weight scales two blocks ahead
+            float g0 = __ldg(ws), g1 = __ldg(ws + min(1, nblk - 1));
+            float u0 = __ldg(wu), u1 = __ldg(wu + min(1, nblk - 1));
+            bool ok = true;
+            for (int b = 0; b < nblk; ++b, ++it) {
+                const int st = it % kStages, ac = it & 1;
+                const float g2 = __ldg(ws + min(b + 2, nblk - 1));
+                const float u2 = kPair ? __ldg(wu + min(b + 2, nblk - 1)) : 0.0f;
+                // the rows' scales were stored before their arrivals on full
+                ok = wait_or_stop(&s.tfull[ac], (it / 2) & 1, stop) &&
+                     wait_or_stop(&s.full[st], (it / kStages) & 1, stop);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t d[kHalves][NMAX];
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+                    tc_ld16(d[h], mine + (ac * kHalves + h) * NMAX);
+                float sc[NMAX];
+#pragma unroll
+                for (int j = 0; j < NMAX / 4; ++j) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&s.scale[st][j * 4]);
+                    sc[4 * j] = f.x;
+                    sc[4 * j + 1] = f.y;
+                    sc[4 * j + 2] = f.z;
+                    sc[4 * j + 3] = f.w;
+                }
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < NMAX; ++j) {
+                    acc[0][j] = __fmaf_rn(sc[j] * g0, __uint_as_float(d[0][j]), acc[0][j]);
+                    if (kPair)
+                        acc[kHalves - 1][j] =
+                            __fmaf_rn(sc[j] * u0, __uint_as_float(d[kHalves - 1][j]),
+                                      acc[kHalves - 1][j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&s.tempty[ac]);
+                    mbar_arrive(&s.empty[st]);
+                }
+                g0 = g1;
+                g1 = g2;
+                u0 = u1;
+                u1 = u2;
+            }
+            if (!ok) break;
+            item = end;
+            if constexpr (kMode == Thin::kDown) {
+                // a thread owns its output of every token
+#pragma unroll
+                for (int j = 0; j < NMAX; ++j) {
+                    if (j < m) {
+                        const int at = start[u] + j;
+                        float *t = sums + (slot[at] / p.R) * 128 + tid;
+                        *t = __fmaf_rn(weight[at], acc[0][j], *t);
+                    }
+                    acc[0][j] = 0.0f;
+                }
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- the end
+    tc_fence_before();
+    __syncthreads();
+    if (s.stop) {  // a kernel that gave up leaves no copy and no product in flight
+        if (warp == kThinTma && lane == 0)
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
+        if (warp == kThinMma && lane == 0) {
+            tc_commit(&s.drain);
+            mbar_wait(&s.drain, 0);
+        }
+        if (tid == 0 && p.status) flag(p.status, MOE_ST_TIMEOUT);
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kThinMma) tc_free<kCols>(tmem);
+
+    if constexpr (kMode == Thin::kDown) {
+        // the parts of the experts' run, added in the cluster's order
+        if (parts > 1) cluster.sync();
+        for (int i = part * kThinThreads + tid; i < p.ntok * 64; i += parts * kThinThreads) {
+            float2 v = make_float2(0.0f, 0.0f);
+            for (int q = 0; q < parts; ++q) {
+                const float2 o = *reinterpret_cast<const float2 *>(cluster.map_shared_rank(sums + i * 2, q));
+                v.x += o.x;
+                v.y += o.y;
+            }
+            *reinterpret_cast<uint32_t *>(p.out + (size_t)(i >> 6) * p.H + blk * 128 + (i & 63) * 2) =
+                pack_bf16x2(v.x, v.y);
+        }
+        if (parts > 1) cluster.sync();  // no part goes while it is read
+        return;
+    }
+    // parts of k: the others leave their sums in their rings, the first adds them
+    float *left = reinterpret_cast<float *>(ring);  // [half][column][128]
+    if (parts > 1) {
+        if (warp < 4 && part > 0) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int j = 0; j < NMAX; ++j)
+                    if (j < m) left[(h * NMAX + j) * 128 + tid] = acc[h][j];
+        }
+        cluster.sync();
+        if (warp < 4 && part == 0) {
+            for (int q = 1; q < parts; ++q) {
+                const float *o = cluster.map_shared_rank(left, q);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                    for (int j = 0; j < NMAX; ++j)
+                        if (j < m) acc[h][j] += o[(h * NMAX + j) * 128 + tid];
+            }
+        }
+        cluster.sync();  // no part goes while it is read
+    }
+    if (part > 0 || warp >= 4) return;
+    const auto row_of = [&](int j) {
+        return kMode == Thin::kUp ? (size_t)s.list[r0 + j] : (size_t)(row0 + j);
+    };
+    if constexpr (!kPair) {
+#pragma unroll
+        for (int j = 0; j < NMAX; ++j)
+            if (j < m) p.y[row_of(j) * p.n + blk * 128 + tid] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(acc[0][j]));
+    } else {
+        const int I = p.n >> 1;
+#pragma unroll
+        for (int j = 0; j < NMAX; ++j) {
+            if (j >= m) continue;
+            acc[0][j] = silu_mul(acc[0][j], acc[kHalves - 1][j]);
+            const uint32_t am = __reduce_max_sync(kFull, abs_bits(acc[0][j]));
+            if (lane == 0) s.peak[warp][j] = am;
+        }
+        bar_named(1, 128);
+#pragma unroll
+        for (int j = 0; j < NMAX; ++j) {
+            if (j >= m) continue;
+            const float scale = block_scale(
+                max(max(s.peak[0][j], s.peak[1][j]), max(s.peak[2][j], s.peak[3][j])));
+            const uint32_t code =
+                scale == 0.0f ? 0u : code4(acc[0][j], 0.0f, 0.0f, 0.0f, scale);
+            p.h_q[row_of(j) * I + blk * 128 + tid] = (uint8_t)code;
+            if (tid == 0) p.h_s[row_of(j) * (I >> 7) + blk] = scale;
+        }
+    }
+}
+
+// ------------------------------------------------------------ host
+
+template <Thin kMode>
+static cudaError_t launch_thin(const ThinArgs &p, const CUtensorMap &map, dim3 grid, int parts,
+                               size_t more_smem, bool after, cudaStream_t st) {
+    const auto kern = k_thin<kMode>;
+    constexpr size_t kFixed = thin_fixed_smem<kMode>();
+    constexpr size_t kMost =
+        kFixed + (kMode == Thin::kDown
+                      ? thin_lists_smem(MOE_FEW_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOPK)
+                      : 0);
+    static_assert(kMost <= 232448, "a CTA's shared memory");
+    static LaunchMemo memo;
+    int done = 0;
+    cudaError_t err = memo.get(0, &done, [&](int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+    });
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = (unsigned)parts;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    grid.z = (unsigned)parts;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThinThreads);
+    cfg.dynamicSmemBytes = kFixed + more_smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, map);
+}
+
+// CTAs that share a unit's k blocks: as many as the SMs hold at two each, eight
+// at most, each with two blocks at least.
+static int thin_parts(int64_t units, int64_t blocks) {
+    int parts = 1;
+    while (parts < 8 && units * parts * 2 <= 2 * (int64_t)sm_count() && blocks >= 4 * parts)
+        parts *= 2;
+    return parts;
+}
+
+cudaError_t launch_thin_product(int N, int E, int cap, int n, int k, const uint8_t *a_q,
+                                const float *a_s, const int32_t *grp_off, const uint8_t *w_q,
+                                const float *w_s, uint16_t *y, uint8_t *h_q, float *h_s,
+                                int32_t *status, cudaStream_t st) {
+    CUtensorMap map;
+    cudaError_t err = tile_map(&map, w_q, (int64_t)E * n, k, 128);
+    if (err != cudaSuccess) return err;
+    ThinArgs p = {};
+    p.E = E;
+    p.N = N;
+    p.cap = cap;
+    p.grp_off = grp_off;
+    p.a_q = a_q;
+    p.a_s = a_s;
+    p.w_s = w_s;
+    p.y = y;
+    p.h_q = h_q;
+    p.h_s = h_s;
+    p.n = n;
+    p.k = k;
+    p.status = status;
+    const int rows = N * cap, units = E < rows ? E : rows;
+    p.passes = (rows + kThinRowsAt - 1) / kThinRowsAt;
+    const dim3 grid((unsigned)(h_q ? n >> 8 : n >> 7), (unsigned)(units * p.passes));
+    const int parts = thin_parts((int64_t)grid.x * units, k >> 7);
+    if (h_q) return launch_thin<Thin::kSwiglu>(p, map, grid, parts, 0, false, st);
+    return launch_thin<Thin::kGemm>(p, map, grid, parts, 0, false, st);
+}
+
+static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13_s,
+                              const uint8_t *w2_q, const float *w2_s, cudaStream_t st) {
+    if (p.ntok == 0) return cudaMemsetAsync(p.status, 0, 4, st);
+    CUtensorMap up, down;
+    cudaError_t err = tile_map(&up, w13_q, (int64_t)p.E * 2 * p.inter, p.H, 128);
+    if (err == cudaSuccess) err = tile_map(&down, w2_q, (int64_t)p.E * p.H, p.inter, 128);
+    if (err != cudaSuccess) return err;
+    const int A = p.ntok * p.R;
+    p.by_expert = A > p.E;
+    p.passes = (p.ntok + kThinRowsAt - 1) / kThinRowsAt;
+    const int units = p.by_expert ? p.E : A;
+    const dim3 gup((unsigned)(p.inter >> 7), (unsigned)(units * p.passes));
+    p.n = 2 * p.inter;
+    p.k = p.H;
+    p.w_s = w13_s;
+    err = launch_thin<Thin::kUp>(p, up, gup, thin_parts((int64_t)gup.x * units, p.H >> 7), 0, false,
+                                 st);
+    if (err != cudaSuccess) return err;
+    p.n = p.H;
+    p.k = p.inter;
+    p.w_s = w2_s;
+    const dim3 gdown((unsigned)(p.H >> 7));
+    return launch_thin<Thin::kDown>(p, down, gdown,
+                                    thin_parts(gdown.x, (int64_t)units * (p.inter >> 7)),
+                                    thin_lists_smem(p.ntok, p.E, p.R), true, st);
+}
+
+}  // namespace moe
+
+extern "C" int moe_layer_few(const moe_shape *sh, int inter, const uint16_t *x,
+                             const int32_t *topk_idx, const float *topk_w, const uint8_t *w13_q,
+                             const float *w13_s, const uint8_t *w2_q, const float *w2_s,
+                             uint8_t *h_q, float *h_s, uint16_t *out, int32_t *status,
+                             void *stream) {
+    MOE_TRACE_CALL();
+    moe_sizes z;
+    int rc = moe_sizes_query(sh, &z);
+    if (rc != MOE_OK || (rc = moe::check_width(inter)) != MOE_OK) return rc;
+    const int64_t ntok = (int64_t)sh->N * sh->T, A = ntok * sh->R;
+    if (ntok > MOE_FEW_MAX_TOKENS) return MOE_ENOTSUP;
+    if (!moe::ok_buffer(x, z.bytes_x) || !moe::ok_buffer(topk_idx, z.bytes_topk_idx) ||
+        !moe::ok_buffer(topk_w, z.bytes_topk_idx) || !moe::ok_buffer(w13_q, 1) ||
+        !moe::ok_buffer(w13_s, 4) || !moe::ok_buffer(w2_q, 1) || !moe::ok_buffer(w2_s, 4) ||
+        !moe::ok_buffer(h_q, A * inter) || !moe::ok_buffer(h_s, A * (inter / 128) * 4) ||
+        !moe::ok_buffer(out, z.bytes_x) || !moe::ok_buffer(status, 4))
+        return MOE_EINVAL;
+    moe::ThinArgs p = {};
+    p.ntok = (int)ntok;
+    p.E = sh->E;
+    p.R = sh->R;
+    p.H = sh->H;
+    p.inter = inter;
+    p.x = x;
+    p.idx = topk_idx;
+    p.topk_w = topk_w;
+    p.h_q = h_q;
+    p.h_s = h_s;
+    p.out = out;
+    p.status = status;
+    return moe::launch_few(p, w13_q, w13_s, w2_q, w2_s, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ECUDA;
+}
