@@ -425,8 +425,23 @@ def moe_combine_ll(shape, y_ll, topk_w, ll_row, out, status, stream=None) -> Non
         "moe_combine_ll")
 
 
+def _ptr(t, nbytes: int, name: str):
+    """_p's address as a number, with its checks in fewer steps: small calls
+    are bound by the host."""
+    if t is not None and t.is_cuda and t.is_contiguous() and t.nbytes >= nbytes:
+        return t.data_ptr()
+    p = _p(t, nbytes, name)
+    return None if p is None else p.value
+
+
 def _maybe(t, nbytes: int, name: str):
-    return None if t is None else _p(t, nbytes, name)
+    return None if t is None else _ptr(t, nbytes, name)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def moe_rmsnorm(shape, x, gamma, eps: float, y=None, q=None, s=None, res=None, res_out=None,
@@ -434,63 +449,61 @@ def moe_rmsnorm(shape, x, gamma, eps: float, y=None, q=None, s=None, res=None, r
     """RMS norm of the N*T rows of ``x`` (plus ``res``) times ``gamma``: the
     bf16 rows ``y``, their block-128 e4m3 coding (``q``, ``s``) and the sum
     ``res_out``, each where a buffer is given."""
-    sh, z = _as_shape(shape), sizes_query(shape)
-    nq = z.bytes_x // 2
-    _check(lib().moe_rmsnorm(
-        ctypes.byref(sh), float(eps), _p(x, z.bytes_x, "x"), _maybe(res, z.bytes_x, "res"),
-        _p(gamma, 2 * sh.H, "gamma"), _maybe(res_out, z.bytes_x, "res_out"),
-        _maybe(y, z.bytes_x, "y"), _maybe(q, nq, "q"), _maybe(s, nq // 32, "s"), _s(stream)),
-        "moe_rmsnorm")
-
-
-def _product_sizes(sh: moe_shape, z: moe_sizes, n: int, k: int) -> tuple[int, int, int, int]:
-    """Bytes of a_q, a_s, w_q and w_s of a product with n outputs of k inputs."""
-    rows = sh.N * z.cap
-    return rows * k, rows * (k // 128) * 4, sh.E * n * k, sh.E * (n // 128) * (k // 128) * 4
+    sh = _as_shape(shape)
+    nx = sizes_query(sh).bytes_x
+    rc = lib().moe_rmsnorm(
+        ctypes.byref(sh), eps, _ptr(x, nx, "x"), _maybe(res, nx, "res"),
+        _ptr(gamma, 2 * sh.H, "gamma"), _maybe(res_out, nx, "res_out"), _maybe(y, nx, "y"),
+        _maybe(q, nx // 2, "q"), _maybe(s, nx // 64, "s"), _raw_stream(stream))
+    _check(rc, "moe_rmsnorm")
 
 
 def moe_expert_gemm(shape, n: int, k: int, a_q, a_s, grp_off, w_q, w_s, y, status=None,
                     stream=None) -> None:
     """y = the grouped 8-bit rows (``a_q``, ``a_s``) times their experts' weights
     [E][n][k]; ``grp_off`` None where every rank has one expert (E == N)."""
-    sh, z = _as_shape(shape), sizes_query(shape)
-    ba, bs, bw, bt = _product_sizes(sh, z, n, k)
-    _check(lib().moe_expert_gemm(
-        ctypes.byref(sh), int(n), int(k), _p(a_q, ba, "a_q"), _p(a_s, bs, "a_s"),
-        _maybe(grp_off, z.bytes_grp_off, "grp_off"), _p(w_q, bw, "w_q"), _p(w_s, bt, "w_s"),
-        _p(y, sh.N * z.cap * n * 2, "y"), _maybe(status, 4, "status"), _s(stream)),
-        "moe_expert_gemm")
+    sh = _as_shape(shape)
+    z = sizes_query(sh)
+    rows, E = sh.N * z.cap, sh.E
+    rc = lib().moe_expert_gemm(
+        ctypes.byref(sh), n, k, _ptr(a_q, rows * k, "a_q"), _ptr(a_s, rows * k // 32, "a_s"),
+        _maybe(grp_off, z.bytes_grp_off, "grp_off"), _ptr(w_q, E * n * k, "w_q"),
+        _ptr(w_s, E * (n // 128) * (k // 128) * 4, "w_s"), _ptr(y, rows * n * 2, "y"),
+        _maybe(status, 4, "status"), _raw_stream(stream))
+    _check(rc, "moe_expert_gemm")
 
 
 def moe_expert_gemm_swiglu(shape, inter: int, k: int, a_q, a_s, grp_off, w13_q, w13_s, h_q, h_s,
                            status=None, stream=None) -> None:
     """The gate and up product [E][2*inter][k], silu(gate) * up and its block-128
     e4m3 coding (``h_q``, ``h_s``): the rows of the second product."""
-    sh, z = _as_shape(shape), sizes_query(shape)
-    ba, bs, bw, bt = _product_sizes(sh, z, 2 * inter, k)
-    rows = sh.N * z.cap
-    _check(lib().moe_expert_gemm_swiglu(
-        ctypes.byref(sh), int(inter), int(k), _p(a_q, ba, "a_q"), _p(a_s, bs, "a_s"),
-        _maybe(grp_off, z.bytes_grp_off, "grp_off"), _p(w13_q, bw, "w13_q"),
-        _p(w13_s, bt, "w13_s"), _p(h_q, rows * inter, "h_q"),
-        _p(h_s, rows * (inter // 128) * 4, "h_s"), _maybe(status, 4, "status"), _s(stream)),
-        "moe_expert_gemm_swiglu")
+    sh = _as_shape(shape)
+    z = sizes_query(sh)
+    rows, E = sh.N * z.cap, sh.E
+    rc = lib().moe_expert_gemm_swiglu(
+        ctypes.byref(sh), inter, k, _ptr(a_q, rows * k, "a_q"), _ptr(a_s, rows * k // 32, "a_s"),
+        _maybe(grp_off, z.bytes_grp_off, "grp_off"), _ptr(w13_q, 2 * E * inter * k, "w13_q"),
+        _ptr(w13_s, 2 * E * (inter // 128) * (k // 128) * 4, "w13_s"),
+        _ptr(h_q, rows * inter, "h_q"), _ptr(h_s, rows * inter // 32, "h_s"),
+        _maybe(status, 4, "status"), _raw_stream(stream))
+    _check(rc, "moe_expert_gemm_swiglu")
 
 
 def moe_layer_few(shape, inter: int, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, h_q, h_s, out,
                   status, stream=None) -> None:
     """A whole expert layer for at most MOE_FEW_MAX_TOKENS tokens; ``h_q``
     [N][T][R][inter] and ``h_s`` [N][T][R][inter/128] are scratch."""
-    sh, z = _as_shape(shape), sizes_query(shape)
-    A, E, H = sh.N * sh.T * sh.R, sh.E, sh.H
-    nw, ns = E * inter * H, E * (inter // 128) * (H // 128) * 4
-    _check(lib().moe_layer_few(
-        ctypes.byref(sh), int(inter), _p(x, z.bytes_x, "x"),
-        _p(topk_idx, z.bytes_topk_idx, "topk_idx"), _p(topk_w, z.bytes_topk_idx, "topk_w"),
-        _p(w13_q, 2 * nw, "w13_q"), _p(w13_s, 2 * ns, "w13_s"), _p(w2_q, nw, "w2_q"),
-        _p(w2_s, ns, "w2_s"), _p(h_q, A * inter, "h_q"), _p(h_s, A * (inter // 128) * 4, "h_s"),
-        _p(out, z.bytes_x, "out"), _p(status, 4, "status"), _s(stream)),
-        "moe_layer_few")
+    sh = _as_shape(shape)
+    z = sizes_query(sh)
+    nx, ni, H = z.bytes_x, z.bytes_topk_idx, sh.H
+    nh, nw, ns = ni // 4 * inter, sh.E * inter * H, sh.E * (inter // 128) * (H // 128) * 4
+    rc = lib().moe_layer_few(
+        ctypes.byref(sh), inter, _ptr(x, nx, "x"), _ptr(topk_idx, ni, "topk_idx"),
+        _ptr(topk_w, ni, "topk_w"), _ptr(w13_q, 2 * nw, "w13_q"), _ptr(w13_s, 2 * ns, "w13_s"),
+        _ptr(w2_q, nw, "w2_q"), _ptr(w2_s, ns, "w2_s"), _ptr(h_q, nh, "h_q"),
+        _ptr(h_s, nh // 32, "h_s"), _ptr(out, nx, "out"), _ptr(status, 4, "status"),
+        _raw_stream(stream))
+    _check(rc, "moe_layer_few")
 
 
 class MoeLLBuffers:
