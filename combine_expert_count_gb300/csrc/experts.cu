@@ -16,6 +16,8 @@
 // power-of-two scales by themselves.  A thread holds one row, so its row's
 // scale is one number for all its columns and the gate, the up value and half
 // of the block maximum of an activation meet in one thread.
+#include <cooperative_groups.h>
+
 #include "bf16.cuh"
 #include "check.h"
 #include "coding.cuh"
@@ -28,22 +30,35 @@
 
 namespace moe {
 
+namespace cg = cooperative_groups;
+
 constexpr int kTileRows = 128;               // rows of a tile: the lanes of tensor memory
 constexpr int kBlk = 128;                    // k block, scale block, half of a tile's columns
 constexpr int kBoxRows = 32;                 // rows of one TMA load of a: a group's last tile
                                              // loads no more than it has, rounded up to 32
-constexpr int kStages = 4;
-constexpr int kStageBytes = 3 * kTileRows * kBlk;  // a, first and second weight block
-constexpr int kSumWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kWBoxRows = 64;                // rows of one TMA load of weights
+// A stage: the CTA's rows of a and its weight rows, both blocks of 128 where it
+// works alone, half of them in a pair.
+__host__ __device__ constexpr int stage_count(bool pair) { return pair ? 6 : 4; }
+__host__ __device__ constexpr int stage_bytes(bool pair) { return (pair ? 2 : 3) * kTileRows * kBlk; }
+constexpr int kStageRing = 4 * stage_bytes(false);
+static_assert(kStageRing == 6 * stage_bytes(true), "one size of shared memory");
+constexpr int kSumWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleWarps = 2;
 // Twelve warps are launched with 168 registers a thread; the sum warps, which
 // hold 128 sums each thread, then take 232 and the others keep 40: the same
 // total, 384 * 168 = 256 * 232 + 128 * 40.
 constexpr int kProductThreads = 32 * 12;
-constexpr int kSumRegs = 232, kOtherRegs = 40;
+constexpr int kSumRegs = 200, kOtherRegs = 96;
 constexpr int kStageOut = 32 * 64;           // a sum warp's output staging: 32 rows of 64 bytes
+
+// Two warps bring the scales of runs of four k blocks to shared memory, two runs
+// ahead at most, by 4-byte asynchronous copies (a row's scales lie one after
+// another, whatever their alignment).
+constexpr int kScaleRun = 4;
 
 struct Product {
     int N, E, cap, n, k;
+    double rows;  // of an expert, estimated
     const float *a_s;
     const int32_t *grp_off;
     const float *w_s;
@@ -63,14 +78,15 @@ __device__ __forceinline__ int2 group_rows(const Product &p, int e) {
 }
 
 struct Tile {
-    int e, rows;      // expert; rows of the tile, 1 .. 128
+    int e, rows;      // expert; rows of the tile, 1 .. 128 (256 in a pair)
     long long row0;   // first row, over all ranks
     int blk0, blk1;   // column blocks of 128; blk1 < 0: there is none
 };
 
 // Shared memory behind the stages and the output staging.
-struct ProductShared {
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+struct alignas(16) ProductShared {
+    float rscale[2][kScaleRun][kTileRows], wscale[2][kScaleRun][2];
+    uint64_t full[6], empty[6], tfull[2], tempty[2], sfull[2], sempty[2], drain;
     uint32_t tmem;
     int stop, total;
     int wsum[32];
@@ -79,14 +95,14 @@ struct ProductShared {
 };
 
 constexpr size_t kProductSmem =
-    1024 + (size_t)kStages * kStageBytes + (size_t)kSumWarps * kStageOut + sizeof(ProductShared);
+    1024 + (size_t)kStageRing + (size_t)kSumWarps * kStageOut + sizeof(ProductShared);
 static_assert(kProductSmem <= 232448, "a CTA's shared memory");
 
 // Tiles run row tile first within runs of kRun row tiles, so that the CTAs at
 // work at one time share weights and rows in L2.
 constexpr int kRun = 16;
 
-template <bool kSwiglu>
+template <bool kSwiglu, int kRows>
 __device__ __forceinline__ Tile tile_at(const Product &p, const int *first, int ntn, int t) {
     int lo = 0, hi = p.E;  // first[lo] * ntn <= t < first[hi] * ntn
     while (hi - lo > 1) {
@@ -102,8 +118,8 @@ __device__ __forceinline__ Tile tile_at(const Product &p, const int *first, int 
     const int2 g = group_rows(p, lo);
     Tile tile;
     tile.e = lo;
-    tile.rows = min(kTileRows, g.y - mi * kTileRows);
-    tile.row0 = (long long)(lo / (p.E / p.N)) * p.cap + g.x + mi * kTileRows;
+    tile.rows = min(kRows, g.y - mi * kRows);
+    tile.row0 = (long long)(lo / (p.E / p.N)) * p.cap + g.x + mi * kRows;
     const int nb = p.n >> 7;
     if (kSwiglu) {
         tile.blk0 = ni;
@@ -136,32 +152,43 @@ __device__ __forceinline__ void store_rows64(uint8_t *stage, const uint32_t (&v)
     }
 }
 
-template <bool kSwiglu>
+// kPair: two CTAs of a cluster share a tile of 256 rows.  Each loads its 128 rows
+// and one of the two weight blocks, and the tensor cores of both read both: half
+// the weight bytes through L2, the port of the SM and its shared memory.  The
+// even CTA issues the products of both and holds the barriers that it waits on;
+// each CTA loads its own stages and sums its own rows.
+template <bool kSwiglu, bool kPair>
 __global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const Product p, const __grid_constant__ CUtensorMap map_a,
               const __grid_constant__ CUtensorMap map_w) {
+    constexpr int kStages = stage_count(kPair), kStageBytes = stage_bytes(kPair);
+    constexpr int kRows = kPair ? 2 * kTileRows : kTileRows;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *stages = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *staging = stages + kStages * kStageBytes;
+    uint8_t *stages = smem_raw + align1024(smem_raw);
+    uint8_t *staging = stages + kStageRing;
     ProductShared &s = *reinterpret_cast<ProductShared *>(staging + kSumWarps * kStageOut);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
+    const int worker = kPair ? blockIdx.x >> 1 : blockIdx.x;
+    const int workers = kPair ? gridDim.x >> 1 : gridDim.x;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s.full[i], 1);
+            mbar_init(&s.full[i], kPair ? 2 : 1);
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], kSumWarps);
+            mbar_init(&s.tempty[i], kPair ? 2 * kSumWarps : kSumWarps);
+            mbar_init(&s.sfull[i], kScaleWarps * 32);
+            mbar_init(&s.sempty[i], kSumWarps);
         }
         mbar_init(&s.drain, 1);
         s.stop = 0;
         s.first[0] = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tc_alloc<512>(&s.tmem);
+    if (warp == kMmaWarp) tc_alloc<512, kPair>(&s.tmem);
     if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_w);
@@ -171,14 +198,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int before = 0;
     for (int e0 = 0; e0 < p.E; e0 += kProductThreads) {
         const int e = e0 + tid;
-        const int mt = e < p.E ? (group_rows(p, e).y + kTileRows - 1) / kTileRows : 0;
+        const int mt = e < p.E ? (group_rows(p, e).y + kRows - 1) / kRows : 0;
         const int upto = block_inclusive_scan(mt, s.wsum, &s.total);
         if (e < p.E) s.first[e + 1] = before + upto;
         before += s.total;
         __syncthreads();
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kPair)
+        cg::this_cluster().sync();  // both CTAs' barriers are there
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     volatile int *stop = &s.stop;
@@ -190,34 +220,63 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kTmaWarp && lane == 0) {
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
-                const int boxes = (tile.rows + kBoxRows - 1) / kBoxRows;
-                const uint32_t bytes =
-                    boxes * kBoxRows * kBlk + (tile.blk1 >= 0 ? 2 : 1) * kBlk * kBlk;
-                const int w0 = tile.e * p.n + tile.blk0 * kBlk, w1 = tile.e * p.n + tile.blk1 * kBlk;
+            for (int t = worker; ok && t < tiles; t += workers) {
+                const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
+                const int rows = min(tile.rows - rank * kTileRows, kTileRows);
+                const int boxes = rows > 0 ? (rows + kBoxRows - 1) / kBoxRows : 0;
+                const bool two = tile.blk1 >= 0;
+                // weight rows: alone one or two blocks; in a pair a block each,
+                // or half of the one block each
+                const int wboxes = kPair ? (two ? 2 : 1) : (two ? 4 : 2);
+                int w0 = tile.e * p.n, w1 = w0;
+                if (kPair) {
+                    w0 += two ? (rank ? tile.blk1 : tile.blk0) * kBlk : tile.blk0 * kBlk + rank * 64;
+                } else {
+                    w0 += tile.blk0 * kBlk;
+                    w1 += tile.blk1 * kBlk;
+                }
+                const uint32_t bytes = boxes * kBoxRows * kBlk + wboxes * kWBoxRows * kBlk;
+                const int arow = (int)tile.row0 + rank * kTileRows;
+#pragma unroll 1
                 for (int b = 0; b < Kb; ++b, ++issued) {
                     const int st = issued % kStages;
                     if (issued >= kStages &&
                         !(ok = wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop)))
                         break;
                     uint8_t *a = stages + st * kStageBytes, *w = a + kTileRows * kBlk;
-                    mbar_arrive_expect_tx(&s.full[st], bytes);
-                    tma_tile(w, &map_w, b * kBlk, w0, &s.full[st]);
-                    if (tile.blk1 >= 0) tma_tile(w + kBlk * kBlk, &map_w, b * kBlk, w1, &s.full[st]);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_tile(a + i * kBoxRows * kBlk, &map_a, b * kBlk,
-                                 (int)tile.row0 + i * kBoxRows, &s.full[st]);
+                    if constexpr (kPair) {
+                        const uint32_t bar = dsmem_addr(&s.full[st], 0);
+                        mbar_arrive_expect_tx_cluster(bar, bytes);
+#pragma unroll 1
+                        for (int i = 0; i < wboxes; ++i)
+                            tma_tile_pair(w + i * kWBoxRows * kBlk, &map_w, b * kBlk,
+                                          w0 + i * kWBoxRows, bar);
+#pragma unroll 1
+                        for (int i = 0; i < boxes; ++i)
+                            tma_tile_pair(a + i * kBoxRows * kBlk, &map_a, b * kBlk,
+                                          arow + i * kBoxRows, bar);
+                    } else {
+                        mbar_arrive_expect_tx(&s.full[st], bytes);
+#pragma unroll 1
+                        for (int i = 0; i < wboxes; ++i)
+                            tma_tile(w + i * kWBoxRows * kBlk, &map_w, b * kBlk,
+                                     (i < 2 ? w0 : w1) + (i & 1) * kWBoxRows, &s.full[st]);
+#pragma unroll 1
+                        for (int i = 0; i < boxes; ++i)
+                            tma_tile(a + i * kBoxRows * kBlk, &map_a, b * kBlk, arow + i * kBoxRows,
+                                     &s.full[st]);
+                    }
                 }
             }
         }
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp == kMmaWarp && lane == 0 && rank == 0) {
             bool ok = true;
             int it = 0;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
+            for (int t = worker; ok && t < tiles; t += workers) {
+                const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
                 const uint32_t idesc =
-                    tile.blk1 >= 0 ? tc_e4m3_f32(kTileRows, 256) : tc_e4m3_f32(kTileRows, 128);
+                    tile.blk1 >= 0 ? tc_e4m3_f32(kRows, 256) : tc_e4m3_f32(kRows, 128);
+#pragma unroll 1
                 for (int b = 0; b < Kb; ++b, ++it) {
                     const int st = it % kStages, ac = it & 1;
                     if (it >= 2 && !(ok = wait_or_stop(&s.tempty[ac], (it / 2 - 1) & 1, stop))) break;
@@ -226,12 +285,54 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     const uint64_t a = tc_operand(stages + st * kStageBytes);
                     const uint64_t w = tc_operand(stages + st * kStageBytes + kTileRows * kBlk);
 #pragma unroll
-                    for (int kk = 0; kk < kBlk / 32; ++kk)  // 32 bytes along k: 2 address units
-                        tc_mma(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0);
-                    tc_commit(&s.empty[st]);
-                    tc_commit(&s.tfull[ac]);
+                    for (int kk = 0; kk < kBlk / 32; ++kk) {  // 32 bytes along k: 2 address units
+                        if constexpr (kPair)
+                            tc_mma_pair(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0);
+                        else
+                            tc_mma(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0);
+                    }
+                    if constexpr (kPair) {
+                        tc_commit_pair(&s.empty[st]);
+                        tc_commit_pair(&s.tfull[ac]);
+                    } else {
+                        tc_commit(&s.empty[st]);
+                        tc_commit(&s.tfull[ac]);
+                    }
                 }
             }
+        }
+        if (warp >= kScaleWarp) {
+            bool ok = true;
+            int run = 0;
+            const int r = tid - kScaleWarp * 32;  // and r + 64; r < 8: a weight scale too
+#pragma unroll 1
+            for (int t = worker; ok && t < tiles; t += workers) {
+                const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
+                // rows past the group's last take its scale; they are not stored
+                const int r0 = min(rank * kTileRows + r, tile.rows - 1);
+                const int r1 = min(rank * kTileRows + r + 64, tile.rows - 1);
+                const float *as = p.a_s + (size_t)(tile.row0 + r0) * Kb;
+                const int more = (r1 - r0) * Kb;
+                const float *ws =
+                    p.w_s + ((size_t)tile.e * nb + ((r & 1) && tile.blk1 >= 0 ? tile.blk1 : tile.blk0)) * Kb;
+#pragma unroll 1
+                for (int b = 0; b < Kb; b += kScaleRun, ++run) {
+                    const int buf = run & 1;
+                    if (run >= 2)
+                        ok = __all_sync(kFull, wait_or_stop(&s.sempty[buf], (run / 2 - 1) & 1, stop));
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < kScaleRun; ++i) {
+                        const float *at = as + min(b + i, Kb - 1);
+                        copy4_async(&s.rscale[buf][i][r], at);
+                        copy4_async(&s.rscale[buf][i][r + 64], at + more);
+                    }
+                    if (r < 2 * kScaleRun)
+                        copy4_async(&s.wscale[buf][r >> 1][r & 1], ws + min(b + (r >> 1), Kb - 1));
+                    copies_arrive(&s.sfull[buf]);
+                }
+            }
+            copies_wait();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
@@ -239,63 +340,61 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + wg * 64;
         uint8_t *stage = staging + warp * kStageOut;
         bool ok = true;
-        int it = 0;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
-            const int r = quad * 32 + lane;
+        int it = 0, run = -1;
+#pragma unroll 1
+        for (int t = worker; ok && t < tiles; t += workers) {
+            const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
+            const int r = quad * 32 + lane, rr = rank * kTileRows + r;
             const bool two = tile.blk1 >= 0;
-            // rows past the group's last read its scale; they are not stored
-            const float *as = p.a_s + (size_t)(tile.row0 + min(r, tile.rows - 1)) * Kb;
-            const float *ws0 = p.w_s + ((size_t)tile.e * nb + tile.blk0) * Kb;
-            const float *ws1 = p.w_s + ((size_t)tile.e * nb + (two ? tile.blk1 : tile.blk0)) * Kb;
             uint64_t acc[2][32] = {};
-            // scales two blocks ahead
-            float sa = __ldg(as), s0 = __ldg(ws0), s1 = __ldg(ws1);
-            const int o1 = min(1, Kb - 1);
-            float sa1 = __ldg(as + o1), s01 = __ldg(ws0 + o1), s11 = __ldg(ws1 + o1);
+#pragma unroll 1
             for (int b = 0; b < Kb; ++b, ++it) {
-                const int ac = it & 1, o2 = min(b + 2, Kb - 1);
-                const float sa2 = __ldg(as + o2), s02 = __ldg(ws0 + o2), s12 = __ldg(ws1 + o2);
+                const int ac = it & 1, at = b % kScaleRun;
+                if (at == 0) {
+                    ++run;
+                    ok = __all_sync(kFull, wait_or_stop(&s.sfull[run & 1], (run / 2) & 1, stop));
+                    if (!ok) break;
+                }
+                const float sa = s.rscale[run & 1][at][r];
+                const float2 sw = *reinterpret_cast<const float2 *>(s.wscale[run & 1][at]);
+                const float f[2] = {sa * sw.x, sa * sw.y};
                 ok = __all_sync(kFull, wait_or_stop(&s.tfull[ac], (it / 2) & 1, stop));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && !two) break;
-                    const float f = sa * (h ? s1 : s0);
-                    const uint64_t ff = pack2(__float_as_uint(f), __float_as_uint(f));
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t v[32];
-                        tc_ld32(v, mine + ac * 256 + h * 128 + q * 32);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[h][q * 16 + i] =
-                                fma2(pack2(v[2 * i], v[2 * i + 1]), ff, acc[h][q * 16 + i]);
+                for (int c = 0; c < 8; ++c) {  // 16 columns; a tile of one block ignores half
+                    uint32_t v[16];
+                    tc_ld16(v, mine + ac * 256 + c / 4 * 128 + c % 4 * 16);
+                    tc_wait_ld();
+                    if (c == 7) {  // all of it is in registers: the accumulator is free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (kPair)
+                                mbar_arrive_cluster(dsmem_addr(&s.tempty[ac], 0));
+                            else
+                                mbar_arrive(&s.tempty[ac]);
+                            if (at == kScaleRun - 1 || b == Kb - 1) mbar_arrive(&s.sempty[run & 1]);
+                        }
                     }
+                    const uint64_t ff = pack2(__float_as_uint(f[c / 4]), __float_as_uint(f[c / 4]));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[c / 4][c % 4 * 8 + j] =
+                            fma2(pack2(v[2 * j], v[2 * j + 1]), ff, acc[c / 4][c % 4 * 8 + j]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.tempty[ac]);
-                sa = sa1;
-                s0 = s01;
-                s1 = s11;
-                sa1 = sa2;
-                s01 = s02;
-                s11 = s12;
             }
             // either every sum warp has its sums or none goes on: the barriers
             // below are met by all
             ok = bar_named_all(1, kSumWarps * 32, ok);
             if (!ok) break;
-            const int rows = tile.rows - quad * 32;  // of this warp
+            const int rows = tile.rows - rank * kTileRows - quad * 32;  // of this warp
             if constexpr (!kSwiglu) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (h == 1 && !two) break;
                     const int blk = h ? tile.blk1 : tile.blk0;
-                    uint16_t *y = p.y + (size_t)(tile.row0 + quad * 32) * p.n + blk * 128 + wg * 64;
+                    uint16_t *y = p.y + (size_t)(tile.row0 + rank * kTileRows + quad * 32) * p.n + blk * 128 + wg * 64;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         uint32_t o[16];
@@ -337,31 +436,56 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
                 const int I = p.n >> 1;
                 store_rows64(stage, o,
-                             p.h_q + (size_t)(tile.row0 + quad * 32) * I + tile.blk0 * 128 + wg * 64,
+                             p.h_q + (size_t)(tile.row0 + rank * kTileRows + quad * 32) * I + tile.blk0 * 128 + wg * 64,
                              (size_t)I, rows);
                 if (wg == 0 && lane < rows)
-                    p.h_s[(size_t)(tile.row0 + r) * (I >> 7) + tile.blk0] = scale;
+                    p.h_s[(size_t)(tile.row0 + rr) * (I >> 7) + tile.blk0] = scale;
             }
         }
     }
     tc_fence_before();
-    __syncthreads();
-    if (s.stop) {  // a kernel that gave up leaves no copy and no product in flight
-        if (warp == kTmaWarp && lane == 0)
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
-        if (warp == kMmaWarp && lane == 0) {
-            tc_commit(&s.drain);
+    bool gave_up;
+    if constexpr (kPair) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();  // no arrival for a CTA that has gone
+        gave_up = *cluster.map_shared_rank(&s.stop, 0) || *cluster.map_shared_rank(&s.stop, 1);
+        cluster.sync();
+    } else {
+        __syncthreads();
+        gave_up = s.stop;
+    }
+    if (gave_up) {  // no copy and no product is left in flight
+        if (warp == kTmaWarp && lane == 0) {
+            if constexpr (kPair) {
+                // the even CTA's barriers count both CTAs' copies; give them
+                // a thousand times what a copy takes
+                for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+            } else {
+                for (int i = max(0, issued - kStages); i < issued; ++i)
+                    mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
+            }
+        }
+        if (warp == kMmaWarp && lane == 0 && rank == 0) {
+            if constexpr (kPair)
+                tc_commit_pair(&s.drain);
+            else
+                tc_commit(&s.drain);
             mbar_wait(&s.drain, 0);
         }
-        __syncthreads();
+        if constexpr (kPair)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
     }
     tc_fence_after();
-    if (warp == kMmaWarp) tc_free<512>(tmem);
-    if (tid == 0 && s.stop && p.status) flag(p.status, MOE_ST_TIMEOUT);
+    if (warp == kMmaWarp) tc_free<512, kPair>(tmem);
+    if (tid == 0 && gave_up && p.status) flag(p.status, MOE_ST_TIMEOUT);
 }
 
 // ------------------------------------------------------------ host
+
+// Rows of an expert from which two CTAs share a tile.
+constexpr double kPairRows = 192;
 
 static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const uint8_t *w_q,
                                   cudaStream_t st) {
@@ -370,24 +494,38 @@ static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const ui
                                    p.h_q, p.h_s, p.status, st);
     CUtensorMap map_a, map_w;
     cudaError_t err = tile_map(&map_a, a_q, (int64_t)p.N * p.cap, p.k, kBoxRows);
-    if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kBlk);
+    if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kWBoxRows);
     if (err != cudaSuccess) return err;
-    const bool swiglu = p.h_q != nullptr;
-    const auto kern = swiglu ? k_product<true> : k_product<false>;
+    const bool swiglu = p.h_q != nullptr, pair = p.rows >= kPairRows;
+    const auto kern = swiglu ? (pair ? k_product<true, true> : k_product<true, false>)
+                             : (pair ? k_product<false, true> : k_product<false, false>);
     static LaunchMemo memo;
     int done = 0;
-    err = memo.get(swiglu, &done, [&](int *v) {
+    err = memo.get(2 * swiglu + pair, &done, [&](int *v) {
         *v = 1;
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kProductSmem);
     });
     if (err != cudaSuccess) return err;
-    // as many CTAs as there can be tiles: every expert's last tile may be part full
+    // as many workers as there can be tiles: every expert's last may be part full
     const int64_t nb = p.n >> 7, ntn = swiglu ? nb >> 1 : (nb + 1) >> 1;
-    const int64_t rows = (int64_t)p.N * p.cap;
-    const int64_t most = (rows / kTileRows + (rows < p.E ? rows : p.E)) * ntn;
-    const int grid = (int)(most < sm_count() ? most : sm_count());
-    return launch_kernel(kern, dim3(grid), dim3(kProductThreads), kProductSmem, st, p, map_a, map_w);
+    const int64_t rows = (int64_t)p.N * p.cap, each = pair ? 2 * kTileRows : kTileRows;
+    const int64_t most = (rows / each + (rows < p.E ? rows : p.E)) * ntn;
+    const int workers = pair ? sm_count() / 2 : sm_count();
+    const int grid = (int)(most < workers ? most : workers) * (pair ? 2 : 1);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = pair ? 2 : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = kProductSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, map_a, map_w);
 }
 
 // The checks that both products share; fills *p.
@@ -404,8 +542,10 @@ static int check_product(const moe_shape *sh, int64_t n, int k, const uint8_t *a
         !ok_optional(status))
         return MOE_EINVAL;
     if (!grp_off && sh->E != sh->N) return MOE_EINVAL;
-    *p = Product{sh->N, sh->E, (int)z.cap, (int)n, k,       a_s,
-                 grp_off, w_s, nullptr,    nullptr, nullptr, status};
+    const double sent = (double)sh->N * sh->T * sh->R;
+    *p = Product{sh->N,   sh->E, (int)z.cap, (int)n,  k,       (sent < rows ? sent : rows) / sh->E,
+                 a_s,     grp_off, w_s,      nullptr, nullptr, nullptr,
+                 status};
     return MOE_OK;
 }
 

@@ -9,7 +9,26 @@
 
 namespace moe {
 
+// Bytes from p to the next multiple of 1024 in shared memory.  As an offset: a
+// pointer rounded by itself would no longer be known to point there, and every
+// access through it would be a generic one.
+__device__ __forceinline__ uint32_t align1024(const void *p) { return -smem_addr(p) & 1023; }
+
 // ------------------------------------------------------------ waits
+
+// mbar_try_wait that may sleep up to 20 us before it answers: a waiting warp
+// that asks again and again takes issue slots from those at work.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 
 // Waits for the phase with the given parity, at most about a second, and
 // leaves at once when another role of the CTA has given up (*stop).  False:
@@ -18,7 +37,7 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, vol
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (clock64() - t0 < kWaitCycles) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait_for(bar, parity)) return true;
         if (*stop) return false;
     }
     *stop = 1;
@@ -45,6 +64,20 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+
+// ------------------------------------------------------------ small copies
+
+// Four bytes, global -> shared, asynchronously; `bar` gets this thread's arrival
+// once its copies so far are there (an arrival that the barrier's count includes).
+__device__ __forceinline__ void copy4_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ------------------------------------------------------------ tcgen05
 
@@ -73,6 +106,49 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
+// The pair forms: the products of two CTAs of a cluster on one tile, issued by
+// the even one.  a: each CTA's own 128 rows (M = 256); b: each CTA's half of the
+// N rows; d: each CTA's rows by all N columns, at the same tensor-memory address.
+__device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// The barrier at this place in both CTAs gets an arrival.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// tma_tile whose bytes are counted on the even CTA's barrier (a cluster address).
+__device__ __forceinline__ void tma_tile_pair(void *dst, const CUtensorMap *map, int x, int y,
+                                              uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Arrivals on a barrier of the cluster, its address from dsmem_addr.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+
 // `bar` gets one arrival once the thread's products so far are done.
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
     asm volatile(
@@ -90,17 +166,28 @@ __device__ __forceinline__ void tc_fence_after() {
 
 // kCols columns of the SM's tensor memory (a power of two from 32 to 512); one
 // warp allocates and frees.
-template <int kCols>
+template <int kCols, bool kPair = false>
 __device__ __forceinline__ void tc_alloc(uint32_t *where) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(where)),
-                 "n"(kCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(where)),
+                     "n"(kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(where)),
+                     "n"(kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
 }
-template <int kCols>
+template <int kCols, bool kPair = false>
 __device__ __forceinline__ void tc_free(uint32_t taddr) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
+    if constexpr (kPair)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
 }
 
 // 32 columns of the warp's 32 lanes, one lane's row a thread.  The values

@@ -117,8 +117,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     constexpr int kCols = 2 * kHalves * NMAX;  // two accumulators
     using Shared = ThinShared<kMode>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~static_cast<uintptr_t>(1023));
+    uint8_t *ring = smem_raw + align1024(smem_raw);
     Shared &s = *reinterpret_cast<Shared *>(ring + kStages * kBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blk = blockIdx.x, Kb = p.k >> 7, nb = p.n >> 7;
