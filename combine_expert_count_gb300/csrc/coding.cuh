@@ -51,10 +51,21 @@ __device__ __forceinline__ uint32_t code4_by(float a, float b, float c, float d,
 // kTinyUp first.
 constexpr float kTinyScale = 0x1p-120f, kTinyUp = 0x1p100f;
 
-// Eight values of a block whose scale is known (0: a block of zeros).
-__device__ __forceinline__ uint2 code8(const float (&v)[8], float scale) {
-    if (scale == 0.0f) return make_uint2(0u, 0u);
-    return make_uint2(code4(v[0], v[1], v[2], v[3], scale), code4(v[4], v[5], v[6], v[7], scale));
+// The factor that takes a block's values to codes, 0 for a block of zeros, and,
+// where the scale is tiny, what to multiply the values by before it (else 1).
+__device__ __forceinline__ float code_factor(float scale, float *first) {
+    *first = scale < kTinyScale ? kTinyUp : 1.0f;
+    return scale == 0.0f ? 0.0f : __frcp_rn(scale * *first);
+}
+
+// Eight values of a block whose scale is known.
+__device__ __forceinline__ uint2 code8_by(float (&v)[8], float scale) {
+    float first;
+    const float inv = code_factor(scale, &first);
+    if (first != 1.0f)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= first;
+    return make_uint2(code4_by(v[0], v[1], v[2], v[3], inv), code4_by(v[4], v[5], v[6], v[7], inv));
 }
 
 }  // namespace moe

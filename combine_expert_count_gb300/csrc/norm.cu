@@ -25,30 +25,43 @@ __device__ __forceinline__ void unpack8(float (&v)[8], const uint4 &w) {
 // from the load to the last store, chunk tid + i * blockDim.x, so a row is
 // read once; blockDim.x is a multiple of 32, so the sixteen chunks of a block
 // of 128 are sixteen neighbouring lanes.
-template <int V>
-__global__ void __launch_bounds__(V == 8 ? 1024 : 256) k_rmsnorm(int H, float eps, const uint16_t *x, const uint16_t *res,
-                          const uint16_t *__restrict__ gamma, uint16_t *res_out, uint16_t *y,
-                          uint8_t *__restrict__ q, float *__restrict__ s) {
+template <int V, int kMost>
+__global__ void __launch_bounds__(kMost) k_rmsnorm(int H, float eps, const uint16_t *x,
+                                                   const uint16_t *res,
+                                                   const uint16_t *__restrict__ gamma,
+                                                   uint16_t *res_out, uint16_t *y,
+                                                   uint8_t *__restrict__ q, float *__restrict__ s) {
     __shared__ float wsum[32];
     const int tid = threadIdx.x, nthr = blockDim.x, nch = H >> 3;
     const size_t row = blockIdx.x, base = row * (size_t)H;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float v[V][8], acc = 0.0f;
+    uint4 g[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nthr;
         if (c >= nch) continue;
         unpack8(v[i], *reinterpret_cast<const uint4 *>(x + base + c * 8));
+        g[i] = __ldg(reinterpret_cast<const uint4 *>(gamma + c * 8));
         if (res) add8(v[i], *reinterpret_cast<const uint4 *>(res + base + c * 8));
-        if (res_out) *reinterpret_cast<uint4 *>(res_out + base + c * 8) = pack_bf16x8(v[i]);
 #pragma unroll
         for (int u = 0; u < 8; ++u) acc = __fmaf_rn(v[i][u], v[i][u], acc);
+    }
+    if (res_out) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = tid + i * nthr;
+            if (c < nch) *reinterpret_cast<uint4 *>(res_out + base + c * 8) = pack_bf16x8(v[i]);
+        }
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(kFull, acc, d);
     if ((tid & 31) == 0) wsum[tid >> 5] = acc;
     __syncthreads();
-    float sum = 0.0f;
-    for (int w = 0; w < (nthr >> 5); ++w) sum += wsum[w];
+    float sum = (tid & 31) < (nthr >> 5) ? wsum[tid & 31] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
     const float rstd = __frsqrt_rn(sum / (float)H + eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -56,10 +69,10 @@ __global__ void __launch_bounds__(V == 8 ? 1024 : 256) k_rmsnorm(int H, float ep
         const bool in = c < nch;
         uint32_t amax = 0;
         if (in) {
-            float g[8];
-            unpack8(g, __ldg(reinterpret_cast<const uint4 *>(gamma + c * 8)));
+            float w[8];
+            unpack8(w, g[i]);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * g[u];
+            for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
             if (y) *reinterpret_cast<uint4 *>(y + base + c * 8) = pack_bf16x8(v[i]);
             amax = amax8(v[i]);
         }
@@ -68,24 +81,47 @@ __global__ void __launch_bounds__(V == 8 ? 1024 : 256) k_rmsnorm(int H, float ep
             for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, d));
             if (in) {
                 const float scale = block_scale(amax);
-                *reinterpret_cast<uint2 *>(q + base + c * 8) = code8(v[i], scale);
+                *reinterpret_cast<uint2 *>(q + base + c * 8) = code8_by(v[i], scale);
                 if ((c & 15) == 0) s[row * (size_t)(H >> 7) + (c >> 4)] = scale;
             }
         }
     }
 }
 
+template <int V, int kMost>
+static cudaError_t launch_rows(int rows, int nthr, cudaStream_t st, int H, float eps,
+                               const uint16_t *x, const uint16_t *res, const uint16_t *gamma,
+                               uint16_t *res_out, uint16_t *y, uint8_t *q, float *s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)rows);
+    cfg.blockDim = dim3((unsigned)nthr);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_rmsnorm<V, kMost>, H, eps, x, res, gamma, res_out, y, q, s);
+}
+
 static cudaError_t launch_rmsnorm(const moe_shape &sh, float eps, const uint16_t *x,
                                   const uint16_t *res, const uint16_t *gamma, uint16_t *res_out,
                                   uint16_t *y, uint8_t *q, float *s, cudaStream_t st) {
-    const long long rows = (long long)sh.N * sh.T;
-    const int nch = sh.H >> 3;
+    const int rows = sh.N * sh.T, nch = sh.H >> 3;
+    const int most = rows <= sm_count() ? 1024 : 256;
     int V = 1;
-    while (V < 8 && nch > 256 * V) V *= 2;
+    while (V < 8 && nch > most * V) V *= 2;
     const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
-    const auto kern = V == 1 ? k_rmsnorm<1> : V == 2 ? k_rmsnorm<2> : V == 4 ? k_rmsnorm<4> : k_rmsnorm<8>;
-    return launch_kernel(kern, dim3((unsigned)rows), dim3(nthr), 0, st, sh.H, eps, x, res, gamma,
-                         res_out, y, q, s);
+    const auto go = nthr <= 256
+                        ? (V == 1   ? launch_rows<1, 256>
+                           : V == 2 ? launch_rows<2, 256>
+                           : V == 4 ? launch_rows<4, 256>
+                                    : launch_rows<8, 256>)
+                        : (V == 1   ? launch_rows<1, 1024>
+                           : V == 2 ? launch_rows<2, 1024>
+                           : V == 4 ? launch_rows<4, 1024>
+                                    : launch_rows<8, 1024>);
+    return go(rows, nthr, st, sh.H, eps, x, res, gamma, res_out, y, q, s);
 }
 
 }  // namespace moe
