@@ -25,8 +25,20 @@ __device__ __forceinline__ void unpack8(float (&v)[8], const uint4 &w) {
 // from the load to the last store, chunk tid + i * blockDim.x, so a row is
 // read once; blockDim.x is a multiple of 32, so the sixteen chunks of a block
 // of 128 are sixteen neighbouring lanes.
+//
+// Bound by HBM: per row 2 H bytes each of x, res, res_out and y and H (1 + 1/32)
+// of codes.  With all of them, 32767 rows of 7168 take 309 us, 6.86 TB/s, as
+// much as a copy.  What that took is threads in flight, not bytes a thread: two
+// chunks a thread (448 threads a row) in 32 registers, four CTAs an SM; at 40
+// registers and three CTAs 339 us, with four chunks a thread 379, eight 506.
+// gamma is read again for the second half (L1 holds it) rather than kept in
+// registers: 322 us with it kept.  Few rows have an SM each: one chunk a thread.
+// The exact divisions of the coding are not what bounds it (379 us either way
+// at four chunks), but their registers are.
+constexpr int norm_ctas(int V, int most) { return most == 512 ? (V <= 2 ? 4 : V == 4 ? 2 : 1) : 1; }
+
 template <int V, int kMost>
-__global__ void __launch_bounds__(kMost) k_rmsnorm(int H, float eps, const uint16_t *x,
+__global__ void __launch_bounds__(kMost, norm_ctas(V, kMost)) k_rmsnorm(int H, float eps, const uint16_t *x,
                                                    const uint16_t *res,
                                                    const uint16_t *__restrict__ gamma,
                                                    uint16_t *res_out, uint16_t *y,
@@ -37,13 +49,11 @@ __global__ void __launch_bounds__(kMost) k_rmsnorm(int H, float eps, const uint1
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float v[V][8], acc = 0.0f;
-    uint4 g[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nthr;
         if (c >= nch) continue;
         unpack8(v[i], *reinterpret_cast<const uint4 *>(x + base + c * 8));
-        g[i] = __ldg(reinterpret_cast<const uint4 *>(gamma + c * 8));
         if (res) add8(v[i], *reinterpret_cast<const uint4 *>(res + base + c * 8));
 #pragma unroll
         for (int u = 0; u < 8; ++u) acc = __fmaf_rn(v[i][u], v[i][u], acc);
@@ -70,7 +80,7 @@ __global__ void __launch_bounds__(kMost) k_rmsnorm(int H, float eps, const uint1
         uint32_t amax = 0;
         if (in) {
             float w[8];
-            unpack8(w, g[i]);
+            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(gamma + c * 8)));
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
             if (y) *reinterpret_cast<uint4 *>(y + base + c * 8) = pack_bf16x8(v[i]);
@@ -108,15 +118,15 @@ static cudaError_t launch_rmsnorm(const moe_shape &sh, float eps, const uint16_t
                                   const uint16_t *res, const uint16_t *gamma, uint16_t *res_out,
                                   uint16_t *y, uint8_t *q, float *s, cudaStream_t st) {
     const int rows = sh.N * sh.T, nch = sh.H >> 3;
-    const int most = rows <= sm_count() ? 1024 : 256;
+    const int most = rows <= sm_count() ? 1024 : 512;
     int V = 1;
     while (V < 8 && nch > most * V) V *= 2;
     const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
-    const auto go = nthr <= 256
-                        ? (V == 1   ? launch_rows<1, 256>
-                           : V == 2 ? launch_rows<2, 256>
-                           : V == 4 ? launch_rows<4, 256>
-                                    : launch_rows<8, 256>)
+    const auto go = nthr <= 512
+                        ? (V == 1   ? launch_rows<1, 512>
+                           : V == 2 ? launch_rows<2, 512>
+                           : V == 4 ? launch_rows<4, 512>
+                                    : launch_rows<8, 512>)
                         : (V == 1   ? launch_rows<1, 1024>
                            : V == 2 ? launch_rows<2, 1024>
                            : V == 4 ? launch_rows<4, 1024>
