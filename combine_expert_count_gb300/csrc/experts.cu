@@ -193,6 +193,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_w);
     }
+    // what is above runs while the kernel before this one ends
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
     // row tiles before each expert
     int before = 0;
@@ -514,7 +517,9 @@ static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const ui
     const int workers = pair ? sm_count() / 2 : sm_count();
     const int grid = (int)(most < workers ? most : workers) * (pair ? 2 : 1);
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = pair ? 2 : 1;
     attr[0].val.clusterDim.y = 1;
@@ -524,7 +529,7 @@ static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const ui
     cfg.dynamicSmemBytes = kProductSmem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p, map_a, map_w);
 }
 

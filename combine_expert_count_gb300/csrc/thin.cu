@@ -44,6 +44,7 @@ struct ThinArgs {
     int ntok, E, R, H, inter;
     bool by_expert;  // k_thin<kUp>: units are experts, not assignments
     int passes;      // units of 16 rows that an expert may need
+    bool push;       // a cluster's parts send their sums to the first one's inbox
     const uint16_t *x;
     const int32_t *idx;
     const float *topk_w;
@@ -58,6 +59,7 @@ struct ThinArgs {
     uint16_t *y;
     // both
     int n, k;  // outputs and inputs of the product
+    int most;  // rows that a unit can have
     const float *w_s;
     int32_t *status;
 };
@@ -67,6 +69,10 @@ __host__ __device__ constexpr bool thin_pair(Thin m) { return m == Thin::kUp || 
 // Columns of a product: rows of one expert that meet its weights at a time.  A
 // unit with more is several units, whose reads of the weights meet in L2.
 constexpr int kThinRowsAt = 16;
+
+// Accumulators in tensor memory: an item's way from its products to its sums
+// takes several times as long as the products of a few rows.
+constexpr int kAccs = 4;
 
 // Ring stages for which two CTAs fit an SM.
 __host__ __device__ constexpr int thin_stages(Thin m) { return thin_pair(m) ? 3 : 5; }
@@ -78,7 +84,7 @@ template <Thin kMode>
 struct alignas(16) ThinShared {
     static constexpr int kStages = thin_stages(kMode);
     float scale[kStages][kThinRowsAt];  // of the rows' pieces in each stage
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint64_t full[kStages], empty[kStages], tfull[kAccs], tempty[kAccs], drain, inbox;
     uint32_t tmem;
     int stop, total, unit[3];
     unsigned chosen[2];
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     constexpr int kHalves = kPair ? 2 : 1;
     constexpr int kStages = thin_stages(kMode), kBytes = thin_stage_bytes(kMode);
     constexpr int NMAX = kThinRowsAt;
-    constexpr int kCols = 2 * kHalves * NMAX;  // two accumulators
+    constexpr int kCols = kAccs * kHalves * NMAX;
     using Shared = ThinShared<kMode>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + align1024(smem_raw);
@@ -123,6 +129,34 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     const int blk = blockIdx.x, Kb = p.k >> 7, nb = p.n >> 7;
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+
+    // ---------------------------------------------------------------- set-up
+    // while the kernel before this one ends
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 1 + kRowWarps);
+            mbar_init(&s.empty[i], 1 + 4);
+        }
+        for (int i = 0; i < kAccs; ++i) {
+            mbar_init(&s.tfull[i], 1);
+            mbar_init(&s.tempty[i], 4);
+        }
+        mbar_init(&s.drain, 1);
+        mbar_init(&s.inbox, max(1, 4 * (parts - 1)));
+        s.stop = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&map_w);
+    }
+    if (warp == kThinMma) tc_alloc<kCols>(&s.tmem);
+    // a part's inbox is there before another sends to it: waited for at the end
+    if (parts > 1 && p.push) cluster.barrier_arrive();
+    if constexpr (kMode != Thin::kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const auto leave = [&]() {  // nothing to do: all threads
+        __syncthreads();
+        if (parts > 1 && p.push) cluster.barrier_wait();
+        if (warp == kThinMma) tc_free<kCols>(s.tmem);
+    };
 
     // ---------------------------------------------------------------- the unit
     // kDown: the whole list of experts; else one expert and its m rows
@@ -146,14 +180,13 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             ids[i] = __ldg(p.idx + i);
             bad |= (unsigned)ids[i] >= (unsigned)p.E;
         }
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (blockIdx.x == 0 && blockIdx.y == 0 && part == 0) {
             bad = __syncthreads_or(bad);
             if (tid == 0) *p.status = bad ? MOE_ST_BAD_EXPERT : 0;
         }
         __syncthreads();
         e = p.by_expert ? unit : ids[unit];
-        if ((unsigned)e >= (unsigned)p.E) return;
+        if ((unsigned)e >= (unsigned)p.E) return leave();
         // thread t < 64: token t's first assignment to the expert
         int k = -1;
         if (tid < MOE_FEW_MAX_TOKENS) {
@@ -172,7 +205,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             s.list[at] = tid * p.R + k;
         }
         __syncthreads();
-        if (m <= r0 || (!p.by_expert && s.list[0] != unit)) return;
+        if (m <= r0 || (!p.by_expert && s.list[0] != unit)) return leave();
         m = min(m - r0, NMAX);
     } else if constexpr (kMode == Thin::kDown) {
         for (int i = tid; i < 2 * p.E; i += kThinThreads) who[i] = 0;
@@ -245,26 +278,11 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             __syncthreads();
         }
         e = s.unit[0];
-        if (e < 0 || s.unit[2] <= r0) return;
+        if (e < 0 || s.unit[2] <= r0) return leave();
         m = min(s.unit[2] - r0, NMAX);
         row0 = (long long)(e / Er) * p.cap + s.unit[1] + r0;
     }
 
-    // ---------------------------------------------------------------- set-up
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s.full[i], 1 + kRowWarps);
-            mbar_init(&s.empty[i], 1 + 4);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], 4);
-        }
-        mbar_init(&s.drain, 1);
-        s.stop = 0;
-        fence_mbar_init();
-    }
-    if (warp == kThinMma) tc_alloc<kCols>(&s.tmem);
     fence_async_smem();  // kUp's ids lay where the ring is
     tc_fence_before();
     __syncthreads();
@@ -305,9 +323,9 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         if (lane == 0) {
             int it = 0;
             for (int item = i0; item < i1; ++item, ++it) {
-                const int st = it % kStages, ac = it & 1;
+                const int st = it % kStages, ac = it % kAccs;
                 const uint32_t idesc = tc_e4m3_f32(128, NMAX);
-                if (it >= 2 && !wait_or_stop(&s.tempty[ac], (it / 2 - 1) & 1, stop)) break;
+                if (it >= kAccs && !wait_or_stop(&s.tempty[ac], (it / kAccs - 1) & 1, stop)) break;
                 if (!wait_or_stop(&s.full[st], (it / kStages) & 1, stop)) break;
                 tc_fence_after();
                 const uint8_t *w = ring + st * kBytes;
@@ -418,11 +436,11 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             float u0 = __ldg(wu), u1 = __ldg(wu + min(1, nblk - 1));
             bool ok = true;
             for (int b = 0; b < nblk; ++b, ++it) {
-                const int st = it % kStages, ac = it & 1;
+                const int st = it % kStages, ac = it % kAccs;
                 const float g2 = __ldg(ws + min(b + 2, nblk - 1));
                 const float u2 = kPair ? __ldg(wu + min(b + 2, nblk - 1)) : 0.0f;
                 // the rows' scales were stored before their arrivals on full
-                ok = wait_or_stop(&s.tfull[ac], (it / 2) & 1, stop) &&
+                ok = wait_or_stop(&s.tfull[ac], (it / kAccs) & 1, stop) &&
                      wait_or_stop(&s.full[st], (it / kStages) & 1, stop);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
@@ -494,8 +512,30 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     tc_fence_after();
     if (warp == kThinMma) tc_free<kCols>(tmem);
 
+    const bool push = parts > 1 && p.push;
+    if (push) cluster.barrier_wait();  // from the set-up
     if constexpr (kMode == Thin::kDown) {
         // the parts of the experts' run, added in the cluster's order
+        if (push) {
+            float *inbox = reinterpret_cast<float *>(experts + thin_entries(A, p.E));
+            if (part > 0) {
+                if (warp >= 4) return;
+                float *to = cluster.map_shared_rank(inbox, 0) + (part - 1) * p.ntok * 128;
+                for (int t = 0; t < p.ntok; ++t) to[t * 128 + tid] = sums[t * 128 + tid];
+                __syncwarp();
+                if (lane == 0) mbar_arrive_release_cluster(dsmem_addr(&s.inbox, 0));
+                return;
+            }
+            if (warp >= 4) return;
+            const bool ok = __all_sync(kFull, mbar_wait_cluster(&s.inbox, 0));
+            if (!ok && tid == 0 && p.status) flag(p.status, MOE_ST_TIMEOUT);
+            for (int t = 0; t < p.ntok; ++t) {
+                float v = sums[t * 128 + tid];
+                for (int q = 1; q < parts; ++q) v += inbox[((q - 1) * p.ntok + t) * 128 + tid];
+                p.out[(size_t)t * p.H + blk * 128 + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            }
+            return;
+        }
         if (parts > 1) cluster.sync();
         for (int i = part * kThinThreads + tid; i < p.ntok * 64; i += parts * kThinThreads) {
             float2 v = make_float2(0.0f, 0.0f);
@@ -510,28 +550,40 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         if (parts > 1) cluster.sync();  // no part goes while it is read
         return;
     }
-    // parts of k: the others leave their sums in their rings, the first adds them
-    float *left = reinterpret_cast<float *>(ring);  // [half][column][128]
+    // parts of k: the others' sums come to the first one's inbox, or wait in
+    // their rings for it to fetch them
     if (parts > 1) {
+        float *left = push ? reinterpret_cast<float *>(&s + 1) : reinterpret_cast<float *>(ring);
+        const int rows = push ? min(NMAX, p.most) : NMAX;  // columns of a part's place
         if (warp < 4 && part > 0) {
+            float *to = push ? cluster.map_shared_rank(left, 0) + (part - 1) * kHalves * rows * 128 : left;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int j = 0; j < NMAX; ++j)
-                    if (j < m) left[(h * NMAX + j) * 128 + tid] = acc[h][j];
+                    if (j < m) to[(h * rows + j) * 128 + tid] = acc[h][j];
+            if (push) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_release_cluster(dsmem_addr(&s.inbox, 0));
+            }
         }
-        cluster.sync();
+        if (!push) cluster.sync();
         if (warp < 4 && part == 0) {
+            if (push) {
+                const bool ok = __all_sync(kFull, mbar_wait_cluster(&s.inbox, 0));
+                if (!ok && tid == 0 && p.status) flag(p.status, MOE_ST_TIMEOUT);
+            }
             for (int q = 1; q < parts; ++q) {
-                const float *o = cluster.map_shared_rank(left, q);
+                const float *o = push ? left + (q - 1) * kHalves * rows * 128
+                                      : cluster.map_shared_rank(left, q);
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                     for (int j = 0; j < NMAX; ++j)
-                        if (j < m) acc[h][j] += o[(h * NMAX + j) * 128 + tid];
+                        if (j < m) acc[h][j] += o[(h * rows + j) * 128 + tid];
             }
         }
-        cluster.sync();  // no part goes while it is read
+        if (!push) cluster.sync();  // no part goes while it is read
     }
     if (part > 0 || warp >= 4) return;
     const auto row_of = [&](int j) {
@@ -567,21 +619,31 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 
 // ------------------------------------------------------------ host
 
+// Room for the sums that the parts of a cluster send to the first one; where they
+// are more, the first one fetches them, with two barriers of the cluster around
+// (about 2 us against 0.7).
+constexpr int kPushBytes = 7 * 1024;
+
 template <Thin kMode>
-static cudaError_t launch_thin(const ThinArgs &p, const CUtensorMap &map, dim3 grid, int parts,
-                               size_t more_smem, bool after, cudaStream_t st) {
+static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, int parts,
+                               size_t more_smem, cudaStream_t st) {
+    const int inbox = (parts - 1) * 512 * (kMode == Thin::kDown ? p.ntok : (thin_pair(kMode) ? 2 : 1) * p.most);
+    p.push = inbox <= kPushBytes;
+    if (p.push) more_smem += inbox;
     const auto kern = k_thin<kMode>;
     constexpr size_t kFixed = thin_fixed_smem<kMode>();
     constexpr size_t kMost =
         kFixed + (kMode == Thin::kDown
                       ? thin_lists_smem(MOE_FEW_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOPK)
                       : 0);
-    static_assert(kMost <= 232448, "a CTA's shared memory");
+    static_assert(kMost + kPushBytes <= 232448, "a CTA's shared memory");
+    static_assert(kFixed + kPushBytes <= 113 * 1024 || kMode == Thin::kDown, "two CTAs an SM");
     static LaunchMemo memo;
     int done = 0;
     cudaError_t err = memo.get(0, &done, [&](int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kMost + kPushBytes);
     });
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -598,7 +660,7 @@ static cudaError_t launch_thin(const ThinArgs &p, const CUtensorMap &map, dim3 g
     cfg.dynamicSmemBytes = kFixed + more_smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = after ? 2 : 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p, map);
 }
 
@@ -636,8 +698,9 @@ cudaError_t launch_thin_product(int N, int E, int cap, int n, int k, const uint8
     p.passes = (rows + kThinRowsAt - 1) / kThinRowsAt;
     const dim3 grid((unsigned)(h_q ? n >> 8 : n >> 7), (unsigned)(units * p.passes));
     const int parts = thin_parts((int64_t)grid.x * units, k >> 7);
-    if (h_q) return launch_thin<Thin::kSwiglu>(p, map, grid, parts, 0, false, st);
-    return launch_thin<Thin::kGemm>(p, map, grid, parts, 0, false, st);
+    p.most = rows < kThinRowsAt ? rows : kThinRowsAt;
+    if (h_q) return launch_thin<Thin::kSwiglu>(p, map, grid, parts, 0, st);
+    return launch_thin<Thin::kGemm>(p, map, grid, parts, 0, st);
 }
 
 static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13_s,
@@ -655,8 +718,8 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.n = 2 * p.inter;
     p.k = p.H;
     p.w_s = w13_s;
-    err = launch_thin<Thin::kUp>(p, up, gup, thin_parts((int64_t)gup.x * units, p.H >> 7), 0, false,
-                                 st);
+    p.most = p.ntok < kThinRowsAt ? p.ntok : kThinRowsAt;
+    err = launch_thin<Thin::kUp>(p, up, gup, thin_parts((int64_t)gup.x * units, p.H >> 7), 0, st);
     if (err != cudaSuccess) return err;
     p.n = p.H;
     p.k = p.inter;
@@ -664,7 +727,7 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     const dim3 gdown((unsigned)(p.H >> 7));
     return launch_thin<Thin::kDown>(p, down, gdown,
                                     thin_parts(gdown.x, (int64_t)units * (p.inter >> 7)),
-                                    thin_lists_smem(p.ntok, p.E, p.R), true, st);
+                                    thin_lists_smem(p.ntok, p.E, p.R), st);
 }
 
 }  // namespace moe
