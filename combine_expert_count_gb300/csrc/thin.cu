@@ -589,28 +589,36 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     const auto row_of = [&](int j) {
         return kMode == Thin::kUp ? (size_t)s.list[r0 + j] : (size_t)(row0 + j);
     };
-    if constexpr (!kPair) {
+    // The columns go through the thread's own words of the ring to be taken one
+    // after another: sixteen copies of what follows cost 2 us of instruction
+    // fetches, as much as all else after the products.
+    float *own = reinterpret_cast<float *>(ring) + tid;  // [half][column], 128 apart
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int j = 0; j < NMAX; ++j)
-            if (j < m) p.y[row_of(j) * p.n + blk * 128 + tid] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(acc[0][j]));
+            if (j < m) own[(h * NMAX + j) * 128] = acc[h][j];
+    if constexpr (!kPair) {
+#pragma unroll 1
+        for (int j = 0; j < m; ++j)
+            p.y[row_of(j) * p.n + blk * 128 + tid] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(own[j * 128]));
     } else {
         const int I = p.n >> 1;
-#pragma unroll
-        for (int j = 0; j < NMAX; ++j) {
-            if (j >= m) continue;
-            acc[0][j] = silu_mul(acc[0][j], acc[kHalves - 1][j]);
-            const uint32_t am = __reduce_max_sync(kFull, abs_bits(acc[0][j]));
+#pragma unroll 1
+        for (int j = 0; j < m; ++j) {
+            const float h = silu_mul(own[j * 128], own[(NMAX + j) * 128]);
+            own[j * 128] = h;
+            const uint32_t am = __reduce_max_sync(kFull, abs_bits(h));
             if (lane == 0) s.peak[warp][j] = am;
         }
         bar_named(1, 128);
-#pragma unroll
-        for (int j = 0; j < NMAX; ++j) {
-            if (j >= m) continue;
+#pragma unroll 1
+        for (int j = 0; j < m; ++j) {
             const float scale = block_scale(
                 max(max(s.peak[0][j], s.peak[1][j]), max(s.peak[2][j], s.peak[3][j])));
             const uint32_t code =
-                scale == 0.0f ? 0u : code4(acc[0][j], 0.0f, 0.0f, 0.0f, scale);
+                scale == 0.0f ? 0u : code4(own[j * 128], 0.0f, 0.0f, 0.0f, scale);
             p.h_q[row_of(j) * I + blk * 128 + tid] = (uint8_t)code;
             if (tid == 0) p.h_s[row_of(j) * (I >> 7) + blk] = scale;
         }
