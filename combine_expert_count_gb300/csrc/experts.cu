@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int issued = 0;  // k blocks whose loads are under way (TMA warp)
     if (warp >= kSumWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kTmaWarp && lane == 0) {
+        const uint32_t one = elect_one();  // the lane that loads, and that issues products
+        if (warp == kTmaWarp) {
             bool ok = true;
             for (int t = worker; ok && t < tiles; t += workers) {
                 const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     if (issued >= kStages &&
                         !(ok = wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop)))
                         break;
+                    if (!one) continue;
                     uint8_t *a = stages + st * kStageBytes, *w = a + kTileRows * kBlk;
                     if constexpr (kPair) {
                         const uint32_t bar = dsmem_addr(&s.full[st], 0);
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
             }
         }
-        if (warp == kMmaWarp && lane == 0 && rank == 0) {
+        if (warp == kMmaWarp && rank == 0) {
             bool ok = true;
             int it = 0;
             for (int t = worker; ok && t < tiles; t += workers) {
@@ -290,16 +292,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < kBlk / 32; ++kk) {  // 32 bytes along k: 2 address units
                         if constexpr (kPair)
-                            tc_mma_pair(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0);
+                            tc_mma_pair(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0, one);
                         else
-                            tc_mma(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0);
+                            tc_mma(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0, one);
                     }
                     if constexpr (kPair) {
-                        tc_commit_pair(&s.empty[st]);
-                        tc_commit_pair(&s.tfull[ac]);
+                        tc_commit_pair(&s.empty[st], one);
+                        tc_commit_pair(&s.tfull[ac], one);
                     } else {
-                        tc_commit(&s.empty[st]);
-                        tc_commit(&s.tfull[ac]);
+                        tc_commit(&s.empty[st], one);
+                        tc_commit(&s.tfull[ac], one);
                     }
                 }
             }
@@ -468,11 +470,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
             }
         }
-        if (warp == kMmaWarp && lane == 0 && rank == 0) {
+        if (warp == kMmaWarp && rank == 0) {
+            const uint32_t one = elect_one();
             if constexpr (kPair)
-                tc_commit_pair(&s.drain);
+                tc_commit_pair(&s.drain, one);
             else
-                tc_commit(&s.drain);
+                tc_commit(&s.drain, one);
             mbar_wait(&s.drain, 0);
         }
         if constexpr (kPair)

@@ -95,14 +95,29 @@ __host__ __device__ constexpr uint32_t tc_e4m3_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// d (+)= a b^T over 32 elements of k, issued by one thread.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool accumulate) {
+// 1 in one lane of the (whole) warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(one));
+    return one;
+}
+
+// d (+)= a b^T over 32 elements of k, issued where `on`.  The whole warp comes
+// here with `on` in one lane: a branch around the instruction would keep its
+// operands out of the uniform registers, and four products with their waits and
+// commits then take the warp 485 cycles to issue, not 239.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
         : "memory");
 }
 
@@ -110,21 +125,24 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 // the even one.  a: each CTA's own 128 rows (M = 256); b: each CTA's half of the
 // N rows; d: each CTA's rows by all N columns, at the same tensor-memory address.
 __device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate) {
+                                            bool accumulate, uint32_t on) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
         : "memory");
 }
 
 // The barrier at this place in both CTAs gets an arrival.
-__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar, uint32_t on) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(smem_addr(bar)),
-        "h"((uint16_t)3)
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster."
+        "b64 [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+        "h"((uint16_t)3), "r"(on)
         : "memory");
 }
 
@@ -171,11 +189,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     return false;
 }
 
-// `bar` gets one arrival once the thread's products so far are done.
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+// `bar` gets one arrival once the thread's products so far are done (where `on`).
+__device__ __forceinline__ void tc_commit(uint64_t *bar, uint32_t on) {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_addr(bar))
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_addr(bar)),
+        "r"(on)
         : "memory");
 }
 

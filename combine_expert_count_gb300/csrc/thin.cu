@@ -304,13 +304,15 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         for (int j = 0; j < NMAX; ++j) acc[h][j] = 0.0f;
 
     if (warp == kThinTma) {
-        if (lane == 0) {
+        const uint32_t one = elect_one();
+        {
             for (int item = i0; item < i1; ++item, ++issued) {
                 const int u = kMode == Thin::kDown ? item / Kb : 0, b = item - u * Kb;
                 const int ex = kMode == Thin::kDown ? experts[u] : e, st = issued % kStages;
                 if (issued >= kStages &&
                     !wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop))
                     break;
+                if (!one) continue;
                 uint8_t *w = ring + st * kBytes;
                 mbar_arrive_expect_tx(&s.full[st], kHalves * kTileBytes);
                 tma_tile(w, &map_w, b * 128, ex * p.n + blk * 128, &s.full[st]);
@@ -320,7 +322,8 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             }
         }
     } else if (warp == kThinMma) {
-        if (lane == 0) {
+        const uint32_t one = elect_one();
+        {
             int it = 0;
             for (int item = i0; item < i1; ++item, ++it) {
                 const int st = it % kStages, ac = it % kAccs;
@@ -339,9 +342,9 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h)
                         tc_mma(tmem + (ac * kHalves + h) * NMAX,
-                               wd + h * (kTileBytes >> 4) + kk * 2, rows + kk * 2, idesc, kk > 0);
-                tc_commit(&s.empty[st]);
-                tc_commit(&s.tfull[ac]);
+                               wd + h * (kTileBytes >> 4) + kk * 2, rows + kk * 2, idesc, kk > 0, one);
+                tc_commit(&s.empty[st], one);
+                tc_commit(&s.tfull[ac], one);
             }
         }
     } else if (warp >= kRowWarp) {
@@ -502,8 +505,8 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         if (warp == kThinTma && lane == 0)
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
-        if (warp == kThinMma && lane == 0) {
-            tc_commit(&s.drain);
+        if (warp == kThinMma) {
+            tc_commit(&s.drain, elect_one());
             mbar_wait(&s.drain, 0);
         }
         if (tid == 0 && p.status) flag(p.status, MOE_ST_TIMEOUT);
