@@ -72,7 +72,7 @@ cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
 
 extern "C" {
 
-int moe_version(void) { return (1 << 16) | 0; }
+int moe_version(void) { return (1 << 16) | 1; }
 
 const char *moe_strerror(int code) {
     switch (code) {

@@ -16,8 +16,6 @@
 // power-of-two scales by themselves.  A thread holds one row, so its row's
 // scale is one number for all its columns and the gate, the up value and half
 // of the block maximum of an activation meet in one thread.
-#include <cooperative_groups.h>
-
 #include "bf16.cuh"
 #include "check.h"
 #include "coding.cuh"
@@ -30,25 +28,24 @@
 
 namespace moe {
 
-namespace cg = cooperative_groups;
-
 constexpr int kTileRows = 128;               // rows of a tile: the lanes of tensor memory
 constexpr int kBlk = 128;                    // k block, scale block, half of a tile's columns
 constexpr int kBoxRows = 32;                 // rows of one TMA load of a: a group's last tile
                                              // loads no more than it has, rounded up to 32
-constexpr int kWBoxRows = 64;                // rows of one TMA load of weights
-// A stage: the CTA's rows of a and its weight rows, both blocks of 128 where it
-// works alone, half of them in a pair.
-__host__ __device__ constexpr int stage_count(bool pair) { return pair ? 6 : 4; }
-__host__ __device__ constexpr int stage_bytes(bool pair) { return (pair ? 2 : 3) * kTileRows * kBlk; }
-constexpr int kStageRing = 4 * stage_bytes(false);
-static_assert(kStageRing == 6 * stage_bytes(true), "one size of shared memory");
+constexpr int kStages = 4;
+constexpr int kStageBytes = 3 * kTileRows * kBlk;  // a, first and second weight block
 constexpr int kSumWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kScaleWarps = 2;
 // Twelve warps are launched with 168 registers a thread; the sum warps, which
-// hold 128 sums each thread, then take 232 and the others keep 40: the same
-// total, 384 * 168 = 256 * 232 + 128 * 40.
+// hold 128 sums each thread, then take more and the others keep less, 384 * 168
+// in all at most.  Which split compiles to the better loop was measured: without
+// the activation 232 and 40 (dense 8191 x 7168 x 7168 308 us; 329 at 200 and 96,
+// 336 at 192 and 112), with it 200 and 96 (prefill 777 us; 795 at 208 and 88, 914
+// at 232 and 40, where the loops of the other warps spill).
+__host__ __device__ constexpr int sum_regs(bool swiglu) { return swiglu ? 200 : 232; }
+__host__ __device__ constexpr int other_regs(bool swiglu) { return swiglu ? 96 : 40; }
+static_assert(256 * sum_regs(true) + 128 * other_regs(true) <= 384 * 168, "registers at launch");
+static_assert(256 * sum_regs(false) + 128 * other_regs(false) <= 384 * 168, "registers at launch");
 constexpr int kProductThreads = 32 * 12;
-constexpr int kSumRegs = 200, kOtherRegs = 96;
 constexpr int kStageOut = 32 * 64;           // a sum warp's output staging: 32 rows of 64 bytes
 
 // Two warps bring the scales of runs of four k blocks to shared memory, two runs
@@ -58,7 +55,6 @@ constexpr int kScaleRun = 4;
 
 struct Product {
     int N, E, cap, n, k;
-    double rows;  // of an expert, estimated
     const float *a_s;
     const int32_t *grp_off;
     const float *w_s;
@@ -78,7 +74,7 @@ __device__ __forceinline__ int2 group_rows(const Product &p, int e) {
 }
 
 struct Tile {
-    int e, rows;      // expert; rows of the tile, 1 .. 128 (256 in a pair)
+    int e, rows;      // expert; rows of the tile, 1 .. 128
     long long row0;   // first row, over all ranks
     int blk0, blk1;   // column blocks of 128; blk1 < 0: there is none
 };
@@ -86,7 +82,7 @@ struct Tile {
 // Shared memory behind the stages and the output staging.
 struct alignas(16) ProductShared {
     float rscale[2][kScaleRun][kTileRows], wscale[2][kScaleRun][2];
-    uint64_t full[6], empty[6], tfull[2], tempty[2], sfull[2], sempty[2], drain;
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], sfull[2], sempty[2], drain;
     uint32_t tmem;
     int stop, total;
     int wsum[32];
@@ -95,14 +91,14 @@ struct alignas(16) ProductShared {
 };
 
 constexpr size_t kProductSmem =
-    1024 + (size_t)kStageRing + (size_t)kSumWarps * kStageOut + sizeof(ProductShared);
+    1024 + (size_t)kStages * kStageBytes + (size_t)kSumWarps * kStageOut + sizeof(ProductShared);
 static_assert(kProductSmem <= 232448, "a CTA's shared memory");
 
 // Tiles run row tile first within runs of kRun row tiles, so that the CTAs at
 // work at one time share weights and rows in L2.
 constexpr int kRun = 16;
 
-template <bool kSwiglu, int kRows>
+template <bool kSwiglu>
 __device__ __forceinline__ Tile tile_at(const Product &p, const int *first, int ntn, int t) {
     int lo = 0, hi = p.E;  // first[lo] * ntn <= t < first[hi] * ntn
     while (hi - lo > 1) {
@@ -118,8 +114,8 @@ __device__ __forceinline__ Tile tile_at(const Product &p, const int *first, int 
     const int2 g = group_rows(p, lo);
     Tile tile;
     tile.e = lo;
-    tile.rows = min(kRows, g.y - mi * kRows);
-    tile.row0 = (long long)(lo / (p.E / p.N)) * p.cap + g.x + mi * kRows;
+    tile.rows = min(kTileRows, g.y - mi * kTileRows);
+    tile.row0 = (long long)(lo / (p.E / p.N)) * p.cap + g.x + mi * kTileRows;
     const int nb = p.n >> 7;
     if (kSwiglu) {
         tile.blk0 = ni;
@@ -152,34 +148,24 @@ __device__ __forceinline__ void store_rows64(uint8_t *stage, const uint32_t (&v)
     }
 }
 
-// kPair: two CTAs of a cluster share a tile of 256 rows.  Each loads its 128 rows
-// and one of the two weight blocks, and the tensor cores of both read both: half
-// the weight bytes through L2, the port of the SM and its shared memory.  The
-// even CTA issues the products of both and holds the barriers that it waits on;
-// each CTA loads its own stages and sums its own rows.
-template <bool kSwiglu, bool kPair>
+template <bool kSwiglu>
 __global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const Product p, const __grid_constant__ CUtensorMap map_a,
               const __grid_constant__ CUtensorMap map_w) {
-    constexpr int kStages = stage_count(kPair), kStageBytes = stage_bytes(kPair);
-    constexpr int kRows = kPair ? 2 * kTileRows : kTileRows;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *stages = smem_raw + align1024(smem_raw);
-    uint8_t *staging = stages + kStageRing;
+    uint8_t *staging = stages + kStages * kStageBytes;
     ProductShared &s = *reinterpret_cast<ProductShared *>(staging + kSumWarps * kStageOut);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
-    const int worker = kPair ? blockIdx.x >> 1 : blockIdx.x;
-    const int workers = kPair ? gridDim.x >> 1 : gridDim.x;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s.full[i], kPair ? 2 : 1);
+            mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], kPair ? 2 * kSumWarps : kSumWarps);
+            mbar_init(&s.tempty[i], kSumWarps);
             mbar_init(&s.sfull[i], kScaleWarps * 32);
             mbar_init(&s.sempty[i], kSumWarps);
         }
@@ -188,7 +174,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         s.first[0] = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tc_alloc<512, kPair>(&s.tmem);
+    if (warp == kMmaWarp) tc_alloc<512>(&s.tmem);
     if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_w);
@@ -201,17 +187,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     int before = 0;
     for (int e0 = 0; e0 < p.E; e0 += kProductThreads) {
         const int e = e0 + tid;
-        const int mt = e < p.E ? (group_rows(p, e).y + kRows - 1) / kRows : 0;
+        const int mt = e < p.E ? (group_rows(p, e).y + kTileRows - 1) / kTileRows : 0;
         const int upto = block_inclusive_scan(mt, s.wsum, &s.total);
         if (e < p.E) s.first[e + 1] = before + upto;
         before += s.total;
         __syncthreads();
     }
     tc_fence_before();
-    if constexpr (kPair)
-        cg::this_cluster().sync();  // both CTAs' barriers are there
-    else
-        __syncthreads();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     volatile int *stop = &s.stop;
@@ -220,27 +203,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
     int issued = 0;  // k blocks whose loads are under way (TMA warp)
     if (warp >= kSumWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(kSwiglu)));
         const uint32_t one = elect_one();  // the lane that loads, and that issues products
         if (warp == kTmaWarp) {
             bool ok = true;
-            for (int t = worker; ok && t < tiles; t += workers) {
-                const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
-                const int rows = min(tile.rows - rank * kTileRows, kTileRows);
-                const int boxes = rows > 0 ? (rows + kBoxRows - 1) / kBoxRows : 0;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
+                const int boxes = (tile.rows + kBoxRows - 1) / kBoxRows;
                 const bool two = tile.blk1 >= 0;
-                // weight rows: alone one or two blocks; in a pair a block each,
-                // or half of the one block each
-                const int wboxes = kPair ? (two ? 2 : 1) : (two ? 4 : 2);
-                int w0 = tile.e * p.n, w1 = w0;
-                if (kPair) {
-                    w0 += two ? (rank ? tile.blk1 : tile.blk0) * kBlk : tile.blk0 * kBlk + rank * 64;
-                } else {
-                    w0 += tile.blk0 * kBlk;
-                    w1 += tile.blk1 * kBlk;
-                }
-                const uint32_t bytes = boxes * kBoxRows * kBlk + wboxes * kWBoxRows * kBlk;
-                const int arow = (int)tile.row0 + rank * kTileRows;
+                const uint32_t bytes = boxes * kBoxRows * kBlk + (two ? 2 : 1) * kBlk * kBlk;
+                const int w0 = tile.e * p.n + tile.blk0 * kBlk, w1 = tile.e * p.n + tile.blk1 * kBlk;
 #pragma unroll 1
                 for (int b = 0; b < Kb; ++b, ++issued) {
                     const int st = issued % kStages;
@@ -249,38 +221,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         break;
                     if (!one) continue;
                     uint8_t *a = stages + st * kStageBytes, *w = a + kTileRows * kBlk;
-                    if constexpr (kPair) {
-                        const uint32_t bar = dsmem_addr(&s.full[st], 0);
-                        mbar_arrive_expect_tx_cluster(bar, bytes);
+                    mbar_arrive_expect_tx(&s.full[st], bytes);
+                    tma_tile(w, &map_w, b * kBlk, w0, &s.full[st]);
+                    if (two) tma_tile(w + kBlk * kBlk, &map_w, b * kBlk, w1, &s.full[st]);
 #pragma unroll 1
-                        for (int i = 0; i < wboxes; ++i)
-                            tma_tile_pair(w + i * kWBoxRows * kBlk, &map_w, b * kBlk,
-                                          w0 + i * kWBoxRows, bar);
-#pragma unroll 1
-                        for (int i = 0; i < boxes; ++i)
-                            tma_tile_pair(a + i * kBoxRows * kBlk, &map_a, b * kBlk,
-                                          arow + i * kBoxRows, bar);
-                    } else {
-                        mbar_arrive_expect_tx(&s.full[st], bytes);
-#pragma unroll 1
-                        for (int i = 0; i < wboxes; ++i)
-                            tma_tile(w + i * kWBoxRows * kBlk, &map_w, b * kBlk,
-                                     (i < 2 ? w0 : w1) + (i & 1) * kWBoxRows, &s.full[st]);
-#pragma unroll 1
-                        for (int i = 0; i < boxes; ++i)
-                            tma_tile(a + i * kBoxRows * kBlk, &map_a, b * kBlk, arow + i * kBoxRows,
-                                     &s.full[st]);
-                    }
+                    for (int i = 0; i < boxes; ++i)
+                        tma_tile(a + i * kBoxRows * kBlk, &map_a, b * kBlk,
+                                 (int)tile.row0 + i * kBoxRows, &s.full[st]);
                 }
             }
         }
-        if (warp == kMmaWarp && rank == 0) {
+        if (warp == kMmaWarp) {
             bool ok = true;
             int it = 0;
-            for (int t = worker; ok && t < tiles; t += workers) {
-                const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
                 const uint32_t idesc =
-                    tile.blk1 >= 0 ? tc_e4m3_f32(kRows, 256) : tc_e4m3_f32(kRows, 128);
+                    tile.blk1 >= 0 ? tc_e4m3_f32(kTileRows, 256) : tc_e4m3_f32(kTileRows, 128);
 #pragma unroll 1
                 for (int b = 0; b < Kb; ++b, ++it) {
                     const int st = it % kStages, ac = it & 1;
@@ -290,19 +247,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     const uint64_t a = tc_operand(stages + st * kStageBytes);
                     const uint64_t w = tc_operand(stages + st * kStageBytes + kTileRows * kBlk);
 #pragma unroll
-                    for (int kk = 0; kk < kBlk / 32; ++kk) {  // 32 bytes along k: 2 address units
-                        if constexpr (kPair)
-                            tc_mma_pair(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0, one);
-                        else
-                            tc_mma(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0, one);
-                    }
-                    if constexpr (kPair) {
-                        tc_commit_pair(&s.empty[st], one);
-                        tc_commit_pair(&s.tfull[ac], one);
-                    } else {
-                        tc_commit(&s.empty[st], one);
-                        tc_commit(&s.tfull[ac], one);
-                    }
+                    for (int kk = 0; kk < kBlk / 32; ++kk)  // 32 bytes along k: 2 address units
+                        tc_mma(tmem + ac * 256, a + kk * 2, w + kk * 2, idesc, kk > 0, one);
+                    tc_commit(&s.empty[st], one);
+                    tc_commit(&s.tfull[ac], one);
                 }
             }
         }
@@ -311,11 +259,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             int run = 0;
             const int r = tid - kScaleWarp * 32;  // and r + 64; r < 8: a weight scale too
 #pragma unroll 1
-            for (int t = worker; ok && t < tiles; t += workers) {
-                const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
                 // rows past the group's last take its scale; they are not stored
-                const int r0 = min(rank * kTileRows + r, tile.rows - 1);
-                const int r1 = min(rank * kTileRows + r + 64, tile.rows - 1);
+                const int r0 = min(r, tile.rows - 1), r1 = min(r + 64, tile.rows - 1);
                 const float *as = p.a_s + (size_t)(tile.row0 + r0) * Kb;
                 const int more = (r1 - r0) * Kb;
                 const float *ws =
@@ -340,16 +287,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             copies_wait();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(sum_regs(kSwiglu)));
         const int quad = warp & 3, wg = warp >> 2;  // lanes 32 quad ..; columns 64 wg .. of each half
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + wg * 64;
         uint8_t *stage = staging + warp * kStageOut;
         bool ok = true;
         int it = 0, run = -1;
 #pragma unroll 1
-        for (int t = worker; ok && t < tiles; t += workers) {
-            const Tile tile = tile_at<kSwiglu, kRows>(p, s.first, ntn, t);
-            const int r = quad * 32 + lane, rr = rank * kTileRows + r;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
+            const int r = quad * 32 + lane;
             const bool two = tile.blk1 >= 0;
             uint64_t acc[2][32] = {};
 #pragma unroll 1
@@ -375,10 +322,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            if constexpr (kPair)
-                                mbar_arrive_cluster(dsmem_addr(&s.tempty[ac], 0));
-                            else
-                                mbar_arrive(&s.tempty[ac]);
+                            mbar_arrive(&s.tempty[ac]);
                             if (at == kScaleRun - 1 || b == Kb - 1) mbar_arrive(&s.sempty[run & 1]);
                         }
                     }
@@ -393,13 +337,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             // below are met by all
             ok = bar_named_all(1, kSumWarps * 32, ok);
             if (!ok) break;
-            const int rows = tile.rows - rank * kTileRows - quad * 32;  // of this warp
+            const int rows = tile.rows - quad * 32;  // of this warp
             if constexpr (!kSwiglu) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (h == 1 && !two) break;
                     const int blk = h ? tile.blk1 : tile.blk0;
-                    uint16_t *y = p.y + (size_t)(tile.row0 + rank * kTileRows + quad * 32) * p.n + blk * 128 + wg * 64;
+                    uint16_t *y = p.y + (size_t)(tile.row0 + quad * 32) * p.n + blk * 128 + wg * 64;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         uint32_t o[16];
@@ -441,57 +385,31 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
                 const int I = p.n >> 1;
                 store_rows64(stage, o,
-                             p.h_q + (size_t)(tile.row0 + rank * kTileRows + quad * 32) * I + tile.blk0 * 128 + wg * 64,
+                             p.h_q + (size_t)(tile.row0 + quad * 32) * I + tile.blk0 * 128 + wg * 64,
                              (size_t)I, rows);
                 if (wg == 0 && lane < rows)
-                    p.h_s[(size_t)(tile.row0 + rr) * (I >> 7) + tile.blk0] = scale;
+                    p.h_s[(size_t)(tile.row0 + r) * (I >> 7) + tile.blk0] = scale;
             }
         }
     }
     tc_fence_before();
-    bool gave_up;
-    if constexpr (kPair) {
-        cg::cluster_group cluster = cg::this_cluster();
-        cluster.sync();  // no arrival for a CTA that has gone
-        gave_up = *cluster.map_shared_rank(&s.stop, 0) || *cluster.map_shared_rank(&s.stop, 1);
-        cluster.sync();
-    } else {
-        __syncthreads();
-        gave_up = s.stop;
-    }
-    if (gave_up) {  // no copy and no product is left in flight
-        if (warp == kTmaWarp && lane == 0) {
-            if constexpr (kPair) {
-                // the even CTA's barriers count both CTAs' copies; give them
-                // a thousand times what a copy takes
-                for (int i = 0; i < 2000; ++i) __nanosleep(1000);
-            } else {
-                for (int i = max(0, issued - kStages); i < issued; ++i)
-                    mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
-            }
-        }
-        if (warp == kMmaWarp && rank == 0) {
-            const uint32_t one = elect_one();
-            if constexpr (kPair)
-                tc_commit_pair(&s.drain, one);
-            else
-                tc_commit(&s.drain, one);
+    __syncthreads();
+    if (s.stop) {  // a kernel that gave up leaves no copy and no product in flight
+        if (warp == kTmaWarp && lane == 0)
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
+        if (warp == kMmaWarp) {
+            tc_commit(&s.drain, elect_one());
             mbar_wait(&s.drain, 0);
         }
-        if constexpr (kPair)
-            cg::this_cluster().sync();
-        else
-            __syncthreads();
+        __syncthreads();
     }
     tc_fence_after();
-    if (warp == kMmaWarp) tc_free<512, kPair>(tmem);
-    if (tid == 0 && gave_up && p.status) flag(p.status, MOE_ST_TIMEOUT);
+    if (warp == kMmaWarp) tc_free<512>(tmem);
+    if (tid == 0 && s.stop && p.status) flag(p.status, MOE_ST_TIMEOUT);
 }
 
 // ------------------------------------------------------------ host
-
-// Rows of an expert from which two CTAs share a tile.
-constexpr double kPairRows = 192;
 
 static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const uint8_t *w_q,
                                   cudaStream_t st) {
@@ -500,39 +418,32 @@ static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const ui
                                    p.h_q, p.h_s, p.status, st);
     CUtensorMap map_a, map_w;
     cudaError_t err = tile_map(&map_a, a_q, (int64_t)p.N * p.cap, p.k, kBoxRows);
-    if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kWBoxRows);
+    if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kBlk);
     if (err != cudaSuccess) return err;
-    const bool swiglu = p.h_q != nullptr, pair = p.rows >= kPairRows;
-    const auto kern = swiglu ? (pair ? k_product<true, true> : k_product<true, false>)
-                             : (pair ? k_product<false, true> : k_product<false, false>);
+    const bool swiglu = p.h_q != nullptr;
+    const auto kern = swiglu ? k_product<true> : k_product<false>;
     static LaunchMemo memo;
     int done = 0;
-    err = memo.get(2 * swiglu + pair, &done, [&](int *v) {
+    err = memo.get(swiglu, &done, [&](int *v) {
         *v = 1;
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kProductSmem);
     });
     if (err != cudaSuccess) return err;
-    // as many workers as there can be tiles: every expert's last may be part full
+    // as many CTAs as there can be tiles: every expert's last may be part full
     const int64_t nb = p.n >> 7, ntn = swiglu ? nb >> 1 : (nb + 1) >> 1;
-    const int64_t rows = (int64_t)p.N * p.cap, each = pair ? 2 * kTileRows : kTileRows;
-    const int64_t most = (rows / each + (rows < p.E ? rows : p.E)) * ntn;
-    const int workers = pair ? sm_count() / 2 : sm_count();
-    const int grid = (int)(most < workers ? most : workers) * (pair ? 2 : 1);
+    const int64_t rows = (int64_t)p.N * p.cap;
+    const int64_t most = (rows / kTileRows + (rows < p.E ? rows : p.E)) * ntn;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = pair ? 2 : 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(grid);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(most < sm_count() ? most : sm_count()));
     cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = kProductSmem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p, map_a, map_w);
 }
 
@@ -550,10 +461,8 @@ static int check_product(const moe_shape *sh, int64_t n, int k, const uint8_t *a
         !ok_optional(status))
         return MOE_EINVAL;
     if (!grp_off && sh->E != sh->N) return MOE_EINVAL;
-    const double sent = (double)sh->N * sh->T * sh->R;
-    *p = Product{sh->N,   sh->E, (int)z.cap, (int)n,  k,       (sent < rows ? sent : rows) / sh->E,
-                 a_s,     grp_off, w_s,      nullptr, nullptr, nullptr,
-                 status};
+    *p = Product{sh->N, sh->E, (int)z.cap, (int)n, k,       a_s,
+                 grp_off, w_s, nullptr,    nullptr, nullptr, status};
     return MOE_OK;
 }
 

@@ -121,54 +121,8 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
-// The pair forms: the products of two CTAs of a cluster on one tile, issued by
-// the even one.  a: each CTA's own 128 rows (M = 256); b: each CTA's half of the
-// N rows; d: each CTA's rows by all N columns, at the same tensor-memory address.
-__device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "setp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
-        : "memory");
-}
-
-// The barrier at this place in both CTAs gets an arrival.
-__device__ __forceinline__ void tc_commit_pair(uint64_t *bar, uint32_t on) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster."
-        "b64 [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
-        "h"((uint16_t)3), "r"(on)
-        : "memory");
-}
-
-// tma_tile whose bytes are counted on the even CTA's barrier (a cluster address).
-__device__ __forceinline__ void tma_tile_pair(void *dst, const CUtensorMap *map, int x, int y,
-                                              uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-        "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-// Arrivals on a barrier of the cluster, its address from dsmem_addr.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
-}
-
-// The same that orders this thread's stores to the cluster before it, and the
-// bounded wait (as mbar_wait) that orders what follows after such arrivals.
+// An arrival on a barrier of the cluster (its address from dsmem_addr) that orders
+// this thread's stores to the cluster before it, and the bounded wait (as mbar_wait) that orders what follows after such arrivals.
 __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
@@ -209,28 +163,17 @@ __device__ __forceinline__ void tc_fence_after() {
 
 // kCols columns of the SM's tensor memory (a power of two from 32 to 512); one
 // warp allocates and frees.
-template <int kCols, bool kPair = false>
+template <int kCols>
 __device__ __forceinline__ void tc_alloc(uint32_t *where) {
-    if constexpr (kPair) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(where)),
-                     "n"(kCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    } else {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(where)),
-                     "n"(kCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(where)),
+                 "n"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
-template <int kCols, bool kPair = false>
+template <int kCols>
 __device__ __forceinline__ void tc_free(uint32_t taddr) {
-    if constexpr (kPair)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
-    else
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
 }
 
 // 32 columns of the warp's 32 lanes, one lane's row a thread.  The values
