@@ -14,7 +14,9 @@ a function without the built library raises.
 ``MoeBuffers`` owns one set of device buffers for a shape (PyTorch is the
 allocator) and strings the calls together for callers who want the whole
 path:  ``dispatch`` = moe_dispatch (or route_count, exchange, dispatch_send,
-dispatch_recv);  ``combine`` = moe_combine (or combine_send, combine_recv).
+dispatch_recv);  ``experts`` = moe_expert_gemm_swiglu, moe_expert_gemm;
+``combine`` = moe_combine (or combine_send, combine_recv).  ``moe_rmsnorm``
+makes x before it, and ``moe_layer_few`` is the whole of it for a few tokens.
 """
 from __future__ import annotations
 
@@ -31,6 +33,7 @@ _lib = None
 
 MOE_OK, MOE_EINVAL, MOE_ENOTSUP, MOE_ECUDA = 0, -1, -2, -3
 MOE_ST_BAD_EXPERT, MOE_ST_CAPACITY, MOE_ST_TIMEOUT = 1, 2, 4
+MOE_FEW_MAX_TOKENS = 64
 
 EXPORTS = ("moe_sizes_query", "moe_route_count", "moe_exchange", "moe_route", "moe_dispatch_send",
            "moe_dispatch_recv", "moe_combine_send", "moe_combine_recv", "moe_dispatch",
@@ -650,6 +653,21 @@ class MoeBuffers:
     def expert(self, mode: int = 0, stream=None) -> None:
         """The grouped-GEMM stand-in (identity or per-expert scale)."""
         moe_expert_standin(self.shape, mode, self.grp_q, self.grp_s, self.grp_off, self.y, stream)
+
+    def experts(self, w13_q, w13_s, w2_q, w2_s, stream=None) -> None:
+        """The experts between ``dispatch`` and ``combine``: moe_expert_gemm_swiglu
+        of the grouped rows and moe_expert_gemm into ``y``.  The weights are
+        [E][2*inter][H] and [E][H][inter] e4m3 with their 128 x 128 block scales;
+        the coded activations (``h_q``, ``h_s``) are allocated on first use."""
+        inter = w2_q.shape[-1]
+        if getattr(self, "h_q", None) is None or self.h_q.shape[-1] != inter:
+            rows, d = (self.N, self.cap), self.y.device
+            self.h_q = torch.empty((*rows, inter), dtype=torch.uint8, device=d)
+            self.h_s = torch.empty((*rows, inter // 128), dtype=torch.float32, device=d)
+        moe_expert_gemm_swiglu(self.shape, inter, self.H, self.grp_q, self.grp_s, self.grp_off,
+                               w13_q, w13_s, self.h_q, self.h_s, self.status, stream)
+        moe_expert_gemm(self.shape, self.H, inter, self.h_q, self.h_s, self.grp_off, w2_q, w2_s,
+                        self.y, self.status, stream)
 
     def combine(self, topk_idx, topk_w, y=None, out=None, stream=None,
                 calls: str = "fused") -> torch.Tensor:

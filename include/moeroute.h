@@ -444,7 +444,9 @@ int moe_combine_ll(const moe_shape *shape, const uint16_t *y_ll, const float *to
  *   res_out = bf16_rn(v)                the residual stream after the addition
  *   y       = bf16_rn((v * rstd) * gamma),  rstd = 1 / sqrt(mean(v^2) + eps)
  *   s, q    = the dispatch's block-128 coding (moe_dispatch_send) of the fp32
- *             values (v * rstd) * gamma: one rounding, not that of y again
+ *             values (v * rstd) * gamma: one rounding, not that of y again; the
+ *             values are multiplied by 1 / s.  A NaN in a block makes its scale
+ *             and its codes NaN
  * gamma is bf16 [H].  Sums are fp32.  res, res_out, y and the pair (q, s) may
  * each be NULL; q and s go together, and at least one output is needed.  y is
  * the x of moe_dispatch; (q, s) feed a product with 8-bit rows directly (a
@@ -469,10 +471,9 @@ int moe_rmsnorm(const moe_shape *shape, float eps, const uint16_t *x_bf16,
  * along k is summed in fp32 by the tensor cores and added, times its two
  * scales, to an fp32 sum over the blocks:
  *   p[i][c] = sum_b (a_s[i][b] * w_s[e][c/128][b]) * sum_{kk in b} a_q[i][kk] * w_q[e][c][kk]
- * Only N, E and cap of the shape decide what is computed (T and R, with which
- * the rows of an expert are estimated, only how).  status may be NULL; a
- * kernel whose bounded waits run out sets MOE_ST_TIMEOUT there (it is not
- * cleared) and leaves outputs unwritten. */
+ * Only N, E and cap of the shape matter here (the others are checked).  status
+ * may be NULL; a kernel whose bounded waits run out sets MOE_ST_TIMEOUT there
+ * (it is not cleared) and leaves outputs unwritten. */
 
 /* y[i][c] = bf16_rn(p[i][c]).
  *   a_q u8 [N][cap][k], a_s float [N][cap][k/128], y bf16 [N][cap][n] */
@@ -483,7 +484,8 @@ int moe_expert_gemm(const moe_shape *shape, int n, int k, const uint8_t *a_q, co
 /* The gate and up product with the activation and the coding of its result:
  * the weights' first `inter` outputs are the gate g, the next `inter` the up u
  * (n = 2 * inter),
- *   h = (g / (1 + exp(-g))) * u   fp32, then the dispatch's block-128 coding:
+ *   h = (g / (1 + exp(-g))) * u   fp32, then the block-128 coding, as
+ *   moe_rmsnorm's:
  *   h_q u8 [N][cap][inter], h_s float [N][cap][inter/128]
  * the row operand of the second moe_expert_gemm. */
 int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8_t *a_q,
@@ -496,7 +498,7 @@ int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8
  * dispatch or combine: only the weights of the experts that some token chose
  * are read, once.  Per token t of rank s, with the coding and the products
  * defined above:
- *   xq      = coding of x[s][t]                      (as moe_dispatch)
+ *   xq      = coding of x[s][t]      (moe_dispatch's, but a NaN spreads as above)
  *   h_k     = coding of silu(g) * u, [g; u] = w13[e_k] xq   (as ..._swiglu)
  *   out     = bf16_rn(sum_k topk_w[s][t][k] * (w2[e_k] h_k))
  * The same steps as moe_dispatch, moe_expert_gemm_swiglu, moe_expert_gemm and
@@ -506,7 +508,10 @@ int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8
  *   w13_q u8 [E][2*inter][H], w13_s float [E][2*inter/128][H/128]
  *   w2_q  u8 [E][H][inter],   w2_s  float [E][H/128][inter/128]
  *   h_q u8 [N][T][R][inter], h_s float [N][T][R][inter/128]: scratch that the
- *     call writes before it reads (rows of skipped ids stay untouched) */
+ *     call writes before it reads (rows of skipped ids stay untouched, and those
+ *     of an id that an earlier slot of the token has: its weights are added)
+ * x may be pinned host memory, but every expert's CTAs read their tokens' rows
+ * again over the link; out may not. */
 #define MOE_FEW_MAX_TOKENS 64
 int moe_layer_few(const moe_shape *shape, int inter, const uint16_t *x_bf16,
                   const int32_t *topk_idx, const float *topk_w, const uint8_t *w13_q,
