@@ -8,14 +8,30 @@
 // two column blocks of 128 (two neighbours of the plain product; the gate
 // block and the up block of the same activations of the other).  One warp
 // loads the operands' 128-byte-wide k blocks by TMA into a ring of four
-// stages; one thread issues the tcgen05 products of a block into one of two
+// stages; one issues the tcgen05 products of a block into one of two
 // 256-column accumulators in tensor memory; eight warps take each finished
 // block out of there and add it, times its two scales, to fp32 sums that stay
-// in registers over the whole of k.  The fp32 scales of a block are why the
-// sums leave tensor memory at every block: the tensor cores can only apply
-// power-of-two scales by themselves.  A thread holds one row, so its row's
-// scale is one number for all its columns and the gate, the up value and half
-// of the block maximum of an activation meet in one thread.
+// in registers over the whole of k; two bring the scales.  The fp32 scales of
+// a block are why the sums leave tensor memory at every block: the tensor cores
+// can only apply power-of-two scales by themselves.  A thread holds one row, so
+// its row's scale is one number for all its columns, and the gate, the up value
+// and half of the block maximum of an activation meet in one thread.
+//
+// What bounds it.  A decode batch: HBM, each weight being read once (32 experts of
+// 7168 x 2048 with 64 rows each 81 us, 6.2 TB/s; gate/up of 2048 by 7168 157 us, 6.1
+// TB/s).  Many rows: taking the sums out.  A k block is 512 cycles of products
+// and about 620 of the sum warps' (128 x 256 fused multiply-adds are 256 of every
+// SM's fp32 lanes; the rest is the way out of tensor memory and two barriers);
+// 8191 x 7168 x 7168 takes 308 to 330 us (2.55 to 2.73 PFLOP/s, a bf16 product's
+// measured rate being 1.89), the uneven prefill gate/up about 800 us (2.4).
+// What did not help: two CTAs on one 256-row tile with the weights halved
+// between them (their hand-over costs what the loads save), sixteen sum warps,
+// 32 columns at a time (registers), longer scale runs in registers.  What did:
+// the products' operands in uniform registers, shared memory addressed as
+// such, no cluster-scope release on a barrier of every block, no exact
+// division in the epilogue (its straight-line code cost more than a short k).
+#include <cooperative_groups.h>
+
 #include "bf16.cuh"
 #include "check.h"
 #include "coding.cuh"
@@ -27,6 +43,8 @@
 #include "trace.h"
 
 namespace moe {
+
+namespace cg = cooperative_groups;
 
 constexpr int kTileRows = 128;               // rows of a tile: the lanes of tensor memory
 constexpr int kBlk = 128;                    // k block, scale block, half of a tile's columns
@@ -55,6 +73,7 @@ constexpr int kScaleRun = 4;
 
 struct Product {
     int N, E, cap, n, k;
+    int wide;  // column blocks of a tile (1 or 2)
     const float *a_s;
     const int32_t *grp_off;
     const float *w_s;
@@ -121,8 +140,8 @@ __device__ __forceinline__ Tile tile_at(const Product &p, const int *first, int 
         tile.blk0 = ni;
         tile.blk1 = ni + (nb >> 1);
     } else {
-        tile.blk0 = 2 * ni;
-        tile.blk1 = 2 * ni + 1 < nb ? 2 * ni + 1 : -1;
+        tile.blk0 = p.wide * ni;
+        tile.blk1 = p.wide == 2 && 2 * ni + 1 < nb ? 2 * ni + 1 : -1;
     }
     return tile;
 }
@@ -148,7 +167,9 @@ __device__ __forceinline__ void store_rows64(uint8_t *stage, const uint32_t (&v)
     }
 }
 
-template <bool kSwiglu>
+// kSplit, for few tiles: the two CTAs of a cluster share one tile, each with half
+// of k; then each adds the other's sums for half of the rows and stores those.
+template <bool kSwiglu, bool kSplit>
 __global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const Product p, const __grid_constant__ CUtensorMap map_a,
               const __grid_constant__ CUtensorMap map_w) {
@@ -198,8 +219,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     volatile int *stop = &s.stop;
-    const int nb = p.n >> 7, ntn = kSwiglu ? nb >> 1 : (nb + 1) >> 1;
+    const int nb = p.n >> 7, ntn = kSwiglu || p.wide == 2 ? (nb + 1) >> 1 : nb;
     const int tiles = before * ntn, Kb = p.k >> 7;
+    const int parts = kSplit ? gridDim.z : 1, part = kSplit ? blockIdx.z : 0;
+    const int kb0 = kSplit ? Kb * part / parts : 0, kb1 = kSplit ? Kb * (part + 1) / parts : Kb;
 
     int issued = 0;  // k blocks whose loads are under way (TMA warp)
     if (warp >= kSumWarps) {
@@ -214,7 +237,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const uint32_t bytes = boxes * kBoxRows * kBlk + (two ? 2 : 1) * kBlk * kBlk;
                 const int w0 = tile.e * p.n + tile.blk0 * kBlk, w1 = tile.e * p.n + tile.blk1 * kBlk;
 #pragma unroll 1
-                for (int b = 0; b < Kb; ++b, ++issued) {
+                for (int b = kb0; b < kb1; ++b, ++issued) {
                     const int st = issued % kStages;
                     if (issued >= kStages &&
                         !(ok = wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop)))
@@ -239,7 +262,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const uint32_t idesc =
                     tile.blk1 >= 0 ? tc_e4m3_f32(kTileRows, 256) : tc_e4m3_f32(kTileRows, 128);
 #pragma unroll 1
-                for (int b = 0; b < Kb; ++b, ++it) {
+                for (int b = kb0; b < kb1; ++b, ++it) {
                     const int st = it % kStages, ac = it & 1;
                     if (it >= 2 && !(ok = wait_or_stop(&s.tempty[ac], (it / 2 - 1) & 1, stop))) break;
                     if (!(ok = wait_or_stop(&s.full[st], (it / kStages) & 1, stop))) break;
@@ -268,7 +291,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 const float *ws =
                     p.w_s + ((size_t)tile.e * nb + ((r & 1) && tile.blk1 >= 0 ? tile.blk1 : tile.blk0)) * Kb;
 #pragma unroll 1
-                for (int b = 0; b < Kb; b += kScaleRun, ++run) {
+                for (int b = kb0; b < kb1; b += kScaleRun, ++run) {
                     const int buf = run & 1;
                     if (run >= 2)
                         ok = __all_sync(kFull, wait_or_stop(&s.sempty[buf], (run / 2 - 1) & 1, stop));
@@ -286,6 +309,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
             copies_wait();
         }
+        if constexpr (kSplit) {
+            __syncwarp();
+            if ((int)blockIdx.x < tiles) {  // the sum warps' two
+                cg::this_cluster().sync();
+                cg::this_cluster().sync();
+            }
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(sum_regs(kSwiglu)));
         const int quad = warp & 3, wg = warp >> 2;  // lanes 32 quad ..; columns 64 wg .. of each half
@@ -297,11 +327,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
             const Tile tile = tile_at<kSwiglu>(p, s.first, ntn, t);
             const int r = quad * 32 + lane;
-            const bool two = tile.blk1 >= 0;
+            const bool two = kSwiglu || tile.blk1 >= 0;
             uint64_t acc[2][32] = {};
 #pragma unroll 1
-            for (int b = 0; b < Kb; ++b, ++it) {
-                const int ac = it & 1, at = b % kScaleRun;
+            for (int b = kb0; b < kb1; ++b, ++it) {
+                const int ac = it & 1, at = (b - kb0) % kScaleRun;
                 if (at == 0) {
                     ++run;
                     ok = __all_sync(kFull, wait_or_stop(&s.sfull[run & 1], (run / 2) & 1, stop));
@@ -314,16 +344,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {  // 16 columns; a tile of one block ignores half
+                for (int c = 0; c < 8; ++c) {  // 16 columns
+                    if (c == 4 && !two) break;
                     uint32_t v[16];
                     tc_ld16(v, mine + ac * 256 + c / 4 * 128 + c % 4 * 16);
                     tc_wait_ld();
-                    if (c == 7) {  // all of it is in registers: the accumulator is free
+                    if (c == 7 || (c == 3 && !two)) {  // all of it is in registers: the accumulator is free
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(&s.tempty[ac]);
-                            if (at == kScaleRun - 1 || b == Kb - 1) mbar_arrive(&s.sempty[run & 1]);
+                            if (at == kScaleRun - 1 || b == kb1 - 1) mbar_arrive(&s.sempty[run & 1]);
                         }
                     }
                     const uint64_t ff = pack2(__float_as_uint(f[c / 4]), __float_as_uint(f[c / 4]));
@@ -336,6 +367,31 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             // either every sum warp has its sums or none goes on: the barriers
             // below are met by all
             ok = bar_named_all(1, kSumWarps * 32, ok);
+            if constexpr (kSplit) {
+                // the stages are free: [warp][column][lane]
+                cg::cluster_group cluster = cg::this_cluster();
+                float *left = reinterpret_cast<float *>(stages) + warp * 128 * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    const float2 f = unpack2(acc[i / 32][i % 32]);
+                    left[2 * i * 32] = f.x;
+                    left[(2 * i + 1) * 32] = f.y;
+                }
+                cluster.sync();
+                const bool mine = quad * parts / 4 == part;
+                for (int q = 0; mine && q < parts; ++q) {
+                    if (q == part) continue;
+                    const float *o = cluster.map_shared_rank(left, q);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        const float2 f = unpack2(acc[i / 32][i % 32]);
+                        acc[i / 32][i % 32] = pack2(__float_as_uint(f.x + o[2 * i * 32]),
+                                                    __float_as_uint(f.y + o[(2 * i + 1) * 32]));
+                    }
+                }
+                cluster.sync();  // no CTA goes while it is read
+                if (!mine) break;
+            }
             if (!ok) break;
             const int rows = tile.rows - quad * 32;  // of this warp
             if constexpr (!kSwiglu) {
@@ -367,9 +423,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
                 // the other 64 columns of the row's block are the other group's
                 s.peak[wg][r] = am;
-                bar_named(1, kSumWarps * 32);
+                bar_named(2 + quad, 64);  // the two warps of these rows
                 const float scale = block_scale(max(s.peak[0][r], s.peak[1][r]));
-                bar_named(1, kSumWarps * 32);
+                bar_named(2 + quad, 64);
                 float inv = __frcp_rn(scale);
                 if (scale < kTinyScale) {
                     const uint64_t up = pack2(__float_as_uint(kTinyUp), __float_as_uint(kTinyUp));
@@ -411,7 +467,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
 // ------------------------------------------------------------ host
 
-static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const uint8_t *w_q,
+// Whether two CTAs share each tile: where an SM each is left for them and k is
+// long.  us with one and two: gate/up of 2048 by 7168, 128 rows, 27.4 and 20.5; 7168
+// x 7168 (narrow tiles) 22.5 and 19.3; k = 4096 14.4 and 13.7; k = 2048 12.0 and
+// 12.3; k = 1024 8.3 and 10.0.  Four: 19.2, 22.6 (wide), 14.0, 15.1, 10.0.
+static int product_parts(int64_t tiles, int blocks) {
+    return tiles * 2 <= sm_count() && blocks >= 32 ? 2 : 1;
+}
+
+static cudaError_t launch_product(Product p, const uint8_t *a_q, const uint8_t *w_q,
                                   cudaStream_t st) {
     if ((int64_t)p.N * p.cap <= kThinRows)
         return launch_thin_product(p.N, p.E, p.cap, p.n, p.k, a_q, p.a_s, p.grp_off, w_q, p.w_s, p.y,
@@ -421,29 +485,40 @@ static cudaError_t launch_product(const Product &p, const uint8_t *a_q, const ui
     if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kBlk);
     if (err != cudaSuccess) return err;
     const bool swiglu = p.h_q != nullptr;
-    const auto kern = swiglu ? k_product<true> : k_product<false>;
+    // as many tiles as there can be: every expert's last may be part full
+    const int64_t nb = p.n >> 7, rows = (int64_t)p.N * p.cap, used = rows < p.E ? rows : p.E;
+    const int64_t row_tiles = (rows - used) / kTileRows + used;
+    // one column block a tile where even those have an SM each: half the sums of a k
+    // block, and its bound where an SM has one tile (7168 x 2048 at 128 rows 9.6 us,
+    // 12.3 with two; 7168 x 7168 22.6, 29.5; 512 x 1024 6.9, 8.6; with up to twice
+    // the SMs' tiles 16.5, 13.1 and 40, 30.4 at 512 rows)
+    p.wide = swiglu || row_tiles * nb > sm_count() ? 2 : 1;
+    const int64_t most = row_tiles * ((nb + p.wide - 1) / p.wide);
+    const int parts = product_parts(most, p.k >> 7);
+    const auto kern = swiglu ? (parts > 1 ? k_product<true, true> : k_product<true, false>)
+                             : (parts > 1 ? k_product<false, true> : k_product<false, false>);
     static LaunchMemo memo;
     int done = 0;
-    err = memo.get(swiglu, &done, [&](int *v) {
+    err = memo.get(2 * swiglu + (parts > 1), &done, [&](int *v) {
         *v = 1;
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kProductSmem);
     });
     if (err != cudaSuccess) return err;
-    // as many CTAs as there can be tiles: every expert's last may be part full
-    const int64_t nb = p.n >> 7, ntn = swiglu ? nb >> 1 : (nb + 1) >> 1;
-    const int64_t rows = (int64_t)p.N * p.cap;
-    const int64_t most = (rows / kTileRows + (rows < p.E ? rows : p.E)) * ntn;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(most < sm_count() ? most : sm_count()));
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = (unsigned)parts;
+    cfg.gridDim = dim3((unsigned)(most < sm_count() ? most : sm_count()), 1, (unsigned)parts);
     cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = kProductSmem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = parts > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p, map_a, map_w);
 }
 
@@ -461,7 +536,7 @@ static int check_product(const moe_shape *sh, int64_t n, int k, const uint8_t *a
         !ok_optional(status))
         return MOE_EINVAL;
     if (!grp_off && sh->E != sh->N) return MOE_EINVAL;
-    *p = Product{sh->N, sh->E, (int)z.cap, (int)n, k,       a_s,
+    *p = Product{sh->N, sh->E, (int)z.cap, (int)n,  k,       2,     a_s,
                  grp_off, w_s, nullptr,    nullptr, nullptr, status};
     return MOE_OK;
 }

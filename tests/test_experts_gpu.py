@@ -227,3 +227,23 @@ def test_rows_past_32_bit_offsets():
         p, err = o.product64(q[rows], s[rows], w[0][e], w[1][e])
         o.assert_bf16(got, p, err)
     assert y[0, 2:].count_nonzero() == 0 and y[1, :-3].count_nonzero() == 0
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("M,n,k", [(20, 256, 4096), (129, 512, 4224), (300, 384, 4096),
+                                   (40, 2304, 8192)])
+def test_few_tiles_share_k(M, n, k, swiglu):
+    """Few tiles and a long k: two CTAs have half of k each."""
+    if swiglu and n % 256:
+        n += 128
+    gen = torch.Generator().manual_seed(M + n + k)
+    check(m.make_shape(1, M, 1, 1, 128, M), n, k, o.make_rows(gen, M, k), None,
+          o.make_weights(gen, 1, n, k), swiglu)
+
+
+def test_few_tiles_share_k_in_groups():
+    gen = torch.Generator().manual_seed(21)
+    sizes, n, k = [[3, 0, 70], [0, 131, 1]], 512, 4096
+    sh = m.make_shape(2, 140, 6, 1, 128, 140)
+    check(sh, n, k, o.make_rows(gen, 280, k), layout(sizes, 140), o.make_weights(gen, 6, n, k),
+          True)
