@@ -1,5 +1,5 @@
-// coding.cuh -- the block-128 e4m3 coding of fp32 values, as the dispatch
-// codes its rows: scale = amax / 448 (fp32 division), code = e4m3 round to
+// coding.cuh -- the experts' activation and the block-128 e4m3 coding of fp32
+// values, as the dispatch codes its rows: scale = amax / 448 (fp32 division), code = e4m3 round to
 // nearest even of v / scale (fp32 division), saturating; a block of zeros has
 // scale 0 and zero bytes.  A NaN makes its block's scale and codes NaN (the
 // dispatch leaves NaN out of amax, so a block of nothing but NaN is coded as
@@ -11,6 +11,13 @@
 #include "common.cuh"
 
 namespace moe {
+
+// silu(g) * u with the fast exponential and division (about (|g| + 4) 2^-23 of
+// the result off; the sums g and u come with more).  For g below -87 the
+// quotient is 0 where the formula has a value of magnitude 2^-119 or less.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
 
 // |v| as bits: their order as unsigned integers is that of the magnitudes,
 // with NaN above infinity, so an integer maximum finds amax and keeps NaN.

@@ -36,7 +36,6 @@
 #include "check.h"
 #include "coding.cuh"
 #include "launch.h"
-#include "mma8.cuh"
 #include "tc.cuh"
 #include "thin.h"
 #include "tilemap.h"

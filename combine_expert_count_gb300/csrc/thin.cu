@@ -8,18 +8,29 @@
 // 128 outputs of one expert (its gate and its up block; or one block over a run
 // of experts) and streams the weights' 16 KB tiles by TMA through a ring of
 // shared memory.  Four warps put the rows' 128-byte pieces beside them: coded
-// from x on the way, or copied from coded rows.  One thread issues the products
-// of a k block; four warps add it, times its scales, to fp32 sums.  Two CTAs
-// fit an SM, so one streams while the other starts or ends; together they keep
-// about 200 KB of weights on the way, and nothing but the ring's TMA copies has
-// to wait for HBM.  Weights are read with plain loads nowhere.
+// from x on the way, or copied from coded rows.  One warp issues the products
+// of a k block; four add it, times its scales, to fp32 sums.  Two CTAs fit an SM,
+// so one streams while the other starts or ends; together they keep about 200 KB
+// of weights on the way, and nothing but the ring's TMA copies waits for HBM.
+// Where there are fewer units than that, the CTAs of a cluster share each one's k
+// blocks (thin_parts).
+//
+// Measured, hidden 7168, experts of 2048, top-8: four tokens of 256 experts 206 to
+// 227 us (30 to 32 experts' weights, 6.0 TB/s), 32 tokens on 64 experts 447 us (6.2
+// TB/s, 92% of a copy's).  One token, hidden 2048, experts of 768: 17.4 us, of which
+// the weights are 5.6 at a copy's rate: about 1 us to find the rows, 3.5 until
+// the first sums, 2 for a part's blocks, 1.3 and 1.5 for the clusters' exchanges,
+// 1.8 for the activation (instruction fetches; 2.8 with its columns unrolled), 1.2
+// from the end of the first kernel to the second's first row, 2.8 for that one's
+// blocks.  The same layer on warp-level products (mma.sync, weights loaded straight
+// to registers) took 311 and 1446 us: an e4m3 mma.sync is a score of instructions
+// here, 340 a 2 KB tile in all, against 160 a 16 KB tile.
 #include <cooperative_groups.h>
 
 #include "bf16.cuh"
 #include "check.h"
 #include "coding.cuh"
 #include "launch.h"
-#include "mma8.cuh"
 #include "tc.cuh"
 #include "thin.h"
 #include "tilemap.h"
@@ -100,8 +111,8 @@ constexpr size_t thin_fixed_smem() {
 
 // kDown's lists behind that: the sums [ntok][128]; ids; the lists' assignments
 // and weights; for each expert its tokens as 64 bits and its first list place;
-// the entries (an expert and up to 16 of
-// its tokens): their experts and where their lists start.
+// the entries (an expert and up to 16 of its tokens): their experts and where
+// their lists start.
 __host__ __device__ constexpr int thin_entries(int A, int E) { return E + A / kThinRowsAt + 1; }
 __host__ __device__ constexpr size_t thin_lists_smem(int ntok, int E, int R) {
     return (size_t)ntok * 512 + (size_t)ntok * R * 12 +
@@ -305,47 +316,37 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 
     if (warp == kThinTma) {
         const uint32_t one = elect_one();
-        {
-            for (int item = i0; item < i1; ++item, ++issued) {
-                const int u = kMode == Thin::kDown ? item / Kb : 0, b = item - u * Kb;
-                const int ex = kMode == Thin::kDown ? experts[u] : e, st = issued % kStages;
-                if (issued >= kStages &&
-                    !wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop))
-                    break;
-                if (!one) continue;
-                uint8_t *w = ring + st * kBytes;
-                mbar_arrive_expect_tx(&s.full[st], kHalves * kTileBytes);
-                tma_tile(w, &map_w, b * 128, ex * p.n + blk * 128, &s.full[st]);
-                if (kPair)
-                    tma_tile(w + kTileBytes, &map_w, b * 128, ex * p.n + (p.n >> 1) + blk * 128,
-                             &s.full[st]);
-            }
+        for (int item = i0; item < i1; ++item, ++issued) {
+            const int u = kMode == Thin::kDown ? item / Kb : 0, b = item - u * Kb;
+            const int ex = kMode == Thin::kDown ? experts[u] : e, st = issued % kStages;
+            if (issued >= kStages && !wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop))
+                break;
+            if (!one) continue;
+            uint8_t *w = ring + st * kBytes;
+            mbar_arrive_expect_tx(&s.full[st], kHalves * kTileBytes);
+            tma_tile(w, &map_w, b * 128, ex * p.n + blk * 128, &s.full[st]);
+            if (kPair)
+                tma_tile(w + kTileBytes, &map_w, b * 128, ex * p.n + (p.n >> 1) + blk * 128,
+                         &s.full[st]);
         }
     } else if (warp == kThinMma) {
-        const uint32_t one = elect_one();
-        {
-            int it = 0;
-            for (int item = i0; item < i1; ++item, ++it) {
-                const int st = it % kStages, ac = it % kAccs;
-                const uint32_t idesc = tc_e4m3_f32(128, NMAX);
-                if (it >= kAccs && !wait_or_stop(&s.tempty[ac], (it / kAccs - 1) & 1, stop)) break;
-                if (!wait_or_stop(&s.full[st], (it / kStages) & 1, stop)) break;
-                tc_fence_after();
-                const uint8_t *w = ring + st * kBytes;
-                const uint64_t rows = tc_operand(w + kHalves * kTileBytes);
-                const uint64_t wd = tc_operand(w);
-                // products on one accumulator follow each other 134 cycles apart,
-                // however narrow; the gate's and the up's go in turn (8 in 730
-                // cycles, 1076 one after the other)
+        const uint32_t one = elect_one(), idesc = tc_e4m3_f32(128, NMAX);
+        int it = 0;
+        for (int item = i0; item < i1; ++item, ++it) {
+            const int st = it % kStages, ac = it % kAccs;
+            if (it >= kAccs && !wait_or_stop(&s.tempty[ac], (it / kAccs - 1) & 1, stop)) break;
+            if (!wait_or_stop(&s.full[st], (it / kStages) & 1, stop)) break;
+            tc_fence_after();
+            const uint64_t w = tc_operand(ring + st * kBytes);
+            const uint64_t rows = tc_operand(ring + st * kBytes + kHalves * kTileBytes);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // 32 bytes along k: 2 address units
+            for (int kk = 0; kk < 4; ++kk)  // 32 bytes along k: 2 address units
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
-                        tc_mma(tmem + (ac * kHalves + h) * NMAX,
-                               wd + h * (kTileBytes >> 4) + kk * 2, rows + kk * 2, idesc, kk > 0, one);
-                tc_commit(&s.empty[st], one);
-                tc_commit(&s.tfull[ac], one);
-            }
+                for (int h = 0; h < kHalves; ++h)
+                    tc_mma(tmem + (ac * kHalves + h) * NMAX, w + h * (kTileBytes >> 4) + kk * 2,
+                           rows + kk * 2, idesc, kk > 0, one);
+            tc_commit(&s.empty[st], one);
+            tc_commit(&s.tfull[ac], one);
         }
     } else if (warp >= kRowWarp) {
         // A piece: kUp one row's block of x; else four rows' 128 bytes.  Pieces
