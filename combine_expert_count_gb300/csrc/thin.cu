@@ -621,9 +621,10 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         for (int j = 0; j < m; ++j) {
             const float scale = block_scale(
                 max(max(s.peak[0][j], s.peak[1][j]), max(s.peak[2][j], s.peak[3][j])));
-            const uint32_t code =
-                scale == 0.0f ? 0u : code4(own[j * 128], 0.0f, 0.0f, 0.0f, scale);
-            p.h_q[row_of(j) * I + blk * 128 + tid] = (uint8_t)code;
+            float first;
+            const float inv = code_factor(scale, &first);  // as the 128-row tiles code it
+            p.h_q[row_of(j) * I + blk * 128 + tid] =
+                (uint8_t)code4_by(own[j * 128] * first, 0.0f, 0.0f, 0.0f, inv);
             if (tid == 0) p.h_s[row_of(j) * (I >> 7) + blk] = scale;
         }
     }
@@ -631,31 +632,36 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 
 // ------------------------------------------------------------ host
 
-// Room for the sums that the parts of a cluster send to the first one; where they
-// are more, the first one fetches them, with two barriers of the cluster around
-// (about 2 us against 0.7).
-constexpr int kPushBytes = 7 * 1024;
+// Room for the sums that the parts of a cluster send to the first one: what two
+// CTAs an SM leave, or all of an SM's where half the SMs have a CTA at most (a
+// cluster has to find its SMs in one GPC: at 128 CTAs of a whole SM each, the
+// last cluster of eight waited for another to end).  Where they are more, the
+// first part fetches them, with two barriers of the cluster around (about 2 us
+// against 1.3).
+constexpr int kPushBytes = 7 * 1024, kMostSmem = 232448;
 
 template <Thin kMode>
 static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, int parts,
                                size_t more_smem, cudaStream_t st) {
-    const int inbox = (parts - 1) * 512 * (kMode == Thin::kDown ? p.ntok : (thin_pair(kMode) ? 2 : 1) * p.most);
-    p.push = inbox <= kPushBytes;
+    const size_t inbox = (size_t)(parts - 1) * 512 *
+                         (kMode == Thin::kDown ? p.ntok : (thin_pair(kMode) ? 2 : 1) * p.most);
+    constexpr size_t kFixed = thin_fixed_smem<kMode>();
+    const bool alone = (int64_t)grid.x * grid.y * parts * 2 <= sm_count();
+    p.push = inbox <= (alone ? kMostSmem - kFixed - more_smem : kPushBytes);
     if (p.push) more_smem += inbox;
     const auto kern = k_thin<kMode>;
-    constexpr size_t kFixed = thin_fixed_smem<kMode>();
-    constexpr size_t kMost =
-        kFixed + (kMode == Thin::kDown
-                      ? thin_lists_smem(MOE_FEW_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOPK)
-                      : 0);
-    static_assert(kMost + kPushBytes <= 232448, "a CTA's shared memory");
-    static_assert(kFixed + kPushBytes <= 113 * 1024 || kMode == Thin::kDown, "two CTAs an SM");
+    static_assert(kFixed + kPushBytes <= 113 * 1024, "two CTAs an SM");
+    static_assert(thin_fixed_smem<Thin::kDown>() +
+                          thin_lists_smem(MOE_FEW_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOPK) +
+                          kPushBytes <=
+                      kMostSmem,
+                  "a CTA's shared memory");
     static LaunchMemo memo;
     int done = 0;
     cudaError_t err = memo.get(0, &done, [&](int *v) {
         *v = 1;
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)kMost + kPushBytes);
+                                    kMostSmem);
     });
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
