@@ -7,10 +7,10 @@
 namespace moe {
 
 // Rows (N * cap) up to which a product goes this way.  us here against the
-// 128-row tiles: one row by 7168 x 2048 6.2 : 11.6, sixteen 8.2 : 11.6, 32 15 : 11.5;
-// gate/up of 2048 by 7168 at one row 11 : 28, sixteen 20 : 28, 32 28 : 28, of 768
-// by 2048 8.2 : 12, 11.3 : 12 (eight), 15.4 : 12 (sixteen); eight experts with one
-// row each 28.6 : 32.7 and (7168 x 2048) 16.1 : 17.1, with four each 52 : 43.
+// 128-row tiles: one row by 7168 x 2048 6.2 : 9.5, sixteen 8.1 : 9.5, 32 15 : 9.5;
+// gate/up of 2048 by 7168 at one row 10.6 : 20.5, sixteen 17.5 : 20.5, of 768 by 2048
+// 8.2 : 11.7, 10.3 : 11.7 (eight), 13.0 : 11.7 (sixteen); eight experts with one row
+// each 28.6 : 32.7 and (7168 x 2048) 16 : 17, with four each 52 : 43 and 26 : 27.
 constexpr int kThinRows = 16;
 
 // y (bf16) or, where h_q is given, the coded activation of the pair of weight

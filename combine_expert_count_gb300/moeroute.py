@@ -454,7 +454,7 @@ def moe_rmsnorm(shape, x, gamma, eps: float, y=None, q=None, s=None, res=None, r
     ``res_out``, each where a buffer is given."""
     sh = _as_shape(shape)
     nx = sizes_query(sh).bytes_x
-    rc = lib().moe_rmsnorm(
+    rc = (_lib or lib()).moe_rmsnorm(
         ctypes.byref(sh), eps, _ptr(x, nx, "x"), _maybe(res, nx, "res"),
         _ptr(gamma, 2 * sh.H, "gamma"), _maybe(res_out, nx, "res_out"), _maybe(y, nx, "y"),
         _maybe(q, nx // 2, "q"), _maybe(s, nx // 64, "s"), _raw_stream(stream))
@@ -468,7 +468,7 @@ def moe_expert_gemm(shape, n: int, k: int, a_q, a_s, grp_off, w_q, w_s, y, statu
     sh = _as_shape(shape)
     z = sizes_query(sh)
     rows, E = sh.N * z.cap, sh.E
-    rc = lib().moe_expert_gemm(
+    rc = (_lib or lib()).moe_expert_gemm(
         ctypes.byref(sh), n, k, _ptr(a_q, rows * k, "a_q"), _ptr(a_s, rows * k // 32, "a_s"),
         _maybe(grp_off, z.bytes_grp_off, "grp_off"), _ptr(w_q, E * n * k, "w_q"),
         _ptr(w_s, E * (n // 128) * (k // 128) * 4, "w_s"), _ptr(y, rows * n * 2, "y"),
@@ -483,7 +483,7 @@ def moe_expert_gemm_swiglu(shape, inter: int, k: int, a_q, a_s, grp_off, w13_q, 
     sh = _as_shape(shape)
     z = sizes_query(sh)
     rows, E = sh.N * z.cap, sh.E
-    rc = lib().moe_expert_gemm_swiglu(
+    rc = (_lib or lib()).moe_expert_gemm_swiglu(
         ctypes.byref(sh), inter, k, _ptr(a_q, rows * k, "a_q"), _ptr(a_s, rows * k // 32, "a_s"),
         _maybe(grp_off, z.bytes_grp_off, "grp_off"), _ptr(w13_q, 2 * E * inter * k, "w13_q"),
         _ptr(w13_s, 2 * E * (inter // 128) * (k // 128) * 4, "w13_s"),
@@ -500,7 +500,7 @@ def moe_layer_few(shape, inter: int, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2
     z = sizes_query(sh)
     nx, ni, H = z.bytes_x, z.bytes_topk_idx, sh.H
     nh, nw, ns = ni // 4 * inter, sh.E * inter * H, sh.E * (inter // 128) * (H // 128) * 4
-    rc = lib().moe_layer_few(
+    rc = (_lib or lib()).moe_layer_few(
         ctypes.byref(sh), inter, _ptr(x, nx, "x"), _ptr(topk_idx, ni, "topk_idx"),
         _ptr(topk_w, ni, "topk_w"), _ptr(w13_q, 2 * nw, "w13_q"), _ptr(w13_s, 2 * ns, "w13_s"),
         _ptr(w2_q, nw, "w2_q"), _ptr(w2_s, ns, "w2_s"), _ptr(h_q, nh, "h_q"),
