@@ -85,15 +85,17 @@ constexpr int kThinRowsAt = 16;
 // takes several times as long as the products of a few rows.
 constexpr int kAccs = 4;
 
-// Ring stages for which two CTAs fit an SM.
+// Ring stages for which two CTAs fit an SM; kDown's lists of many tokens take two
+// stages' room (64 tokens on 64 experts, hidden 7168: 224 CTAs are two waves of
+// one an SM, DOWN64).
 __host__ __device__ constexpr int thin_stages(Thin m) { return thin_pair(m) ? 3 : 5; }
+constexpr int kDownFewStages = 3;
 __host__ __device__ constexpr int thin_stage_bytes(Thin m) {
     return (thin_pair(m) ? 2 : 1) * kTileBytes + kThinRowsAt * 128;
 }
 
-template <Thin kMode>
+template <int kStages>
 struct alignas(16) ThinShared {
-    static constexpr int kStages = thin_stages(kMode);
     float scale[kStages][kThinRowsAt];  // of the rows' pieces in each stage
     uint64_t full[kStages], empty[kStages], tfull[kAccs], tempty[kAccs], drain, inbox;
     uint32_t tmem;
@@ -104,9 +106,9 @@ struct alignas(16) ThinShared {
     int list[MOE_FEW_MAX_TOKENS];  // kUp: the expert's assignments, one a token
 };
 
-template <Thin kMode>
+template <Thin kMode, int kStages>
 constexpr size_t thin_fixed_smem() {
-    return 1024 + (size_t)thin_stages(kMode) * thin_stage_bytes(kMode) + sizeof(ThinShared<kMode>);
+    return 1024 + (size_t)kStages * thin_stage_bytes(kMode) + sizeof(ThinShared<kStages>);
 }
 
 // kDown's lists behind that: the sums [ntok][128]; ids; the lists' assignments
@@ -124,15 +126,15 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     return (uint32_t)r * 128 + (uint32_t)((c ^ (r & 7)) << 4);
 }
 
-template <Thin kMode>
+template <Thin kMode, int kStages>
 __global__ void __launch_bounds__(kThinThreads, 2)
     k_thin(const ThinArgs p, const __grid_constant__ CUtensorMap map_w) {
     constexpr bool kPair = thin_pair(kMode);
     constexpr int kHalves = kPair ? 2 : 1;
-    constexpr int kStages = thin_stages(kMode), kBytes = thin_stage_bytes(kMode);
+    constexpr int kBytes = thin_stage_bytes(kMode);
     constexpr int NMAX = kThinRowsAt;
     constexpr int kCols = kAccs * kHalves * NMAX;
-    using Shared = ThinShared<kMode>;
+    using Shared = ThinShared<kStages>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + align1024(smem_raw);
     Shared &s = *reinterpret_cast<Shared *>(ring + kStages * kBytes);
@@ -181,8 +183,9 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     unsigned *who = reinterpret_cast<unsigned *>(weight + A);  // [E][2]
     int *place = reinterpret_cast<int *>(who + 2 * p.E), *start = place + p.E;
     int *experts = start + thin_entries(A, p.E);
-    const int unit = kMode == Thin::kDown ? 0 : blockIdx.y / p.passes;
-    const int r0 = kMode == Thin::kDown ? 0 : (blockIdx.y - unit * p.passes) * NMAX;
+    // the units' first 16 rows come first; few have more
+    const int units = kMode == Thin::kDown ? 1 : gridDim.y / p.passes;
+    const int unit = blockIdx.y % units, r0 = blockIdx.y / units * NMAX;
     int U = 0;  // kDown: entries
     if constexpr (kMode == Thin::kUp) {
         ids = reinterpret_cast<int *>(ring);  // the ring is not in use yet
@@ -638,20 +641,20 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 // last cluster of eight waited for another to end).  Where they are more, the
 // first part fetches them, with two barriers of the cluster around (about 2 us
 // against 1.3).
-constexpr int kPushBytes = 7 * 1024, kMostSmem = 232448;
+constexpr int kPushBytes = 7 * 1024, kMostSmem = 232448, kTwoSmem = 113 * 1024;
 
-template <Thin kMode>
+template <Thin kMode, int kStages = thin_stages(kMode)>
 static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, int parts,
                                size_t more_smem, cudaStream_t st) {
     const size_t inbox = (size_t)(parts - 1) * 512 *
                          (kMode == Thin::kDown ? p.ntok : (thin_pair(kMode) ? 2 : 1) * p.most);
-    constexpr size_t kFixed = thin_fixed_smem<kMode>();
+    constexpr size_t kFixed = thin_fixed_smem<kMode, kStages>();
     const bool alone = (int64_t)grid.x * grid.y * parts * 2 <= sm_count();
     p.push = inbox <= (alone ? kMostSmem - kFixed - more_smem : kPushBytes);
     if (p.push) more_smem += inbox;
-    const auto kern = k_thin<kMode>;
-    static_assert(kFixed + kPushBytes <= 113 * 1024, "two CTAs an SM");
-    static_assert(thin_fixed_smem<Thin::kDown>() +
+    const auto kern = k_thin<kMode, kStages>;
+    static_assert(kFixed + kPushBytes <= kTwoSmem, "two CTAs an SM");
+    static_assert(thin_fixed_smem<Thin::kDown, thin_stages(Thin::kDown)>() +
                           thin_lists_smem(MOE_FEW_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOPK) +
                           kPushBytes <=
                       kMostSmem,
@@ -743,9 +746,11 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.k = p.inter;
     p.w_s = w2_s;
     const dim3 gdown((unsigned)(p.H >> 7));
-    return launch_thin<Thin::kDown>(p, down, gdown,
-                                    thin_parts(gdown.x, (int64_t)units * (p.inter >> 7)),
-                                    thin_lists_smem(p.ntok, p.E, p.R), st);
+    const int parts = thin_parts(gdown.x, (int64_t)units * (p.inter >> 7));
+    const size_t lists = thin_lists_smem(p.ntok, p.E, p.R);
+    constexpr size_t kFixed = thin_fixed_smem<Thin::kDown, thin_stages(Thin::kDown)>();
+    if (kFixed + lists <= kTwoSmem) return launch_thin<Thin::kDown>(p, down, gdown, parts, lists, st);
+    return launch_thin<Thin::kDown, kDownFewStages>(p, down, gdown, parts, lists, st);
 }
 
 }  // namespace moe
