@@ -219,7 +219,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t tmem = s.tmem;
     volatile int *stop = &s.stop;
     const int nb = p.n >> 7, ntn = kSwiglu || p.wide == 2 ? (nb + 1) >> 1 : nb;
-    const int tiles = before * ntn, Kb = p.k >> 7;
+    // kSplit: a cluster has one tile at most (offsets that do not ascend may name
+    // rows twice, and so more tiles than the grid was made for)
+    const int Kb = p.k >> 7;
+    const int tiles = kSplit ? min(before * ntn, (int)gridDim.x) : before * ntn;
     const int parts = kSplit ? gridDim.z : 1, part = kSplit ? blockIdx.z : 0;
     const int kb0 = kSplit ? Kb * part / parts : 0, kb1 = kSplit ? Kb * (part + 1) / parts : Kb;
 

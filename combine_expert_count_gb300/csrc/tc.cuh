@@ -122,7 +122,8 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 
 // An arrival on a barrier of the cluster (its address from dsmem_addr) that orders
-// this thread's stores to the cluster before it, and the bounded wait (as mbar_wait) that orders what follows after such arrivals.
+// this thread's stores to the cluster before it, and the bounded wait (as
+// mbar_wait) that orders what follows after such arrivals.
 __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");

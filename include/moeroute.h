@@ -465,7 +465,8 @@ int moe_rmsnorm(const moe_shape *shape, float eps, const uint16_t *x_bf16,
  * n and k are multiples of 128 up to 65536.  Row i of rank r belongs to local
  * expert j (e = r*Er + j) when grp_off[r][j] <= i < grp_off[r][j+1], offsets
  * being read on the device and clipped to [0, cap]; rows of no expert, and
- * those at or beyond cap, are left untouched.  grp_off may be NULL when E = N:
+ * those at or beyond cap, are left untouched (where a rank's offsets do not
+ * ascend, what its rows hold is not defined).  grp_off may be NULL when E = N:
  * each rank's cap rows are then all its one expert's (N = E = 1 is a dense
  * product of cap rows).  Products of e4m3 values are exact; each block of 128
  * along k is summed in fp32 by the tensor cores and added, times its two

@@ -62,6 +62,30 @@ def test_products(sizes, n, k):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("rows,n,k", [(512, 128, 4096), (512, 512, 256), (9, 128, 1024)])
+def test_offsets_that_do_not_ascend(rows, n, k):
+    """Rows named twice are more tiles than rows are: the calls end, inside their
+    outputs, and the next one is right."""
+    gen = torch.Generator().manual_seed(rows + n)
+    off = torch.tensor([[0, rows, 0, rows, 0]], dtype=torch.int32).cuda()
+    a = [t.cuda() for t in o.make_rows(gen, rows, k)]
+    w = [t.cuda() for t in o.make_weights(gen, 4, 2 * n, k)]
+    sh, g = m.make_shape(1, rows, 4, 1, 128, rows), Guarded()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y, hq = g((rows, n), torch.bfloat16), g((rows, n), torch.uint8)
+    hs = g((rows, n // 128), torch.float32)
+    m.moe_expert_gemm(sh, n, k, *a, off, w[0][:, :n].contiguous(), w[1][:, :n // 128].contiguous(),
+                      y, status)
+    m.moe_expert_gemm_swiglu(sh, n, k, *a, off, *w, hq, hs, status)
+    g.check()
+    assert int(status) == 0
+    off = torch.tensor([[0, rows, rows, rows, rows]], dtype=torch.int32).cuda()
+    m.moe_expert_gemm_swiglu(sh, n, k, *a, off, *w, hq, hs, status)
+    torch.cuda.synchronize()
+    p, err = o.product64(a[0].cpu(), a[1].cpu(), w[0][0].cpu(), w[1][0].cpu())
+    o.assert_codes(hq.cpu(), hs.cpu(), *o.swiglu64(p, err))
+
+
 @pytest.mark.parametrize("T,E,R,H,I", [(1, 8, 2, 128, 128), (5, 16, 4, 1408, 256),
                                        (33, 4, 2, 256, 384), (64, 32, 8, 512, 128)])
 def test_few(T, E, R, H, I):
