@@ -67,10 +67,14 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
 
 // ------------------------------------------------------------ small copies
 
-// Four bytes, global -> shared, asynchronously; `bar` gets this thread's arrival
+// Four or sixteen bytes, global -> shared, asynchronously; `bar` gets this thread's arrival
 // once its copies so far are there (an arrival that the barrier's count includes).
 __device__ __forceinline__ void copy4_async(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
                  : "memory");
 }
 __device__ __forceinline__ void copies_arrive(uint64_t *bar) {

@@ -1,4 +1,4 @@
-// thin.cu -- products of the experts' weights with few rows: the two kernels of
+// thin.cu -- products of the experts' weights with few rows: the kernels of
 // moe_layer_few, and moe_expert_gemm / moe_expert_gemm_swiglu for a few rows in
 // all.  They are bound by reading the weights once.
 //
@@ -7,22 +7,22 @@
 // and a lane of tensor memory is an output feature.  A CTA owns one block of
 // 128 outputs of one expert (its gate and its up block; or one block over a run
 // of experts) and streams the weights' 16 KB tiles by TMA through a ring of
-// shared memory.  Four warps put the rows' 128-byte pieces beside them: coded
-// from x on the way, or copied from coded rows.  One warp issues the products
-// of a k block; four add it, times its scales, to fp32 sums.  Two CTAs fit an SM,
-// so one streams while the other starts or ends; together they keep about 200 KB
-// of weights on the way, and nothing but the ring's TMA copies waits for HBM.
+// shared memory.  Two warps put the rows' 128-byte pieces beside them, a k block
+// each in turn: by asynchronous copies as deep as the ring, or coded from x where
+// the tokens are very few.  One warp issues the products of a k block; four add it,
+// times its scales, to fp32 sums.  Two CTAs fit an SM, so one streams while the other
+// starts or ends; together they keep about 200 KB of weights on the way.  Rows that
+// come through registers, by four warps a block, are late where there are many: 64
+// tokens on 64 experts (hidden 7168, experts of 2048) 521 us, now 415 to 420.
 // Where there are fewer units than that, the CTAs of a cluster share each one's k
 // blocks (thin_parts).
 //
-// Measured, hidden 7168, experts of 2048, top-8: four tokens of 256 experts 206 to
-// 227 us (30 to 32 experts' weights, 6.0 TB/s), 32 tokens on 64 experts 447 us (6.2
-// TB/s, 92% of a copy's).  One token, hidden 2048, experts of 768: 17.4 us, of which
-// the weights are 5.6 at a copy's rate: about 1 us to find the rows, 3.5 until
-// the first sums, 2 for a part's blocks, 1.3 and 1.5 for the clusters' exchanges,
-// 1.8 for the activation (instruction fetches; 2.8 with its columns unrolled), 1.2
-// from the end of the first kernel to the second's first row, 2.8 for that one's
-// blocks.  The same layer on warp-level products (mma.sync, weights loaded straight
+// Measured, hidden 7168, experts of 2048, top-8: four tokens of 256 experts 208 to
+// 221 us (30 to 32 experts' weights, 6.1 to 6.8 TB/s), 32 tokens on 64 experts 401 to 411 us (6.9 TB/s, a
+// copy's rate).  One token, hidden 2048, experts of 768: 16.3 us, of which the weights
+// are 5.6 at a copy's rate (13.9 where L2 has them); the rest is finding the rows (1 us), the clusters'
+// exchanges (1.3 and 1.5), the activation (1.8, instruction fetches; 2.8 with its
+// columns unrolled) and the second kernel's wait for the first.  The same layer on warp-level products (mma.sync, weights loaded straight
 // to registers) took 311 and 1446 us: an e4m3 mma.sync is a score of instructions
 // here, 340 a 2 KB tile in all, against 160 a 16 KB tile.
 #include <cooperative_groups.h>
@@ -42,18 +42,22 @@ namespace cg = cooperative_groups;
 
 // What a kernel multiplies and what becomes of it:
 //   kUp    rows coded from x, gate and up, activation coded to h     (few tokens)
+//   kUpCoded  the same of rows that k_code_rows coded
 //   kDown  rows of h, an output block of every token over all experts (few tokens)
 //   kGemm, kSwiglu  grouped coded rows, as the entry points say
-enum class Thin { kUp, kDown, kGemm, kSwiglu };
+enum class Thin { kUp, kUpCoded, kDown, kGemm, kSwiglu };
 
-constexpr int kThinWarps = 10, kThinThreads = 32 * kThinWarps;
-constexpr int kRowWarp = 4, kRowWarps = 4, kThinTma = 8, kThinMma = 9;  // warps 0-3: sums
+// Warps 0-3 have the sums; the last two bring the rows, in turn: no more warps than
+// stages, or one could miss two phases of a stage's barrier.  Eight warps leave two
+// CTAs 128 registers a thread.
+constexpr int kThinTma = 4, kThinMma = 5, kRowWarp = 6, kRowWarps = 2;
+constexpr int kThinThreads = 32 * (kRowWarp + kRowWarps);
 constexpr int kTileBytes = 128 * 128;
 
 struct ThinArgs {
     // few tokens
     int ntok, E, R, H, inter;
-    bool by_expert;  // k_thin<kUp>: units are experts, not assignments
+    bool by_expert;  // gate and up: units are experts, not assignments
     int passes;      // units of 16 rows that an expert may need
     bool push;       // a cluster's parts send their sums to the first one's inbox
     const uint16_t *x;
@@ -75,7 +79,14 @@ struct ThinArgs {
     int32_t *status;
 };
 
-__host__ __device__ constexpr bool thin_pair(Thin m) { return m == Thin::kUp || m == Thin::kSwiglu; }
+__host__ __device__ constexpr bool thin_up(Thin m) { return m == Thin::kUp || m == Thin::kUpCoded; }
+__host__ __device__ constexpr bool thin_pair(Thin m) { return thin_up(m) || m == Thin::kSwiglu; }
+
+// Up to so many tokens the gate and up kernel codes the rows of x that it multiplies,
+// each of its CTAs again; beyond, a kernel before it codes them once.  us: four
+// tokens 15.8 and 16.1 (8 experts of 768, hidden 2048, in L2), 98.9 and 100.6 (32 of 2048,
+// 4096); with room for eight rows eight tokens 18.1 and 16.1, and fewer tokens 2% more.
+constexpr int kOwnRows = 4;
 
 // Columns of a product: rows of one expert that meet its weights at a time.  A
 // unit with more is several units, whose reads of the weights meet in L2.
@@ -103,7 +114,8 @@ struct alignas(16) ThinShared {
     unsigned chosen[2];
     int wsum[32];
     uint32_t peak[4][kThinRowsAt];
-    int list[MOE_FEW_MAX_TOKENS];  // kUp: the expert's assignments, one a token
+    int list[MOE_FEW_MAX_TOKENS];  // gate and up of few tokens: the expert's assignments,
+    int token[MOE_FEW_MAX_TOKENS];  // one a token; and their tokens
 };
 
 template <Thin kMode, int kStages>
@@ -124,6 +136,31 @@ __host__ __device__ constexpr size_t thin_lists_smem(int ntok, int E, int R) {
 // Where byte 16 c of row r of a 128-byte-swizzled tile is.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     return (uint32_t)r * 128 + (uint32_t)((c ^ (r & 7)) << 4);
+}
+
+// One row's block of 128, four values a lane: a lane's codes, and the scale.
+__device__ __forceinline__ uint32_t code_row(float a, float b, float c, float d, float *scale) {
+    *scale = block_scale(__reduce_max_sync(
+        kFull, max(max(abs_bits(a), abs_bits(b)), max(abs_bits(c), abs_bits(d)))));
+    return *scale == 0.0f ? 0u : code4(a, b, c, d, *scale);
+}
+
+// Codes x's blocks of 128, a warp each, to where the layer's output will be: 128
+// codes and the scale in the 256 bytes that the block's outputs take (so x and out
+// may be the same).
+constexpr int kCodedBlock = 256, kCodeWarps = 4;
+__global__ void __launch_bounds__(32 * kCodeWarps) k_code_rows(int blocks, const uint16_t *x, uint8_t *out) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int i = blockIdx.x * kCodeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (i >= blocks) return;
+    const uint2 w = *reinterpret_cast<const uint2 *>(x + (size_t)i * 128 + lane * 4);
+    float scale;
+    const uint32_t code =
+        code_row(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), &scale);
+    uint8_t *to = out + (size_t)i * kCodedBlock;
+    *reinterpret_cast<uint32_t *>(to + lane * 4) = code;
+    if (lane == 0) *reinterpret_cast<float *>(to + 128) = scale;
 }
 
 template <Thin kMode, int kStages>
@@ -147,7 +184,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     // while the kernel before this one ends
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s.full[i], 1 + kRowWarps);
+            mbar_init(&s.full[i], kMode == Thin::kUp ? 2 : 1 + 32);  // TMA's, and a row warp's
             mbar_init(&s.empty[i], 1 + 4);
         }
         for (int i = 0; i < kAccs; ++i) {
@@ -163,12 +200,17 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     if (warp == kThinMma) tc_alloc<kCols>(&s.tmem);
     // a part's inbox is there before another sends to it: waited for at the end
     if (parts > 1 && p.push) cluster.barrier_arrive();
-    if constexpr (kMode != Thin::kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the kernel before kUpCoded and kDown is this call's, which has waited: only
+    // what it made is waited for, where it is read
+    constexpr bool kLate = kMode == Thin::kDown || kMode == Thin::kUpCoded;
+    if constexpr (!kLate) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const auto leave = [&]() {  // nothing to do: all threads
         __syncthreads();
         if (parts > 1 && p.push) cluster.barrier_wait();
         if (warp == kThinMma) tc_free<kCols>(s.tmem);
+        // not done before the kernel that it follows is
+        if constexpr (kLate) asm volatile("griddepcontrol.wait;" ::: "memory");
     };
 
     // ---------------------------------------------------------------- the unit
@@ -183,11 +225,12 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     unsigned *who = reinterpret_cast<unsigned *>(weight + A);  // [E][2]
     int *place = reinterpret_cast<int *>(who + 2 * p.E), *start = place + p.E;
     int *experts = start + thin_entries(A, p.E);
-    // the units' first 16 rows come first; few have more
-    const int units = kMode == Thin::kDown ? 1 : gridDim.y / p.passes;
-    const int unit = blockIdx.y % units, r0 = blockIdx.y / units * NMAX;
+    // CTAs with the same weights and other rows are neighbours: one reads HBM, the
+    // others L2 (16 experts, 64 tokens, 16 rows an expert on average, hidden 7168: 146 us;
+    // 158 with all units' first 16 rows first; 8 experts with 8 rows at most 17.6 and 17.0)
+    const int unit = blockIdx.y / p.passes, r0 = blockIdx.y % p.passes * NMAX;
     int U = 0;  // kDown: entries
-    if constexpr (kMode == Thin::kUp) {
+    if constexpr (thin_up(kMode)) {
         ids = reinterpret_cast<int *>(ring);  // the ring is not in use yet
         int bad = 0;
         for (int i = tid; i < A; i += kThinThreads) {
@@ -217,6 +260,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             const unsigned below = (1u << lane) - 1u;
             const int at = warp == 0 ? __popc(lo & below) : __popc(lo) + __popc(hi & below);
             s.list[at] = tid * p.R + k;
+            s.token[at] = tid;
         }
         __syncthreads();
         if (m <= r0 || (!p.by_expert && s.list[0] != unit)) return leave();
@@ -297,7 +341,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         row0 = (long long)(e / Er) * p.cap + s.unit[1] + r0;
     }
 
-    fence_async_smem();  // kUp's ids lay where the ring is
+    fence_async_smem();  // gate and up: the ids lay where the ring is
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -339,6 +383,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             const int st = it % kStages, ac = it % kAccs;
             if (it >= kAccs && !wait_or_stop(&s.tempty[ac], (it / kAccs - 1) & 1, stop)) break;
             if (!wait_or_stop(&s.full[st], (it / kStages) & 1, stop)) break;
+            fence_async_smem();  // the rows, for the tensor cores
             tc_fence_after();
             const uint64_t w = tc_operand(ring + st * kBytes);
             const uint64_t rows = tc_operand(ring + st * kBytes + kHalves * kTileBytes);
@@ -352,80 +397,74 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             tc_commit(&s.tfull[ac], one);
         }
     } else if (warp >= kRowWarp) {
-        // A piece: kUp one row's block of x; else four rows' 128 bytes.  Pieces
-        // go round the four warps, each loading its next one while it works.
         const int rw = warp - kRowWarp;
-        if constexpr (kMode == Thin::kDown)
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // h is k_thin<kUp>'s
-        constexpr int kPer = kMode == Thin::kUp ? 1 : 4;
-        const auto rows_of = [&](int item) {
-            return kMode == Thin::kDown ? start[item / Kb + 1] - start[item / Kb] : m;
-        };
-        int item = i0, first = 0;       // first piece of the item, counted over all items
-        int ni = i0, nfirst = 0, nq = rw;  // this warp's next piece to load: of item ni
-        uint4 v = make_uint4(0, 0, 0, 0);
-        float sc = 0.0f;
-        const auto load_next = [&]() {
-            while (ni < i1) {
-                const int pieces = (rows_of(ni) + kPer - 1) / kPer;
-                if (nq < nfirst + pieces) break;
-                nfirst += pieces;
-                ++ni;
+        if constexpr (kMode == Thin::kUp) {
+            // A warp codes its next item's rows before it waits for their stage, and loads
+            // the ones after meanwhile.  A row is all lanes', four values each.
+            const uint16_t *x[kOwnRows];
+            uint2 v[kOwnRows];
+            uint32_t code[kOwnRows];
+            float scale[kOwnRows];
+#pragma unroll
+            for (int q = 0; q < kOwnRows; ++q) {
+                if (q >= m || i0 + rw >= i1) break;
+                x[q] = p.x + (size_t)s.token[q] * p.H + lane * 4;
+                v[q] = *reinterpret_cast<const uint2 *>(x[q] + (i0 + rw) * 128);
             }
-            if (ni >= i1) return;
-            const int q = nq - nfirst;
-            if constexpr (kMode == Thin::kUp) {
-                const int tok = s.list[r0 + q] / p.R;
-                const uint2 w = *reinterpret_cast<const uint2 *>(p.x + (size_t)tok * p.H + ni * 128 +
-                                                                 lane * 4);
-                v.x = w.x;
-                v.y = w.y;
-            } else {
-                const int u = kMode == Thin::kDown ? ni / Kb : 0, b = ni - u * Kb;
-                const int r = min(q * 4 + (lane >> 3), rows_of(ni) - 1);
-                const size_t row = kMode == Thin::kDown ? (size_t)slot[start[u] + r] : row0 + r;
-                const uint8_t *rq = kMode == Thin::kDown ? p.h_q : p.a_q;
-                const float *rs = kMode == Thin::kDown ? p.h_s : p.a_s;
-                v = *reinterpret_cast<const uint4 *>(rq + row * p.k + b * 128 + (lane & 7) * 16);
-                sc = rs[row * Kb + b];
-            }
-            nq += kRowWarps;
-        };
-        load_next();
-        int mine = rw;  // this warp's next piece to put in place
-        for (int it = 0; item < i1; ++item, ++it) {
-            const int st = it % kStages;
-            const bool ok = it < kStages ||
-                            __all_sync(kFull, wait_or_stop(&s.empty[st], (it / kStages - 1) & 1, stop));
-            if (!ok) break;
-            const int mm = rows_of(item), pieces = (mm + kPer - 1) / kPer;
-            uint8_t *rows = ring + st * kBytes + kHalves * kTileBytes;
-            for (; mine < first + pieces; mine += kRowWarps) {
-                const int q = mine - first;
-                const uint4 cur = v;
-                const float cs = sc;
-                load_next();
-                if constexpr (kMode == Thin::kUp) {
-                    const float f0 = bf16_lo(cur.x), f1 = bf16_hi(cur.x), f2 = bf16_lo(cur.y),
-                                f3 = bf16_hi(cur.y);
-                    const uint32_t am = __reduce_max_sync(
-                        kFull, max(max(abs_bits(f0), abs_bits(f1)), max(abs_bits(f2), abs_bits(f3))));
-                    const float scale = block_scale(am);
-                    *reinterpret_cast<uint32_t *>(rows + swizzled(q, lane >> 2) + (lane & 3) * 4) =
-                        scale == 0.0f ? 0u : code4(f0, f1, f2, f3, scale);
-                    if (lane == 0) s.scale[st][q] = scale;
-                } else {
-                    const int r = q * 4 + (lane >> 3);
-                    if (r < mm) {
-                        *reinterpret_cast<uint4 *>(rows + swizzled(r, lane & 7)) = cur;
-                        if ((lane & 7) == 0) s.scale[st][r] = cs;
-                    }
+            for (int it = rw; i0 + it < i1; it += kRowWarps) {
+                const int st = it % kStages, next = i0 + it + kRowWarps;
+#pragma unroll
+                for (int q = 0; q < kOwnRows; ++q) {
+                    if (q >= m) break;
+                    const float f0 = bf16_lo(v[q].x), f1 = bf16_hi(v[q].x), f2 = bf16_lo(v[q].y),
+                                f3 = bf16_hi(v[q].y);
+                    if (next < i1) v[q] = *reinterpret_cast<const uint2 *>(x[q] + next * 128);
+                    code[q] = code_row(f0, f1, f2, f3, &scale[q]);
                 }
+                if (it >= kStages &&
+                    !__all_sync(kFull, wait_or_stop(&s.empty[st], (it / kStages - 1) & 1, stop)))
+                    break;
+                uint8_t *rows = ring + st * kBytes + kHalves * kTileBytes;
+#pragma unroll
+                for (int q = 0; q < kOwnRows; ++q) {
+                    if (q >= m) break;
+                    *reinterpret_cast<uint32_t *>(rows + swizzled(q, lane >> 2) + (lane & 3) * 4) =
+                        code[q];
+                    if (lane == 0) s.scale[st][q] = scale[q];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.full[st]);
             }
-            first += pieces;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.full[st]);
+        } else {
+            // eight lanes a row, by asynchronous copies
+            if constexpr (kLate) asm volatile("griddepcontrol.wait;" ::: "memory");
+            const int c = lane & 7;
+            for (int it = rw; i0 + it < i1; it += kRowWarps) {
+                const int item = i0 + it, st = it % kStages;
+                const int u = kMode == Thin::kDown ? item / Kb : 0, b = item - u * Kb;
+                const int l = kMode == Thin::kDown ? start[u] : 0;
+                const int mm = kMode == Thin::kDown ? start[u + 1] - l : m;
+                if (it >= kStages &&
+                    !__all_sync(kFull, wait_or_stop(&s.empty[st], (it / kStages - 1) & 1, stop)))
+                    break;
+                uint8_t *rows = ring + st * kBytes + kHalves * kTileBytes;
+                for (int r = lane >> 3; r < mm; r += 4) {
+                    const uint8_t *q;
+                    const float *sc;
+                    if constexpr (kMode == Thin::kUpCoded) {
+                        q = p.a_q + ((size_t)s.token[r0 + r] * Kb + b) * kCodedBlock;
+                        sc = reinterpret_cast<const float *>(q + 128);
+                    } else {
+                        const size_t row = kMode == Thin::kDown ? (size_t)slot[l + r] : row0 + r;
+                        q = (kMode == Thin::kDown ? p.h_q : p.a_q) + row * p.k + b * 128;
+                        sc = (kMode == Thin::kDown ? p.h_s : p.a_s) + row * Kb + b;
+                    }
+                    copy16_async(rows + swizzled(r, c), q + c * 16);
+                    if (c == 0) copy4_async(&s.scale[st][r], sc);
+                }
+                copies_arrive(&s.full[st]);
+            }
+            copies_wait();
         }
     } else {
         // sums: lane = output 32 warp + lane of the block, column = row of x or h
@@ -594,7 +633,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     }
     if (part > 0 || warp >= 4) return;
     const auto row_of = [&](int j) {
-        return kMode == Thin::kUp ? (size_t)s.list[r0 + j] : (size_t)(row0 + j);
+        return thin_up(kMode) ? (size_t)s.list[r0 + j] : (size_t)(row0 + j);
     };
     // The columns go through the thread's own words of the ring to be taken one
     // after another: sixteen copies of what follows cost 2 us of instruction
@@ -724,6 +763,19 @@ cudaError_t launch_thin_product(int N, int E, int cap, int n, int k, const uint8
     return launch_thin<Thin::kGemm>(p, map, grid, parts, 0, st);
 }
 
+static cudaError_t launch_code_rows(int blocks, const uint16_t *x, uint8_t *out, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((blocks + kCodeWarps - 1) / kCodeWarps));
+    cfg.blockDim = dim3(32 * kCodeWarps);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_code_rows, blocks, x, out);
+}
+
 static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13_s,
                               const uint8_t *w2_q, const float *w2_s, cudaStream_t st) {
     if (p.ntok == 0) return cudaMemsetAsync(p.status, 0, 4, st);
@@ -740,7 +792,15 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.k = p.H;
     p.w_s = w13_s;
     p.most = p.ntok < kThinRowsAt ? p.ntok : kThinRowsAt;
-    err = launch_thin<Thin::kUp>(p, up, gup, thin_parts((int64_t)gup.x * units, p.H >> 7), 0, st);
+    const int up_parts = thin_parts((int64_t)gup.x * units, p.H >> 7);
+    if (p.ntok <= kOwnRows) {
+        err = launch_thin<Thin::kUp>(p, up, gup, up_parts, 0, st);
+    } else {
+        uint8_t *coded = reinterpret_cast<uint8_t *>(p.out);
+        err = launch_code_rows(p.ntok * (p.H >> 7), p.x, coded, st);
+        p.a_q = coded;
+        if (err == cudaSuccess) err = launch_thin<Thin::kUpCoded>(p, up, gup, up_parts, 0, st);
+    }
     if (err != cudaSuccess) return err;
     p.n = p.H;
     p.k = p.inter;

@@ -495,7 +495,7 @@ int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8
                            void *stream);
 
 /* ---------------------------------------------------------------- a few tokens
- * A whole expert layer for a few tokens, in two kernels and without a
+ * A whole expert layer for a few tokens, in two or three kernels and without a
  * dispatch or combine: only the weights of the experts that some token chose
  * are read, once.  Per token t of rank s, with the coding and the products
  * defined above:
@@ -511,8 +511,9 @@ int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8
  *   h_q u8 [N][T][R][inter], h_s float [N][T][R][inter/128]: scratch that the
  *     call writes before it reads (rows of skipped ids stay untouched, and those
  *     of an id that an earlier slot of the token has: its weights are added)
- * x may be pinned host memory, but every expert's CTAs read their tokens' rows
- * again over the link; out may not. */
+ * out may be x, or not overlap it; beyond four tokens it holds x's coding until
+ * the outputs are there.  x may be pinned host memory (up to four tokens every
+ * expert's CTAs read their tokens' rows again over the link); out may not. */
 #define MOE_FEW_MAX_TOKENS 64
 int moe_layer_few(const moe_shape *shape, int inter, const uint16_t *x_bf16,
                   const int32_t *topk_idx, const float *topk_w, const uint8_t *w13_q,

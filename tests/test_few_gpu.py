@@ -158,3 +158,47 @@ def test_repeats_streams_and_graphs_are_identical():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 17, 64])
+def test_x_is_coded_as_the_dispatch_codes_it(T):
+    """Gates of amax and up weights of one: h's codes are x's own, ties included."""
+    gen = torch.Generator().manual_seed(T)
+    amax = 448.0 / 2 ** torch.randint(0, 4, (T, 1), generator=gen).double()
+    ties = (8.5 + torch.randint(0, 8, (T, 64), generator=gen)) * \
+        2.0 ** torch.randint(-13, 5, (T, 64), generator=gen) * amax / 448
+    any_ = amax * torch.rand((T, 63), generator=gen, dtype=torch.float64)
+    x = torch.cat([amax, torch.cat([ties, any_], 1) *
+                   (1 - 2 * torch.randint(0, 2, (T, 127), generator=gen))], 1)
+    x[T // 2, 0] = 33.25  # no power of two between its scale and 1
+    x[T // 2, 1:] = x[T // 2, 1:].clamp(-33.25, 33.25)
+    x = o.bf16(x.float())
+    w13 = torch.zeros((1, 256, 128), dtype=torch.uint8)
+    w13[0, :128, 0] = 0x38  # 1.0
+    w13[0, 128 + torch.arange(128), torch.arange(128)] = 0x38
+    w2 = o.make_weights(gen, 1, 128, 128)
+    hq, _, _, status = run(T, 1, 1, 128, 128, x, torch.zeros((T, 1), dtype=torch.int32),
+                           torch.ones((T, 1)), (w13, torch.ones((1, 2, 1))), w2)
+    want = o.code_rows(x)[0]
+    assert status == 0 and torch.equal(hq[:, 0], torch.where(want == 0x80, 0, want))
+
+
+@pytest.mark.parametrize("T", [3, 20])
+def test_output_in_the_place_of_x(T):
+    T, E, R, H, inter = T, 8, 3, 384, 256
+    x, idx, w, w13, w2 = inputs(T, E, R, H, inter, 31)
+    want = run(T, E, R, H, inter, x, idx, w, w13, w2)[2]
+    d = [t.cuda() for t in (x, idx, w, *w13, *w2)]
+    hq = torch.zeros((T, R, inter), dtype=torch.uint8, device="cuda")
+    hs = torch.zeros((T, R, inter // 128), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.moe_layer_few(m.make_shape(1, T, E, R, H), inter, *d, hq, hs, d[0], status)
+    torch.cuda.synchronize()
+    assert torch.equal(d[0].cpu(), want)
+
+
+@pytest.mark.parametrize("T", [2, 9])
+def test_no_valid_id_gives_zeros(T):
+    x, idx, w, w13, w2 = inputs(T, 4, 2, 256, 128, 32, torch.full((T, 2), 4, dtype=torch.int32))
+    _, _, out, status = run(T, 4, 2, 256, 128, x, idx, w, w13, w2)
+    assert status == m.MOE_ST_BAD_EXPERT and out.count_nonzero() == 0
