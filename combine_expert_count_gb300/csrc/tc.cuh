@@ -125,29 +125,6 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
-// An arrival on a barrier of the cluster (its address from dsmem_addr) that orders
-// this thread's stores to the cluster before it, and the bounded wait (as
-// mbar_wait) that orders what follows after such arrivals.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
-    const long long t0 = clock64();
-    do {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    } while (clock64() - t0 < kWaitCycles);
-    return false;
-}
-
 // `bar` gets one arrival once the thread's products so far are done (where `on`).
 __device__ __forceinline__ void tc_commit(uint64_t *bar, uint32_t on) {
     asm volatile(

@@ -1,6 +1,6 @@
 // thin.cu -- products of the experts' weights with few rows: the kernels of
-// moe_layer_few, and moe_expert_gemm / moe_expert_gemm_swiglu for a few rows in
-// all.  They are bound by reading the weights once.
+// moe_layer_few, and moe_expert_gemm / moe_expert_gemm_swiglu for few rows
+// (few_rows).  They are bound by reading the weights once.
 //
 // The weights are the 128-row operand of the tensor cores and the rows of x (or
 // h) the narrow one of 16 columns: a product costs what its real rows cost,
@@ -15,16 +15,17 @@
 // come through registers, by four warps a block, are late where there are many: 64
 // tokens on 64 experts (hidden 7168, experts of 2048) 521 us, now 415 to 420.
 // Where there are fewer units than that, the CTAs of a cluster share each one's k
-// blocks (thin_parts).
+// blocks (thin_parts), and then its rows: each adds up and stores its own of them.
 //
 // Measured, hidden 7168, experts of 2048, top-8: four tokens of 256 experts 208 to
-// 221 us (30 to 32 experts' weights, 6.1 to 6.8 TB/s), 32 tokens on 64 experts 401 to 411 us (6.9 TB/s, a
-// copy's rate).  One token, hidden 2048, experts of 768: 16.3 us, of which the weights
-// are 5.6 at a copy's rate (13.9 where L2 has them); the rest is finding the rows (1 us), the clusters'
-// exchanges (1.3 and 1.5), the activation (1.8, instruction fetches; 2.8 with its
-// columns unrolled) and the second kernel's wait for the first.  The same layer on warp-level products (mma.sync, weights loaded straight
-// to registers) took 311 and 1446 us: an e4m3 mma.sync is a score of instructions
-// here, 340 a 2 KB tile in all, against 160 a 16 KB tile.
+// 221 us (30 to 32 experts' weights, 6.1 to 6.8 TB/s), 32 tokens on 64 experts 401
+// to 411 us (6.8 to 6.9 TB/s, a copy's rate).  One token, hidden 2048, experts of
+// 768: 16.2 us (13.9 where L2 has the weights), of which they are 5.6 at a copy's
+// rate; the rest is two launches, finding the rows (1 us each), the first blocks' way
+// from HBM (1 us each) and the clusters' barriers.  The same layer on warp-level
+// products (mma.sync, weights loaded straight to registers) took 311 and 1446 us
+// for four tokens and 32: an e4m3 mma.sync is a score of instructions here, 340 a
+// 2 KB tile in all, against 160 a 16 KB tile.
 #include <cooperative_groups.h>
 
 #include "bf16.cuh"
@@ -51,7 +52,7 @@ enum class Thin { kUp, kUpCoded, kDown, kGemm, kSwiglu };
 // stages, or one could miss two phases of a stage's barrier.  Eight warps leave two
 // CTAs 128 registers a thread.
 constexpr int kThinTma = 4, kThinMma = 5, kRowWarp = 6, kRowWarps = 2;
-constexpr int kThinThreads = 32 * (kRowWarp + kRowWarps);
+constexpr int kThinWarps = kRowWarp + kRowWarps, kThinThreads = 32 * kThinWarps;
 constexpr int kTileBytes = 128 * 128;
 
 struct ThinArgs {
@@ -59,7 +60,6 @@ struct ThinArgs {
     int ntok, E, R, H, inter;
     bool by_expert;  // gate and up: units are experts, not assignments
     int passes;      // units of 16 rows that an expert may need
-    bool push;       // a cluster's parts send their sums to the first one's inbox
     const uint16_t *x;
     const int32_t *idx;
     const float *topk_w;
@@ -74,7 +74,6 @@ struct ThinArgs {
     uint16_t *y;
     // both
     int n, k;  // outputs and inputs of the product
-    int most;  // rows that a unit can have
     const float *w_s;
     int32_t *status;
 };
@@ -87,10 +86,6 @@ __host__ __device__ constexpr bool thin_pair(Thin m) { return thin_up(m) || m ==
 // tokens 15.8 and 16.1 (8 experts of 768, hidden 2048, in L2), 98.9 and 100.6 (32 of 2048,
 // 4096); with room for eight rows eight tokens 18.1 and 16.1, and fewer tokens 2% more.
 constexpr int kOwnRows = 4;
-
-// Columns of a product: rows of one expert that meet its weights at a time.  A
-// unit with more is several units, whose reads of the weights meet in L2.
-constexpr int kThinRowsAt = 16;
 
 // Accumulators in tensor memory: an item's way from its products to its sums
 // takes several times as long as the products of a few rows.
@@ -108,12 +103,11 @@ __host__ __device__ constexpr int thin_stage_bytes(Thin m) {
 template <int kStages>
 struct alignas(16) ThinShared {
     float scale[kStages][kThinRowsAt];  // of the rows' pieces in each stage
-    uint64_t full[kStages], empty[kStages], tfull[kAccs], tempty[kAccs], drain, inbox;
+    uint64_t full[kStages], empty[kStages], tfull[kAccs], tempty[kAccs], drain;
     uint32_t tmem;
     int stop, total, unit[3];
     unsigned chosen[2];
     int wsum[32];
-    uint32_t peak[4][kThinRowsAt];
     int list[MOE_FEW_MAX_TOKENS];  // gate and up of few tokens: the expert's assignments,
     int token[MOE_FEW_MAX_TOKENS];  // one a token; and their tokens
 };
@@ -138,10 +132,15 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     return (uint32_t)r * 128 + (uint32_t)((c ^ (r & 7)) << 4);
 }
 
-// One row's block of 128, four values a lane: a lane's codes, and the scale.
+// The maximum of a block of 128, four values a lane, as bits.
+__device__ __forceinline__ uint32_t warp_amax(float a, float b, float c, float d) {
+    return __reduce_max_sync(kFull,
+                             max(max(abs_bits(a), abs_bits(b)), max(abs_bits(c), abs_bits(d))));
+}
+
+// One row's block of x: a lane's codes, and the scale.
 __device__ __forceinline__ uint32_t code_row(float a, float b, float c, float d, float *scale) {
-    *scale = block_scale(__reduce_max_sync(
-        kFull, max(max(abs_bits(a), abs_bits(b)), max(abs_bits(c), abs_bits(d)))));
+    *scale = block_scale(warp_amax(a, b, c, d));
     return *scale == 0.0f ? 0u : code4(a, b, c, d, *scale);
 }
 
@@ -192,14 +191,11 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             mbar_init(&s.tempty[i], 4);
         }
         mbar_init(&s.drain, 1);
-        mbar_init(&s.inbox, max(1, 4 * (parts - 1)));
         s.stop = 0;
         fence_mbar_init();
         tma_prefetch_map(&map_w);
     }
     if (warp == kThinMma) tc_alloc<kCols>(&s.tmem);
-    // a part's inbox is there before another sends to it: waited for at the end
-    if (parts > 1 && p.push) cluster.barrier_arrive();
     // the kernel before kUpCoded and kDown is this call's, which has waited: only
     // what it made is waited for, where it is read
     constexpr bool kLate = kMode == Thin::kDown || kMode == Thin::kUpCoded;
@@ -207,7 +203,6 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const auto leave = [&]() {  // nothing to do: all threads
         __syncthreads();
-        if (parts > 1 && p.push) cluster.barrier_wait();
         if (warp == kThinMma) tc_free<kCols>(s.tmem);
         // not done before the kernel that it follows is
         if constexpr (kLate) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -558,30 +553,8 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     tc_fence_after();
     if (warp == kThinMma) tc_free<kCols>(tmem);
 
-    const bool push = parts > 1 && p.push;
-    if (push) cluster.barrier_wait();  // from the set-up
     if constexpr (kMode == Thin::kDown) {
         // the parts of the experts' run, added in the cluster's order
-        if (push) {
-            float *inbox = reinterpret_cast<float *>(experts + thin_entries(A, p.E));
-            if (part > 0) {
-                if (warp >= 4) return;
-                float *to = cluster.map_shared_rank(inbox, 0) + (part - 1) * p.ntok * 128;
-                for (int t = 0; t < p.ntok; ++t) to[t * 128 + tid] = sums[t * 128 + tid];
-                __syncwarp();
-                if (lane == 0) mbar_arrive_release_cluster(dsmem_addr(&s.inbox, 0));
-                return;
-            }
-            if (warp >= 4) return;
-            const bool ok = __all_sync(kFull, mbar_wait_cluster(&s.inbox, 0));
-            if (!ok && tid == 0 && p.status) flag(p.status, MOE_ST_TIMEOUT);
-            for (int t = 0; t < p.ntok; ++t) {
-                float v = sums[t * 128 + tid];
-                for (int q = 1; q < parts; ++q) v += inbox[((q - 1) * p.ntok + t) * 128 + tid];
-                p.out[(size_t)t * p.H + blk * 128 + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-            }
-            return;
-        }
         if (parts > 1) cluster.sync();
         for (int i = part * kThinThreads + tid; i < p.ntok * 64; i += parts * kThinThreads) {
             float2 v = make_float2(0.0f, 0.0f);
@@ -596,106 +569,69 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         if (parts > 1) cluster.sync();  // no part goes while it is read
         return;
     }
-    // parts of k: the others' sums come to the first one's inbox, or wait in
-    // their rings for it to fetch them
-    if (parts > 1) {
-        float *left = push ? reinterpret_cast<float *>(&s + 1) : reinterpret_cast<float *>(ring);
-        const int rows = push ? min(NMAX, p.most) : NMAX;  // columns of a part's place
-        if (warp < 4 && part > 0) {
-            float *to = push ? cluster.map_shared_rank(left, 0) + (part - 1) * kHalves * rows * 128 : left;
+    // The sums go through the ring, [half][row][128], so that a warp can take a row:
+    // the row's block maximum is then its own, and the rows are shared by all warps of
+    // all parts (which fetch what the others have of theirs).  A row after another
+    // by the four warps with the sums was 0.2 us a row.
+    float *left = reinterpret_cast<float *>(ring);
+    if (warp < 4)
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-                for (int j = 0; j < NMAX; ++j)
-                    if (j < m) to[(h * rows + j) * 128 + tid] = acc[h][j];
-            if (push) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive_release_cluster(dsmem_addr(&s.inbox, 0));
+            for (int j = 0; j < NMAX; ++j)
+                if (j < m) left[(h * NMAX + j) * 128 + tid] = acc[h][j];
+    if (parts > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+    for (int j = part + warp * parts; j < m; j += parts * kThinWarps) {
+        float4 v[kHalves];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+            const float *at = left + (h * NMAX + j) * 128 + lane * 4;
+            v[h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int q = 0; q < parts; ++q) {
+                const float4 o = *reinterpret_cast<const float4 *>(
+                    parts > 1 ? cluster.map_shared_rank(at, q) : at);
+                v[h].x += o.x;
+                v[h].y += o.y;
+                v[h].z += o.z;
+                v[h].w += o.w;
             }
         }
-        if (!push) cluster.sync();
-        if (warp < 4 && part == 0) {
-            if (push) {
-                const bool ok = __all_sync(kFull, mbar_wait_cluster(&s.inbox, 0));
-                if (!ok && tid == 0 && p.status) flag(p.status, MOE_ST_TIMEOUT);
-            }
-            for (int q = 1; q < parts; ++q) {
-                const float *o = push ? left + (q - 1) * kHalves * rows * 128
-                                      : cluster.map_shared_rank(left, q);
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                    for (int j = 0; j < NMAX; ++j)
-                        if (j < m) acc[h][j] += o[(h * rows + j) * 128 + tid];
-            }
-        }
-        if (!push) cluster.sync();  // no part goes while it is read
-    }
-    if (part > 0 || warp >= 4) return;
-    const auto row_of = [&](int j) {
-        return thin_up(kMode) ? (size_t)s.list[r0 + j] : (size_t)(row0 + j);
-    };
-    // The columns go through the thread's own words of the ring to be taken one
-    // after another: sixteen copies of what follows cost 2 us of instruction
-    // fetches, as much as all else after the products.
-    float *own = reinterpret_cast<float *>(ring) + tid;  // [half][column], 128 apart
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-        for (int j = 0; j < NMAX; ++j)
-            if (j < m) own[(h * NMAX + j) * 128] = acc[h][j];
-    if constexpr (!kPair) {
-#pragma unroll 1
-        for (int j = 0; j < m; ++j)
-            p.y[row_of(j) * p.n + blk * 128 + tid] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(own[j * 128]));
-    } else {
-        const int I = p.n >> 1;
-#pragma unroll 1
-        for (int j = 0; j < m; ++j) {
-            const float h = silu_mul(own[j * 128], own[(NMAX + j) * 128]);
-            own[j * 128] = h;
-            const uint32_t am = __reduce_max_sync(kFull, abs_bits(h));
-            if (lane == 0) s.peak[warp][j] = am;
-        }
-        bar_named(1, 128);
-#pragma unroll 1
-        for (int j = 0; j < m; ++j) {
-            const float scale = block_scale(
-                max(max(s.peak[0][j], s.peak[1][j]), max(s.peak[2][j], s.peak[3][j])));
+        const size_t row = thin_up(kMode) ? (size_t)s.list[r0 + j] : (size_t)(row0 + j);
+        if constexpr (!kPair) {
+            *reinterpret_cast<uint2 *>(p.y + row * p.n + blk * 128 + lane * 4) =
+                make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[0].z, v[0].w));
+        } else {
+            const float4 g = v[0], u = v[kHalves - 1];
+            const float a = silu_mul(g.x, u.x), b = silu_mul(g.y, u.y), c = silu_mul(g.z, u.z),
+                        d = silu_mul(g.w, u.w);
+            const float scale = block_scale(warp_amax(a, b, c, d));
             float first;
             const float inv = code_factor(scale, &first);  // as the 128-row tiles code it
-            p.h_q[row_of(j) * I + blk * 128 + tid] =
-                (uint8_t)code4_by(own[j * 128] * first, 0.0f, 0.0f, 0.0f, inv);
-            if (tid == 0) p.h_s[row_of(j) * (I >> 7) + blk] = scale;
+            const int I = p.n >> 1;
+            *reinterpret_cast<uint32_t *>(p.h_q + row * I + blk * 128 + lane * 4) =
+                code4_by(a * first, b * first, c * first, d * first, inv);
+            if (lane == 0) p.h_s[row * (I >> 7) + blk] = scale;
         }
     }
+    if (parts > 1) cluster.sync();  // no part goes while it is read
 }
 
 // ------------------------------------------------------------ host
 
-// Room for the sums that the parts of a cluster send to the first one: what two
-// CTAs an SM leave, or all of an SM's where half the SMs have a CTA at most (a
-// cluster has to find its SMs in one GPC: at 128 CTAs of a whole SM each, the
-// last cluster of eight waited for another to end).  Where they are more, the
-// first part fetches them, with two barriers of the cluster around (about 2 us
-// against 1.3).
-constexpr int kPushBytes = 7 * 1024, kMostSmem = 232448, kTwoSmem = 113 * 1024;
+constexpr int kMostSmem = 232448, kTwoSmem = 113 * 1024;  // a CTA's; of two an SM
 
 template <Thin kMode, int kStages = thin_stages(kMode)>
 static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, int parts,
                                size_t more_smem, cudaStream_t st) {
-    const size_t inbox = (size_t)(parts - 1) * 512 *
-                         (kMode == Thin::kDown ? p.ntok : (thin_pair(kMode) ? 2 : 1) * p.most);
     constexpr size_t kFixed = thin_fixed_smem<kMode, kStages>();
-    const bool alone = (int64_t)grid.x * grid.y * parts * 2 <= sm_count();
-    p.push = inbox <= (alone ? kMostSmem - kFixed - more_smem : kPushBytes);
-    if (p.push) more_smem += inbox;
     const auto kern = k_thin<kMode, kStages>;
-    static_assert(kFixed + kPushBytes <= kTwoSmem, "two CTAs an SM");
+    static_assert(kFixed <= kTwoSmem, "two CTAs an SM");
     static_assert(thin_fixed_smem<Thin::kDown, thin_stages(Thin::kDown)>() +
-                          thin_lists_smem(MOE_FEW_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOPK) +
-                          kPushBytes <=
+                          thin_lists_smem(MOE_FEW_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOPK) <=
                       kMostSmem,
                   "a CTA's shared memory");
     static LaunchMemo memo;
@@ -724,11 +660,20 @@ static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, in
     return cudaLaunchKernelEx(&cfg, kern, p, map);
 }
 
-// CTAs that share a unit's k blocks: as many as the SMs hold at two each, eight
-// at most, each with two blocks at least.
-static int thin_parts(int64_t units, int64_t blocks) {
+// Units of 16 rows that `rows` rows of at most `experts` experts can be.
+static int64_t thin_units(int rows, int experts, int passes) {
+    const int most = experts + rows / kThinRowsAt, all = experts * passes;
+    return most < all ? most : all;
+}
+
+// CTAs that share a unit's k blocks: as many as the SMs hold at two each, eight at
+// most, with a block each at least and one CTA for two or three blocks (us: 2048 x
+// 256 3.6 and 4.1 with two; 2048 x 512 4.4 with two and 4.1 with four).  `grid` units,
+// those without rows among them, are not more than four an SM.
+static int thin_parts(int64_t units, int64_t grid, int64_t blocks) {
     int parts = 1;
-    while (parts < 8 && units * parts * 2 <= 2 * (int64_t)sm_count() && blocks >= 4 * parts)
+    while (parts < 8 && blocks >= 4 && blocks >= 2 * parts && units * parts * 2 <= 2 * (int64_t)sm_count() &&
+           grid * parts * 2 <= 4 * (int64_t)sm_count())
         parts *= 2;
     return parts;
 }
@@ -755,10 +700,9 @@ cudaError_t launch_thin_product(int N, int E, int cap, int n, int k, const uint8
     p.k = k;
     p.status = status;
     const int rows = N * cap, units = E < rows ? E : rows;
-    p.passes = (rows + kThinRowsAt - 1) / kThinRowsAt;
+    p.passes = (cap + kThinRowsAt - 1) / kThinRowsAt;
     const dim3 grid((unsigned)(h_q ? n >> 8 : n >> 7), (unsigned)(units * p.passes));
-    const int parts = thin_parts((int64_t)grid.x * units, k >> 7);
-    p.most = rows < kThinRowsAt ? rows : kThinRowsAt;
+    const int parts = thin_parts(grid.x * thin_units(rows, units, p.passes), (int64_t)grid.x * grid.y, k >> 7);
     if (h_q) return launch_thin<Thin::kSwiglu>(p, map, grid, parts, 0, st);
     return launch_thin<Thin::kGemm>(p, map, grid, parts, 0, st);
 }
@@ -791,8 +735,7 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.n = 2 * p.inter;
     p.k = p.H;
     p.w_s = w13_s;
-    p.most = p.ntok < kThinRowsAt ? p.ntok : kThinRowsAt;
-    const int up_parts = thin_parts((int64_t)gup.x * units, p.H >> 7);
+    const int up_parts = thin_parts(gup.x * thin_units(A, units, p.passes), (int64_t)gup.x * gup.y, p.H >> 7);
     if (p.ntok <= kOwnRows) {
         err = launch_thin<Thin::kUp>(p, up, gup, up_parts, 0, st);
     } else {
@@ -806,7 +749,7 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.k = p.inter;
     p.w_s = w2_s;
     const dim3 gdown((unsigned)(p.H >> 7));
-    const int parts = thin_parts(gdown.x, (int64_t)units * (p.inter >> 7));
+    const int parts = thin_parts(gdown.x, gdown.x, (int64_t)units * (p.inter >> 7));
     const size_t lists = thin_lists_smem(p.ntok, p.E, p.R);
     constexpr size_t kFixed = thin_fixed_smem<Thin::kDown, thin_stages(Thin::kDown)>();
     if (kFixed + lists <= kTwoSmem) return launch_thin<Thin::kDown>(p, down, gdown, parts, lists, st);

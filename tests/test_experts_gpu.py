@@ -247,3 +247,25 @@ def test_few_tiles_share_k_in_groups():
     sh = m.make_shape(2, 140, 6, 1, 128, 140)
     check(sh, n, k, o.make_rows(gen, 280, k), layout(sizes, 140), o.make_weights(gen, 6, n, k),
           True)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("M,n,k", [(129, 2560, 4096), (300, 1024, 4224), (40, 7168, 4096),
+                                   (33, 20480, 128)])
+def test_wide_products_of_a_few_tiles(M, n, k, swiglu):
+    gen = torch.Generator().manual_seed(M + n + k)
+    check(m.make_shape(1, M, 1, 1, 128, M), n, k, o.make_rows(gen, M, k), None,
+          o.make_weights(gen, 1, n, k), swiglu)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("sizes,cap,n,k", [
+    ([[1000]], 0, 256, 512), ([[16, 17]], 0, 512, 1024), ([[40, 0, 17, 33]], 0, 256, 640),
+    ([[5, 0], [31, 1], [0, 48]], 48, 256, 2048), ([[0, 0, 65, 0, 0, 1]], 66, 256, 128),
+])
+def test_more_rows_than_meet_the_weights_at_a_time(sizes, cap, n, k, swiglu):
+    N, Er = len(sizes), len(sizes[0])
+    cap = cap or max(sum(s) for s in sizes)
+    gen = torch.Generator().manual_seed(N + Er + n + k)
+    check(m.make_shape(N, cap, N * Er, 1, 128, cap), n, k, o.make_rows(gen, N * cap, k),
+          layout(sizes, cap), o.make_weights(gen, N * Er, n, k), swiglu)
