@@ -479,7 +479,7 @@ static int product_parts(int64_t tiles, int blocks) {
 
 static cudaError_t launch_product(Product p, const uint8_t *a_q, const uint8_t *w_q,
                                   cudaStream_t st) {
-    if (few_rows(p.N, p.cap, p.E, p.n))
+    if (few_rows(p.N, p.cap, p.E, p.n, p.k, p.h_q != nullptr))
         return launch_thin_product(p.N, p.E, p.cap, p.n, p.k, a_q, p.a_s, p.grp_off, w_q, p.w_s, p.y,
                                    p.h_q, p.h_s, p.status, st);
     CUtensorMap map_a, map_w;

@@ -220,12 +220,15 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     unsigned *who = reinterpret_cast<unsigned *>(weight + A);  // [E][2]
     int *place = reinterpret_cast<int *>(who + 2 * p.E), *start = place + p.E;
     int *experts = start + thin_entries(A, p.E);
-    // CTAs with the same weights and other rows are neighbours: one reads HBM, the
-    // others L2 (16 experts, 64 tokens, 16 rows an expert on average, hidden 7168: 146 us;
-    // 158 with all units' first 16 rows first; 8 experts with 8 rows at most 17.6 and 17.0)
-    const int unit = blockIdx.y / p.passes, r0 = blockIdx.y % p.passes * NMAX;
+    int r0 = 0;  // the unit's first row of its expert's
     int U = 0;  // kDown: entries
     if constexpr (thin_up(kMode)) {
+        // CTAs with the same weights and other rows are neighbours: one reads HBM, the
+        // others L2 (16 experts, 64 tokens, 16 rows an expert on average, hidden 7168: 146
+        // us; 158 with all experts' first 16 rows first; 8 experts with 8 rows at most 17.6
+        // and 17.0)
+        const int unit = blockIdx.y / p.passes;
+        r0 = blockIdx.y % p.passes * NMAX;
         ids = reinterpret_cast<int *>(ring);  // the ring is not in use yet
         int bad = 0;
         for (int i = tid; i < A; i += kThinThreads) {
@@ -306,11 +309,11 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             weight[at] = w;
         }
     } else {
-        // the unit-th expert that has rows
+        // the unit-th 16 rows of one expert
         if (tid == 0) s.unit[0] = -1;
         __syncthreads();
         int seen = 0;
-        const int Er = p.E / p.N;
+        const int Er = p.E / p.N, unit = blockIdx.y;
         for (int e0 = 0; e0 < p.E; e0 += kThinThreads) {
             const int x = e0 + tid;
             int b = 0, c = 0;
@@ -321,19 +324,20 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             } else if (x < p.E) {
                 c = p.cap;
             }
-            const int at = seen + block_inclusive_scan(c > 0, s.wsum, &s.total);
-            if (c > 0 && at == unit + 1) {
+            const int mine = (c + NMAX - 1) / NMAX;
+            const int before = seen + block_inclusive_scan(mine, s.wsum, &s.total) - mine;
+            if (before <= unit && unit < before + mine) {
                 s.unit[0] = x;
-                s.unit[1] = b;
-                s.unit[2] = c;
+                s.unit[1] = b + (unit - before) * NMAX;
+                s.unit[2] = c - (unit - before) * NMAX;
             }
             seen += s.total;
             __syncthreads();
         }
         e = s.unit[0];
-        if (e < 0 || s.unit[2] <= r0) return leave();
-        m = min(s.unit[2] - r0, NMAX);
-        row0 = (long long)(e / Er) * p.cap + s.unit[1] + r0;
+        if (e < 0) return leave();
+        m = min(s.unit[2], NMAX);
+        row0 = (long long)(e / Er) * p.cap + s.unit[1];
     }
 
     fence_async_smem();  // gate and up: the ids lay where the ring is
@@ -660,20 +664,13 @@ static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, in
     return cudaLaunchKernelEx(&cfg, kern, p, map);
 }
 
-// Units of 16 rows that `rows` rows of at most `experts` experts can be.
-static int64_t thin_units(int rows, int experts, int passes) {
-    const int most = experts + rows / kThinRowsAt, all = experts * passes;
-    return most < all ? most : all;
-}
-
 // CTAs that share a unit's k blocks: as many as the SMs hold at two each, eight at
 // most, with a block each at least and one CTA for two or three blocks (us: 2048 x
-// 256 3.6 and 4.1 with two; 2048 x 512 4.4 with two and 4.1 with four).  `grid` units,
-// those without rows among them, are not more than four an SM.
-static int thin_parts(int64_t units, int64_t grid, int64_t blocks) {
+// 256 3.6 and 4.1 with two; 2048 x 512 4.4 with two and 4.1 with four).
+static int thin_parts(int64_t units, int64_t blocks) {
     int parts = 1;
-    while (parts < 8 && blocks >= 4 && blocks >= 2 * parts && units * parts * 2 <= 2 * (int64_t)sm_count() &&
-           grid * parts * 2 <= 4 * (int64_t)sm_count())
+    while (parts < 8 && blocks >= 4 && blocks >= 2 * parts &&
+           units * parts * 2 <= 2 * (int64_t)sm_count())
         parts *= 2;
     return parts;
 }
@@ -699,10 +696,9 @@ cudaError_t launch_thin_product(int N, int E, int cap, int n, int k, const uint8
     p.n = n;
     p.k = k;
     p.status = status;
-    const int rows = N * cap, units = E < rows ? E : rows;
-    p.passes = (cap + kThinRowsAt - 1) / kThinRowsAt;
-    const dim3 grid((unsigned)(h_q ? n >> 8 : n >> 7), (unsigned)(units * p.passes));
-    const int parts = thin_parts(grid.x * thin_units(rows, units, p.passes), (int64_t)grid.x * grid.y, k >> 7);
+    const int units = thin_units(N, cap, E);
+    const dim3 grid((unsigned)(h_q ? n >> 8 : n >> 7), (unsigned)units);
+    const int parts = thin_parts((int64_t)grid.x * units, k >> 7);
     if (h_q) return launch_thin<Thin::kSwiglu>(p, map, grid, parts, 0, st);
     return launch_thin<Thin::kGemm>(p, map, grid, parts, 0, st);
 }
@@ -735,7 +731,9 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.n = 2 * p.inter;
     p.k = p.H;
     p.w_s = w13_s;
-    const int up_parts = thin_parts(gup.x * thin_units(A, units, p.passes), (int64_t)gup.x * gup.y, p.H >> 7);
+// an expert's second and further 16 rows are A / 16 units more at most
+    const int64_t real = p.passes > 1 ? units + A / kThinRowsAt : units;
+    const int up_parts = thin_parts((real < gup.y ? real : gup.y) * gup.x, p.H >> 7);
     if (p.ntok <= kOwnRows) {
         err = launch_thin<Thin::kUp>(p, up, gup, up_parts, 0, st);
     } else {
@@ -749,7 +747,7 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.k = p.inter;
     p.w_s = w2_s;
     const dim3 gdown((unsigned)(p.H >> 7));
-    const int parts = thin_parts(gdown.x, gdown.x, (int64_t)units * (p.inter >> 7));
+    const int parts = thin_parts(gdown.x, (int64_t)units * (p.inter >> 7));
     const size_t lists = thin_lists_smem(p.ntok, p.E, p.R);
     constexpr size_t kFixed = thin_fixed_smem<Thin::kDown, thin_stages(Thin::kDown)>();
     if (kFixed + lists <= kTwoSmem) return launch_thin<Thin::kDown>(p, down, gdown, parts, lists, st);

@@ -12,16 +12,27 @@ namespace moe {
 // several CTAs, whose reads of the weights meet in L2.
 constexpr int kThinRowsAt = 16;
 
-// Whether a product goes this way: few rows in all, or few enough groups of 16 of
-// an expert that all their CTAs are on the SMs at once.  us here against the
-// 128-row tiles: 7168 x 2048 one row 7.3 : 9.4, 32 rows 8.5 : 9.8, 96 (not so) 16.4 :
-// 10.1; 7168 x 7168 32 rows 16.1 : 19.2, 48 (not so) 22.9 : 19.3; 16 experts with
-// 32 rows in all 39 : 41; 512 x 2048 256 rows 6.2 : 8.7; 128 x 7168 1024 rows 10.4 :
-// 17.4; gate/up of 2048 by 7168 16 rows 11.7 : 20.3, 64 rows 14.1 : 20.3.
-inline bool few_rows(int64_t N, int64_t cap, int64_t E, int64_t n) {
+// Groups of 16 rows of an expert that there can be, at least one for each expert
+// with rows.
+inline int64_t thin_units(int64_t N, int64_t cap, int64_t E) {
+    const int64_t rows = N * cap, used = rows < E ? rows : E;
+    return (rows - used) / kThinRowsAt + used;
+}
+
+// Whether a product goes this way.  us here against the 128-row tiles:
+//   32 rows in all: 7168 x 2048 8.5 : 9.8; 7168 x 7168 16.1 : 19.2; 16 experts of
+//   7168 x 2048 39 : 41; gate/up of 2048 by 7168 11.8 : 20.2
+//   or all CTAs on the SMs at once: 4096 x 4096, 64 rows 10.6 : 14.1; 128 x 7168, 1024
+//   rows 10.4 : 17.4; gate/up of 2048 by 7168, 64 rows 13.9 : 20.3; (not so) 7168 x
+//   2048, 96 rows 16.3 : 10.1
+//   or at most eight rows an expert, and 512 KB of weights to each CTA: 32 experts'
+//   gate/up of 2048 by 7168, 128 rows 145 : 157, of 128 uneven ones of 768 by 2048, 1021
+//   rows 64.7 : 65.4; 32 of 2048 x 7168, 256 rows 76.5 : 80.1; (not so, 12 rows each)
+//   the last, uneven 83.8 : 80.3; (not so, 96 KB) 128 of 2048 x 768, 512 rows 48 : 43
+inline bool few_rows(int64_t N, int64_t cap, int64_t E, int64_t n, int64_t k, bool pair) {
     const int64_t rows = N * cap;
-    const int64_t units = (rows < E ? rows : E) * ((cap + kThinRowsAt - 1) / kThinRowsAt);
-    return rows <= 2 * kThinRowsAt || (n >> 7) * units < sm_count();
+    return rows <= 32 || (n >> 7) * thin_units(N, cap, E) < sm_count() ||
+           (rows <= 8 * E && (pair ? 2 : 1) * k >= 4096);
 }
 
 // y (bf16) or, where h_q is given, the coded activation of the pair of weight

@@ -269,3 +269,15 @@ def test_more_rows_than_meet_the_weights_at_a_time(sizes, cap, n, k, swiglu):
     gen = torch.Generator().manual_seed(N + Er + n + k)
     check(m.make_shape(N, cap, N * Er, 1, 128, cap), n, k, o.make_rows(gen, N * cap, k),
           layout(sizes, cap), o.make_weights(gen, N * Er, n, k), swiglu)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("sizes,cap,n,k", [
+    ([[0, 1, 19, 0, 33, 2, 0, 5]], 64, 2560, 4096), ([[7, 0, 16, 1], [17, 12, 0, 0]], 30, 2560, 4096),
+    ([[1, 0] * 150], 2000, 256, 2048),
+])
+def test_few_rows_an_expert(sizes, cap, n, k, swiglu):
+    N, Er = len(sizes), len(sizes[0])
+    gen = torch.Generator().manual_seed(N + Er + n + k)
+    check(m.make_shape(N, cap, N * Er, 1, 128, cap), n, k, o.make_rows(gen, N * cap, k),
+          layout(sizes, cap), o.make_weights(gen, N * Er, n, k), swiglu)
