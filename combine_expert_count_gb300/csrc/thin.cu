@@ -666,7 +666,9 @@ static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, in
 
 // CTAs that share a unit's k blocks: as many as the SMs hold at two each, eight at
 // most, with a block each at least and one CTA for two or three blocks (us: 2048 x
-// 256 3.6 and 4.1 with two; 2048 x 512 4.4 with two and 4.1 with four).
+// 256 3.6 and 4.1 with two; 2048 x 512 4.4 with two and 4.1 with four).  Powers of
+// two: clusters of five for four cost a layer of four tokens 211 us for 185 (hidden
+// 7168), their CTAs not filling the SMs in pairs.
 static int thin_parts(int64_t units, int64_t blocks) {
     int parts = 1;
     while (parts < 8 && blocks >= 4 && blocks >= 2 * parts &&
