@@ -148,7 +148,8 @@ __device__ __forceinline__ uint32_t code_row(float a, float b, float c, float d,
 // codes and the scale in the 256 bytes that the block's outputs take (so x and out
 // may be the same).
 constexpr int kCodedBlock = 256, kCodeWarps = 4;
-__global__ void __launch_bounds__(32 * kCodeWarps) k_code_rows(int blocks, const uint16_t *x, uint8_t *out) {
+__global__ void __launch_bounds__(32 * kCodeWarps)
+    k_code_rows(int blocks, const uint16_t *x, uint8_t *out) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int i = blockIdx.x * kCodeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -563,12 +564,13 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         for (int i = part * kThinThreads + tid; i < p.ntok * 64; i += parts * kThinThreads) {
             float2 v = make_float2(0.0f, 0.0f);
             for (int q = 0; q < parts; ++q) {
-                const float2 o = *reinterpret_cast<const float2 *>(cluster.map_shared_rank(sums + i * 2, q));
+                const float2 o =
+                    *reinterpret_cast<const float2 *>(cluster.map_shared_rank(sums + i * 2, q));
                 v.x += o.x;
                 v.y += o.y;
             }
-            *reinterpret_cast<uint32_t *>(p.out + (size_t)(i >> 6) * p.H + blk * 128 + (i & 63) * 2) =
-                pack_bf16x2(v.x, v.y);
+            uint16_t *to = p.out + (size_t)(i >> 6) * p.H + blk * 128 + (i & 63) * 2;
+            *reinterpret_cast<uint32_t *>(to) = pack_bf16x2(v.x, v.y);
         }
         if (parts > 1) cluster.sync();  // no part goes while it is read
         return;
