@@ -583,6 +583,7 @@ class MoeBuffers:
         self.out = e((N, T, H), torch.bfloat16)
         # moe_dispatch_signalled's group counters and flags (zero between calls)
         self.sig = torch.zeros(int(z.bytes_sig) // 4, dtype=torch.int32, device=d)
+        self._h = {}  # activations() by width
 
     def partial_rows(self) -> torch.Tensor:
         """The send-side reduction's partial rows [N][N][T][H] bf16, allocated
@@ -593,8 +594,9 @@ class MoeBuffers:
         return self.part
 
     def device_bytes(self) -> int:
-        return sum(t.numel() * t.element_size() for t in vars(self).values()
-                   if isinstance(t, torch.Tensor))
+        held = [*vars(self).values(), *(t for pair in self._h.values() for t in pair)]
+        return sum(t.numel() * t.element_size()
+                   for t in {id(t): t for t in held if isinstance(t, torch.Tensor)}.values())
 
     def route(self, topk_idx, stream=None, fused: bool = True) -> None:
         """Counts, offsets and slots: one ``moe_route`` launch, or
@@ -654,16 +656,27 @@ class MoeBuffers:
         """The grouped-GEMM stand-in (identity or per-expert scale)."""
         moe_expert_standin(self.shape, mode, self.grp_q, self.grp_s, self.grp_off, self.y, stream)
 
+    def activations(self, inter: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+        """The coded activations [N][cap][inter] and scales [N][cap][inter/128]
+        of experts ``inter`` wide, allocated at that width's first use, on the
+        stream that uses them (so that no earlier work of another stream is
+        still on their memory), and kept as long as this object: a captured graph
+        or work under way may hold those of another width."""
+        if inter not in self._h:
+            rows, d = (self.N, self.cap), self.y.device
+            with torch.cuda.stream(stream):
+                self._h[inter] = (torch.empty((*rows, inter), dtype=torch.uint8, device=d),
+                                  torch.empty((*rows, inter // 128), dtype=torch.float32,
+                                              device=d))
+        return self._h[inter]
+
     def experts(self, w13_q, w13_s, w2_q, w2_s, stream=None) -> None:
         """The experts between ``dispatch`` and ``combine``: moe_expert_gemm_swiglu
         of the grouped rows and moe_expert_gemm into ``y``.  The weights are
         [E][2*inter][H] and [E][H][inter] e4m3 with their 128 x 128 block scales;
-        the coded activations (``h_q``, ``h_s``) are allocated on first use."""
+        the coded activations (``h_q``, ``h_s``) are ``activations``'."""
         inter = w2_q.shape[-1]
-        if getattr(self, "h_q", None) is None or self.h_q.shape[-1] != inter:
-            rows, d = (self.N, self.cap), self.y.device
-            self.h_q = torch.empty((*rows, inter), dtype=torch.uint8, device=d)
-            self.h_s = torch.empty((*rows, inter // 128), dtype=torch.float32, device=d)
+        self.h_q, self.h_s = self.activations(inter, stream)
         moe_expert_gemm_swiglu(self.shape, inter, self.H, self.grp_q, self.grp_s, self.grp_off,
                                w13_q, w13_s, self.h_q, self.h_s, self.status, stream)
         moe_expert_gemm(self.shape, self.H, inter, self.h_q, self.h_s, self.grp_off, w2_q, w2_s,

@@ -141,3 +141,42 @@ def test_calls_follow_each_other_on_a_stream():
             sync()
         return x
     assert torch.equal(chain(lambda: None), chain(torch.cuda.synchronize))
+
+
+def test_a_graph_keeps_its_activations_when_another_width_is_called():
+    """A captured layer is replayed after calls with other experts on the same
+    buffers and with new tensors in memory."""
+    gen = torch.Generator().manual_seed(13)
+    N, T, E, R, H = 2, 24, 8, 2, 512
+    x = o.bf16(torch.randn((N, T, H), generator=gen)).cuda()
+    idx = torch.rand((N, T, E), generator=gen).topk(R, dim=-1).indices.int().cuda()
+    w = torch.rand((N, T, R), generator=gen).cuda()
+    wide, narrow = ([t.cuda() for t in (*o.make_weights(gen, E, 2 * I, H),
+                                        *o.make_weights(gen, E, H, I))] for I in (512, 128))
+    buf = m.MoeBuffers(N, T, E, R, H)
+
+    def layer(weights, stream=None):
+        buf.dispatch(x, idx, stream=stream)
+        buf.experts(*weights, stream=stream)
+        return buf.combine(idx, w, stream=stream)
+    want = layer(wide).clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer(wide)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = layer(narrow, side)
+    torch.cuda.current_stream().wait_stream(side)
+    other = other.clone()
+    rows = N * buf.cap
+    # the sizes of the first width's buffers: what the allocator would give again
+    new = [torch.full((rows * 512,), 0x5C, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    new += [torch.full((rows * 16,), 0x5C, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(buf.out, want) and not torch.equal(other, want)
+    assert all((t == 0x5C).all() for t in new)
+    side.wait_stream(torch.cuda.current_stream())
+    again = layer(narrow, side)
+    side.synchronize()
+    assert torch.equal(again, other)
