@@ -167,7 +167,8 @@ __device__ __forceinline__ void store_rows64(uint8_t *stage, const uint32_t (&v)
 }
 
 // kSplit, for few tiles: the two CTAs of a cluster share one tile, each with half
-// of k; then each adds the other's sums for half of the rows and stores those.
+// of k; then each adds the other's sums for half of the rows and stores those (or
+// none where either gave up).
 template <bool kSwiglu, bool kSplit>
 __global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const Product p, const __grid_constant__ CUtensorMap map_a,
@@ -380,10 +381,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     left[(2 * i + 1) * 32] = f.y;
                 }
                 cluster.sync();
-                const bool mine = quad * parts / 4 == part;
-                for (int q = 0; mine && q < parts; ++q) {
-                    if (q == part) continue;
-                    const float *o = cluster.map_shared_rank(left, q);
+                const bool mine = (quad >> 1) == part;
+                if (mine) {
+                    const float *o = cluster.map_shared_rank(left, 1 - part);
 #pragma unroll
                     for (int i = 0; i < 64; ++i) {
                         const float2 f = unpack2(acc[i / 32][i % 32]);
@@ -391,8 +391,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                                                     __float_as_uint(f.y + o[(2 * i + 1) * 32]));
                     }
                 }
+                if (tid == 0 && *cluster.map_shared_rank(&s.stop, 1 - part)) *stop = 1;
                 cluster.sync();  // no CTA goes while it is read
-                if (!mine) break;
+                if (!mine || *stop) break;
             }
             if (!ok) break;
             const int rows = tile.rows - quad * 32;  // of this warp

@@ -438,6 +438,9 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         } else {
             // eight lanes a row, by asynchronous copies
             if constexpr (kLate) asm volatile("griddepcontrol.wait;" ::: "memory");
+            // where the kernel that makes h gave up, this one does too
+            const int before = kMode == Thin::kDown
+                                   ? *reinterpret_cast<volatile const int32_t *>(p.status) : 0;
             const int c = lane & 7;
             for (int it = rw; i0 + it < i1; it += kRowWarps) {
                 const int item = i0 + it, st = it % kStages;
@@ -465,6 +468,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
                 copies_arrive(&s.full[st]);
             }
             copies_wait();
+            if (before & MOE_ST_TIMEOUT) *stop = 1;
         }
     } else {
         // sums: lane = output 32 warp + lane of the block, column = row of x or h
@@ -558,9 +562,15 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     tc_fence_after();
     if (warp == kThinMma) tc_free<kCols>(tmem);
 
+    // Where a part gave up, the sums are not whole and no part stores any.  Each
+    // lane reads one part's flag; the answer is waited for where a warp has its sums.
+    const auto gave_up = [&]() {
+        return *(parts > 1 ? cluster.map_shared_rank(&s.stop, min(lane, parts - 1)) : &s.stop);
+    };
     if constexpr (kMode == Thin::kDown) {
         // the parts of the experts' run, added in the cluster's order
         if (parts > 1) cluster.sync();
+        const int any = gave_up();
         for (int i = part * kThinThreads + tid; i < p.ntok * 64; i += parts * kThinThreads) {
             float2 v = make_float2(0.0f, 0.0f);
             for (int q = 0; q < parts; ++q) {
@@ -569,6 +579,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
                 v.x += o.x;
                 v.y += o.y;
             }
+            if (__any_sync(kFull, any)) break;  // whole warps come here: 64 outputs a token
             uint16_t *to = p.out + (size_t)(i >> 6) * p.H + blk * 128 + (i & 63) * 2;
             *reinterpret_cast<uint32_t *>(to) = pack_bf16x2(v.x, v.y);
         }
@@ -590,6 +601,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         cluster.sync();
     else
         __syncthreads();
+    const int any = gave_up();
     for (int j = part + warp * parts; j < m; j += parts * kThinWarps) {
         float4 v[kHalves];
 #pragma unroll
@@ -606,6 +618,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
                 v[h].w += o.w;
             }
         }
+        if (__any_sync(kFull, any)) break;
         const size_t row = thin_up(kMode) ? (size_t)s.list[r0 + j] : (size_t)(row0 + j);
         if constexpr (!kPair) {
             *reinterpret_cast<uint2 *>(p.y + row * p.n + blk * 128 + lane * 4) =

@@ -474,7 +474,8 @@ int moe_rmsnorm(const moe_shape *shape, float eps, const uint16_t *x_bf16,
  *   p[i][c] = sum_b (a_s[i][b] * w_s[e][c/128][b]) * sum_{kk in b} a_q[i][kk] * w_q[e][c][kk]
  * Only N, E and cap of the shape matter here (the others are checked).  status
  * may be NULL; a kernel whose bounded waits run out sets MOE_ST_TIMEOUT there
- * (it is not cleared) and leaves outputs unwritten. */
+ * (it is not cleared) and leaves unwritten every output that those waits were
+ * for. */
 
 /* y[i][c] = bf16_rn(p[i][c]).
  *   a_q u8 [N][cap][k], a_s float [N][cap][k/128], y bf16 [N][cap][n] */
@@ -506,6 +507,7 @@ int moe_expert_gemm_swiglu(const moe_shape *shape, int inter, int k, const uint8
  * moe_combine, except that an expert's output is not rounded to bf16 before
  * the weighted sum.  Ids outside [0, E) are skipped (MOE_ST_BAD_EXPERT);
  * *status is cleared first.  N*T <= MOE_FEW_MAX_TOKENS (MOE_ENOTSUP beyond).
+ * A bounded wait that runs out sets MOE_ST_TIMEOUT; out then holds no outputs.
  *   w13_q u8 [E][2*inter][H], w13_s float [E][2*inter/128][H/128]
  *   w2_q  u8 [E][H][inter],   w2_s  float [E][H/128][inter/128]
  *   h_q u8 [N][T][R][inter], h_s float [N][T][R][inter/128]: scratch that the
