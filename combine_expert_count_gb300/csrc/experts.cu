@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     left[(2 * i + 1) * 32] = f.y;
                 }
                 cluster.sync();
+                if (tid == 0 && *cluster.map_shared_rank(&s.stop, 1 - part)) *stop = 1;
                 const bool mine = (quad >> 1) == part;
                 if (mine) {
                     const float *o = cluster.map_shared_rank(left, 1 - part);
@@ -391,7 +392,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                                                     __float_as_uint(f.y + o[(2 * i + 1) * 32]));
                     }
                 }
-                if (tid == 0 && *cluster.map_shared_rank(&s.stop, 1 - part)) *stop = 1;
                 cluster.sync();  // no CTA goes while it is read
                 if (!mine || *stop) break;
             }
