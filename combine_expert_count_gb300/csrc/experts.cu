@@ -316,6 +316,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             __syncwarp();
             if ((int)blockIdx.x < tiles) {  // the sum warps' two
                 cg::this_cluster().sync();
+                // where the other CTA gave up its sums are not whole
+                if (tid == kTmaWarp * 32 && *cg::this_cluster().map_shared_rank(&s.stop, 1 - part))
+                    *stop = 1;
+                __syncwarp();
                 cg::this_cluster().sync();
             }
         }
@@ -381,10 +385,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     left[(2 * i + 1) * 32] = f.y;
                 }
                 cluster.sync();
-                if (tid == 0 && *cluster.map_shared_rank(&s.stop, 1 - part)) *stop = 1;
-                const bool mine = (quad >> 1) == part;
-                if (mine) {
-                    const float *o = cluster.map_shared_rank(left, 1 - part);
+                const bool mine = quad * parts / 4 == part;
+                for (int q = 0; mine && q < parts; ++q) {
+                    if (q == part) continue;
+                    const float *o = cluster.map_shared_rank(left, q);
 #pragma unroll
                     for (int i = 0; i < 64; ++i) {
                         const float2 f = unpack2(acc[i / 32][i % 32]);

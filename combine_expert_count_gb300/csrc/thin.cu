@@ -564,9 +564,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
 
     // Where a part gave up, the sums are not whole and no part stores any.  Each
     // lane reads one part's flag; the answer is waited for where a warp has its sums.
-    const auto gave_up = [&]() {
-        return *(parts > 1 ? cluster.map_shared_rank(&s.stop, min(lane, parts - 1)) : &s.stop);
-    };
+    const auto gave_up = [&]() { return ld_dsmem(dsmem_addr(&s.stop, min(lane, parts - 1))); };
     if constexpr (kMode == Thin::kDown) {
         // the parts of the experts' run, added in the cluster's order
         if (parts > 1) cluster.sync();
