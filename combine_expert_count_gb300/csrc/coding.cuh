@@ -58,8 +58,9 @@ __device__ __forceinline__ uint32_t code4_by(float a, float b, float c, float d,
 // kTinyUp first.
 constexpr float kTinyScale = 0x1p-120f, kTinyUp = 0x1p100f;
 
-// The factor that takes a block's values to codes, 0 for a block of zeros, and,
-// where the scale is tiny, what to multiply the values by before it (else 1).
+// The factor that takes a block's values to codes and, where the scale is tiny,
+// what to multiply the values by before it (else 1).  A block with scale 0 has
+// zero bytes, not these products' (negative zeros have a code of their own).
 __device__ __forceinline__ float code_factor(float scale, float *first) {
     *first = scale < kTinyScale ? kTinyUp : 1.0f;
     return scale == 0.0f ? 0.0f : __frcp_rn(scale * *first);
@@ -72,6 +73,7 @@ __device__ __forceinline__ uint2 code8_by(float (&v)[8], float scale) {
     if (first != 1.0f)
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= first;
+    if (scale == 0.0f) return make_uint2(0, 0);
     return make_uint2(code4_by(v[0], v[1], v[2], v[3], inv), code4_by(v[4], v[5], v[6], v[7], inv));
 }
 

@@ -435,7 +435,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 bar_named(2 + quad, 64);
                 float inv = __frcp_rn(scale);
                 if (scale < kTinyScale) {
-                    const uint64_t up = pack2(__float_as_uint(kTinyUp), __float_as_uint(kTinyUp));
+                    // with scale 0 all to positive zeros, whose codes are zero bytes
+                    const uint32_t by = __float_as_uint(scale == 0.0f ? 0.0f : kTinyUp);
+                    const uint64_t up = pack2(by, by);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) acc[0][i] = fma2(acc[0][i], up, 0);
                     inv = scale == 0.0f ? 0.0f : __frcp_rn(scale * kTinyUp);

@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             const float inv = code_factor(scale, &first);  // as the 128-row tiles code it
             const int I = p.n >> 1;
             *reinterpret_cast<uint32_t *>(p.h_q + row * I + blk * 128 + lane * 4) =
-                code4_by(a * first, b * first, c * first, d * first, inv);
+                scale == 0.0f ? 0u : code4_by(a * first, b * first, c * first, d * first, inv);
             if (lane == 0) p.h_s[row * (I >> 7) + blk] = scale;
         }
     }
