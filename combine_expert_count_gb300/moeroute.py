@@ -495,9 +495,12 @@ def moe_expert_gemm_swiglu(shape, inter: int, k: int, a_q, a_s, grp_off, w13_q, 
 def moe_layer_few(shape, inter: int, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2_s, h_q, h_s, out,
                   status, stream=None) -> None:
     """A whole expert layer for at most MOE_FEW_MAX_TOKENS tokens; ``h_q``
-    [N][T][R][inter] and ``h_s`` [N][T][R][inter/128] are scratch."""
+    [N][T][R][inter] and ``h_s`` [N][T][R][inter/128] are scratch.  ``x`` may be
+    pinned host memory, ``out`` may not."""
     sh = _as_shape(shape)
     z = sizes_query(sh)
+    if out is not None and not out.is_cuda:
+        raise ValueError("out: must be a CUDA tensor")
     nx, ni, H = z.bytes_x, z.bytes_topk_idx, sh.H
     nh, nw, ns = ni // 4 * inter, sh.E * inter * H, sh.E * (inter // 128) * (H // 128) * 4
     rc = (_lib or lib()).moe_layer_few(
