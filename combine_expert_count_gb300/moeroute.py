@@ -677,8 +677,14 @@ class MoeBuffers:
         """The experts between ``dispatch`` and ``combine``: moe_expert_gemm_swiglu
         of the grouped rows and moe_expert_gemm into ``y``.  The weights are
         [E][2*inter][H] and [E][H][inter] e4m3 with their 128 x 128 block scales;
+        inter is the last axis of ``w2_q``, or what its bytes make where it is flat;
         the coded activations (``h_q``, ``h_s``) are ``activations``'."""
-        inter = w2_q.shape[-1]
+        if w2_q.dim() > 1:
+            inter = w2_q.shape[-1] * w2_q.element_size()
+        else:
+            inter, rest = divmod(w2_q.nbytes, self.E * self.H)
+            if rest or not inter or inter % 128:
+                raise ValueError(f"w2_q: {w2_q.nbytes} bytes are not [{self.E}][{self.H}][inter]")
         self.h_q, self.h_s = self.activations(inter, stream)
         moe_expert_gemm_swiglu(self.shape, inter, self.H, self.grp_q, self.grp_s, self.grp_off,
                                w13_q, w13_s, self.h_q, self.h_s, self.status, stream)

@@ -61,3 +61,32 @@ def test_few_takes_pinned_x_but_no_pinned_out(launched, x_cuda):
     assert not launched
     call(big)
     assert len(launched) == 1
+
+
+@pytest.fixture
+def experts(monkeypatch):
+    """MoeBuffers of E = 4 experts and hidden 256, and the widths its products get."""
+    widths = []
+    monkeypatch.setattr(m, "moe_expert_gemm_swiglu", lambda sh, inter, k, *a: widths.append(inter))
+    monkeypatch.setattr(m, "moe_expert_gemm", lambda sh, n, k, *a: widths.append(k))
+    from combine_expert_count_gb300 import build
+    build.build()
+    return m.MoeBuffers(1, 2, 4, 2, 256, device="cpu"), widths
+
+
+@pytest.mark.parametrize("shape,dtype", [
+    ((4, 256, 384), torch.uint8), ((4 * 256, 384), torch.uint8), ((4 * 256 * 384,), torch.uint8),
+    ((4, 256, 384), torch.float8_e4m3fn), ((4 * 256 * 96,), torch.int32), ((4, 256, 96), torch.int32),
+])
+def test_the_experts_width_is_that_of_the_bytes_given(experts, shape, dtype):
+    buf, widths = experts
+    buf.experts(None, None, torch.empty(shape, dtype=dtype), None)
+    assert widths == [384, 384]
+
+
+@pytest.mark.parametrize("n", [0, 4 * 256 * 100, 4 * 256 * 128 + 1])
+def test_flat_weights_of_no_whole_width_are_refused(experts, n):
+    buf, widths = experts
+    with pytest.raises(ValueError, match="w2_q"):
+        buf.experts(None, None, torch.empty(n, dtype=torch.uint8), None)
+    assert not widths and not buf._h
