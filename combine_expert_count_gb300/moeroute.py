@@ -588,12 +588,14 @@ class MoeBuffers:
         self.sig = torch.zeros(int(z.bytes_sig) // 4, dtype=torch.int32, device=d)
         self._h = {}  # activations() by width
 
-    def partial_rows(self) -> torch.Tensor:
+    def partial_rows(self, stream=None) -> torch.Tensor:
         """The send-side reduction's partial rows [N][N][T][H] bf16, allocated
-        on first use."""
+        on first use, on the stream that uses them."""
         if not hasattr(self, "part"):
             N, T, H = self.N, self.T, self.H
-            self.part = torch.empty((N, N, T, H), dtype=torch.bfloat16, device=self.out.device)
+            with torch.cuda.stream(stream):
+                self.part = torch.empty((N, N, T, H), dtype=torch.bfloat16,
+                                        device=self.out.device)
         return self.part
 
     def device_bytes(self) -> int:
@@ -700,7 +702,7 @@ class MoeBuffers:
         moe_combine_recv."""
         out = self.out if out is None else out
         if calls in ("partial", "partial_separate"):
-            part = self.partial_rows()
+            part = self.partial_rows(stream)
             if calls == "partial":
                 b = self._struct(_PARTIAL_NEEDS, topk_idx=topk_idx, topk_w=topk_w,
                                  y=self.y if y is None else y, out=out)

@@ -54,7 +54,9 @@ def test_a_call_with_another_width_keeps_the_first_ones_buffers(calls):
         assert s().shape == (N, buf.cap, inter // 128) and s().dtype == torch.float32
 
 
-def test_buffers_are_allocated_on_the_calls_stream(calls, monkeypatch):
+@pytest.fixture
+def allocated(monkeypatch):
+    """The stream that each torch.empty is called on."""
     current, at = [None], []
 
     @contextlib.contextmanager
@@ -67,14 +69,29 @@ def test_buffers_are_allocated_on_the_calls_stream(calls, monkeypatch):
     def noted(*a, **k):
         at.append(current[0])
         return empty(*a, **k)
-    buf = m.MoeBuffers(N, T, E, R, H, device="cpu")
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch, "empty", noted)
+    return at
+
+
+def test_buffers_are_allocated_on_the_calls_stream(calls, allocated):
+    buf = m.MoeBuffers(N, T, E, R, H, device="cpu")
+    del allocated[:]
     buf.experts(*weights(128), stream="side")
-    assert at == ["side", "side"]
+    assert allocated == ["side", "side"]
     buf.experts(*weights(128), stream="side")
     buf.experts(*weights(256))
-    assert at == ["side", "side", None, None]
+    assert allocated == ["side", "side", None, None]
+
+
+def test_partial_rows_are_allocated_on_the_calls_stream(allocated, monkeypatch):
+    monkeypatch.setattr(m, "moe_combine_partial_send", lambda *a: None)
+    monkeypatch.setattr(m, "moe_combine_partial_recv", lambda *a: None)
+    buf = m.MoeBuffers(N, T, E, R, H, device="cpu")
+    del allocated[:]
+    for _ in range(2):
+        buf.combine(None, None, stream="side", calls="partial_separate")
+    assert allocated == ["side"]
 
 
 def test_device_bytes_count_every_width_once(calls):
