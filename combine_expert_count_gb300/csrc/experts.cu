@@ -36,6 +36,7 @@
 #include "check.h"
 #include "coding.cuh"
 #include "launch.h"
+#include "plan.h"
 #include "tc.cuh"
 #include "thin.h"
 #include "tilemap.h"
@@ -45,7 +46,6 @@ namespace moe {
 
 namespace cg = cooperative_groups;
 
-constexpr int kTileRows = 128;               // rows of a tile: the lanes of tensor memory
 constexpr int kBlk = 128;                    // k block, scale block, half of a tile's columns
 constexpr int kBoxRows = 32;                 // rows of one TMA load of a: a group's last tile
                                              // loads no more than it has, rounded up to 32
@@ -476,34 +476,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
 // ------------------------------------------------------------ host
 
-// Whether two CTAs share each tile: where an SM each is left for them and k is
-// long.  us with one and two: gate/up of 2048 by 7168, 128 rows, 27.4 and 20.5; 7168
-// x 7168 (narrow tiles) 22.5 and 19.3; k = 4096 14.4 and 13.7; k = 2048 12.0 and
-// 12.3; k = 1024 8.3 and 10.0.  Four: 19.2, 22.6 (wide), 14.0, 15.1, 10.0.
-static int product_parts(int64_t tiles, int blocks) {
-    return tiles * 2 <= sm_count() && blocks >= 32 ? 2 : 1;
-}
-
 static cudaError_t launch_product(Product p, const uint8_t *a_q, const uint8_t *w_q,
                                   cudaStream_t st) {
-    if (few_rows(p.N, p.cap, p.E, p.n, p.k, p.h_q != nullptr))
-        return launch_thin_product(p.N, p.E, p.cap, p.n, p.k, a_q, p.a_s, p.grp_off, w_q, p.w_s, p.y,
-                                   p.h_q, p.h_s, p.status, st);
+    const bool swiglu = p.h_q != nullptr;
+    const ProductPlan plan = product_plan(p.N, p.cap, p.E, p.n, p.k, swiglu, sm_count());
+    if (plan.few)
+        return launch_thin_product(plan, p.N, p.E, p.cap, p.n, p.k, a_q, p.a_s, p.grp_off, w_q,
+                                   p.w_s, p.y, p.h_q, p.h_s, p.status, st);
     CUtensorMap map_a, map_w;
     cudaError_t err = tile_map(&map_a, a_q, (int64_t)p.N * p.cap, p.k, kBoxRows);
     if (err == cudaSuccess) err = tile_map(&map_w, w_q, (int64_t)p.E * p.n, p.k, kBlk);
     if (err != cudaSuccess) return err;
-    const bool swiglu = p.h_q != nullptr;
-    // as many tiles as there can be: every expert's last may be part full
-    const int64_t nb = p.n >> 7, rows = (int64_t)p.N * p.cap, used = rows < p.E ? rows : p.E;
-    const int64_t row_tiles = (rows - used) / kTileRows + used;
-    // one column block a tile where even those have an SM each: half the sums of a k
-    // block, and its bound where an SM has one tile (7168 x 2048 at 128 rows 9.6 us,
-    // 12.3 with two; 7168 x 7168 22.6, 29.5; 512 x 1024 6.9, 8.6; with up to twice
-    // the SMs' tiles 16.5, 13.1 and 40, 30.4 at 512 rows)
-    p.wide = swiglu || row_tiles * nb > sm_count() ? 2 : 1;
-    const int64_t most = row_tiles * ((nb + p.wide - 1) / p.wide);
-    const int parts = product_parts(most, p.k >> 7);
+    p.wide = plan.wide;
+    const int parts = plan.parts;
     const auto kern = swiglu ? (parts > 1 ? k_product<true, true> : k_product<true, false>)
                              : (parts > 1 ? k_product<false, true> : k_product<false, false>);
     static LaunchMemo memo;
@@ -522,7 +507,7 @@ static cudaError_t launch_product(Product p, const uint8_t *a_q, const uint8_t *
     attr[1].val.clusterDim.x = 1;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = (unsigned)parts;
-    cfg.gridDim = dim3((unsigned)(most < sm_count() ? most : sm_count()), 1, (unsigned)parts);
+    cfg.gridDim = dim3((unsigned)(plan.tiles < sm_count() ? plan.tiles : sm_count()), 1, (unsigned)parts);
     cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = kProductSmem;
     cfg.stream = st;

@@ -1,6 +1,6 @@
 // thin.cu -- products of the experts' weights with few rows: the kernels of
 // moe_layer_few, and moe_expert_gemm / moe_expert_gemm_swiglu for few rows
-// (few_rows).  They are bound by reading the weights once.
+// (by plan.h).  They are bound by reading the weights once.
 //
 // The weights are the 128-row operand of the tensor cores and the rows of x (or
 // h) the narrow one of 16 columns: a product costs what its real rows cost,
@@ -677,23 +677,10 @@ static cudaError_t launch_thin(ThinArgs p, const CUtensorMap &map, dim3 grid, in
     return cudaLaunchKernelEx(&cfg, kern, p, map);
 }
 
-// CTAs that share a unit's k blocks: as many as the SMs hold at two each, eight at
-// most, with a block each at least and one CTA for two or three blocks (us: 2048 x
-// 256 3.6 and 4.1 with two; 2048 x 512 4.4 with two and 4.1 with four).  Powers of
-// two: clusters of five for four cost a layer of four tokens 211 us for 185 (hidden
-// 7168), their CTAs not filling the SMs in pairs.
-static int thin_parts(int64_t units, int64_t blocks) {
-    int parts = 1;
-    while (parts < 8 && blocks >= 4 && blocks >= 2 * parts &&
-           units * parts * 2 <= 2 * (int64_t)sm_count())
-        parts *= 2;
-    return parts;
-}
-
-cudaError_t launch_thin_product(int N, int E, int cap, int n, int k, const uint8_t *a_q,
-                                const float *a_s, const int32_t *grp_off, const uint8_t *w_q,
-                                const float *w_s, uint16_t *y, uint8_t *h_q, float *h_s,
-                                int32_t *status, cudaStream_t st) {
+cudaError_t launch_thin_product(const ProductPlan &plan, int N, int E, int cap, int n, int k,
+                                const uint8_t *a_q, const float *a_s, const int32_t *grp_off,
+                                const uint8_t *w_q, const float *w_s, uint16_t *y, uint8_t *h_q,
+                                float *h_s, int32_t *status, cudaStream_t st) {
     CUtensorMap map;
     cudaError_t err = tile_map(&map, w_q, (int64_t)E * n, k, 128);
     if (err != cudaSuccess) return err;
@@ -711,11 +698,9 @@ cudaError_t launch_thin_product(int N, int E, int cap, int n, int k, const uint8
     p.n = n;
     p.k = k;
     p.status = status;
-    const int units = thin_units(N, cap, E);
-    const dim3 grid((unsigned)(h_q ? n >> 8 : n >> 7), (unsigned)units);
-    const int parts = thin_parts((int64_t)grid.x * units, k >> 7);
-    if (h_q) return launch_thin<Thin::kSwiglu>(p, map, grid, parts, 0, st);
-    return launch_thin<Thin::kGemm>(p, map, grid, parts, 0, st);
+    const dim3 grid((unsigned)(h_q ? n >> 8 : n >> 7), (unsigned)plan.units);
+    if (h_q) return launch_thin<Thin::kSwiglu>(p, map, grid, plan.parts, 0, st);
+    return launch_thin<Thin::kGemm>(p, map, grid, plan.parts, 0, st);
 }
 
 static cudaError_t launch_code_rows(int blocks, const uint16_t *x, uint8_t *out, cudaStream_t st) {
@@ -746,9 +731,9 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.n = 2 * p.inter;
     p.k = p.H;
     p.w_s = w13_s;
-// an expert's second and further 16 rows are A / 16 units more at most
+    // an expert's second and further 16 rows are A / 16 units more at most
     const int64_t real = p.passes > 1 ? units + A / kThinRowsAt : units;
-    const int up_parts = thin_parts((real < gup.y ? real : gup.y) * gup.x, p.H >> 7);
+    const int up_parts = thin_parts((real < gup.y ? real : gup.y) * gup.x, p.H >> 7, sm_count());
     if (p.ntok <= kOwnRows) {
         err = launch_thin<Thin::kUp>(p, up, gup, up_parts, 0, st);
     } else {
@@ -762,7 +747,7 @@ static cudaError_t launch_few(ThinArgs p, const uint8_t *w13_q, const float *w13
     p.k = p.inter;
     p.w_s = w2_s;
     const dim3 gdown((unsigned)(p.H >> 7));
-    const int parts = thin_parts(gdown.x, (int64_t)units * (p.inter >> 7));
+    const int parts = thin_parts(gdown.x, (int64_t)units * (p.inter >> 7), sm_count());
     const size_t lists = thin_lists_smem(p.ntok, p.E, p.R);
     constexpr size_t kFixed = thin_fixed_smem<Thin::kDown, thin_stages(Thin::kDown)>();
     if (kFixed + lists <= kTwoSmem) return launch_thin<Thin::kDown>(p, down, gdown, parts, lists, st);
