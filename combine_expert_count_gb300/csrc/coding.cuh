@@ -72,8 +72,7 @@ __device__ __forceinline__ uint2 code8_by(float (&v)[8], float scale) {
     const float inv = code_factor(scale, &first);
     if (first != 1.0f)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= first;
-    if (scale == 0.0f) return make_uint2(0, 0);
+        for (int i = 0; i < 8; ++i) v[i] = scale == 0.0f ? 0.0f : v[i] * first;
     return make_uint2(code4_by(v[0], v[1], v[2], v[3], inv), code4_by(v[4], v[5], v[6], v[7], inv));
 }
 
