@@ -19,11 +19,15 @@
 //
 // What bounds it.  A decode batch: HBM, each weight being read once (32 experts of
 // 7168 x 2048 with 64 rows each 81 us, 6.2 TB/s; gate/up of 2048 by 7168 157 us, 6.1
-// TB/s).  Many rows: taking the sums out.  A k block is 512 cycles of products
-// and about 620 of the sum warps' (128 x 256 fused multiply-adds are 256 of every
-// SM's fp32 lanes; the rest is the way out of tensor memory and two barriers);
-// 8191 x 7168 x 7168 takes 308 to 330 us (2.55 to 2.73 PFLOP/s, a bf16 product's
-// measured rate being 1.89), the uneven prefill gate/up about 800 us (2.4).
+// TB/s).  Many rows: the sums.  8191 x 7168 x 7168 takes 308 to 330 us alone (2.55 to
+// 2.73 PFLOP/s, a bf16 product's measured rate being 1.89) and 354 to 365 under
+// sustained load, the uneven prefill gate/up 760 to 833 us and 850 to 870.  That is
+// about 880 cycles a k block (12 rounds of 56 blocks on an SM), of which the products
+// are 512.  By clock readings around the waits, which make it 1030, the sum warps
+// wait 176 for products, take 486 to read an accumulator and give it back, and need
+// the other 370 for scales, the last multiply-adds and, once a tile, the output; the
+// warp that issues waits 424 for an accumulator.  (128 x 256 fused multiply-adds are
+// 256 cycles of an SM's fp32 lanes; the loop by itself, its operands at hand, 620.)
 // What did not help: two CTAs on one 256-row tile with the weights halved
 // between them (their hand-over costs what the loads save), sixteen sum warps,
 // 32 columns at a time (registers), longer scale runs in registers.  What did:
@@ -385,6 +389,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     left[(2 * i + 1) * 32] = f.y;
                 }
                 cluster.sync();
+                // over `parts` though it is 2: without the loop it spills (22.2 us for 18.0,
+                // 128 rows by 7168 x 7168)
                 const bool mine = quad * parts / 4 == part;
                 for (int q = 0; mine && q < parts; ++q) {
                     if (q == part) continue;
