@@ -41,6 +41,18 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&a)[8]) {
                       pack_bf16x2(a[6], a[7]));
 }
 
+// The eight bf16 values of v.
+__device__ __forceinline__ void unpack8(float (&v)[8], const uint4 &w) {
+    v[0] = bf16_lo(w.x);
+    v[1] = bf16_hi(w.x);
+    v[2] = bf16_lo(w.y);
+    v[3] = bf16_hi(w.y);
+    v[4] = bf16_lo(w.z);
+    v[5] = bf16_hi(w.z);
+    v[6] = bf16_lo(w.w);
+    v[7] = bf16_hi(w.w);
+}
+
 __device__ __forceinline__ void fma8(float (&acc)[8], float w, const uint4 &v) {
     acc[0] = __fmaf_rn(w, bf16_lo(v.x), acc[0]);
     acc[1] = __fmaf_rn(w, bf16_hi(v.x), acc[1]);

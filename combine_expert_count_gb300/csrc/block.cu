@@ -1,0 +1,179 @@
+// block.cu -- moe_block_norm: the norm after a branch, its gate and scale, the
+// residual addition, the next norm and its block-128 e4m3 coding in one pass.
+#include <cmath>
+
+#include "bf16.cuh"
+#include "check.h"
+#include "coding.cuh"
+#include "launch.h"
+#include "trace.h"
+
+namespace moe {
+
+struct BlockNorm {
+    int H;
+    unsigned per_gate;  // rows that share a row of gate
+    float eps, scale;
+    const uint16_t *x, *post, *gate, *res, *gamma;
+    uint16_t *res_out, *y;
+    uint8_t *q;
+    float *s;
+};
+
+// The sum over the block of one value a thread; `part` is shared float[32], not in
+// use by anyone else.
+__device__ __forceinline__ float block_sum(float v, float *part) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float sum = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+    return sum;
+}
+
+// One CTA per row, V chunks of eight elements a thread, chunk tid + i * blockDim.x.
+template <int V, int kMost>
+__global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 3 : V == 4 ? 2 : 1) : 1)
+    k_block_norm(const BlockNorm p) {
+    __shared__ float part[2][32];
+    const int tid = threadIdx.x, nthr = blockDim.x, nch = p.H >> 3;
+    const size_t row = blockIdx.x, base = row * (size_t)p.H;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float v[V][8];
+    uint4 r[V];
+    float acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nthr;
+        r[i] = make_uint4(0, 0, 0, 0);
+        if (c >= nch) continue;
+        unpack8(v[i], *reinterpret_cast<const uint4 *>(p.x + base + c * 8));
+        if (p.res) r[i] = *reinterpret_cast<const uint4 *>(p.res + base + c * 8);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) acc = __fmaf_rn(v[i][u], v[i][u], acc);
+    }
+    float rstd = 1.0f;
+    if (p.post) rstd = __frsqrt_rn(block_sum(acc, part[0]) / (float)p.H + p.eps);
+    const uint16_t *gate = p.gate ? p.gate + (size_t)((unsigned)row / p.per_gate) * p.H : nullptr;
+    acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nthr;
+        if (c >= nch) continue;
+        float w[8];
+        if (p.post) {
+            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(p.post + c * 8)));
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
+        }
+        if (gate) {
+            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(gate + c * 8)));
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[i][u] *= w[u];
+        }
+        unpack8(w, r[i]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            v[i][u] = __fmaf_rn(p.scale, v[i][u], w[u]);
+            acc = __fmaf_rn(v[i][u], v[i][u], acc);
+        }
+        if (p.res_out)
+            *reinterpret_cast<uint4 *>(p.res_out + base + c * 8) = pack_bf16x8(v[i]);
+    }
+    if (!p.y && !p.q) return;
+    rstd = __frsqrt_rn(block_sum(acc, part[1]) / (float)p.H + p.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nthr;
+        const bool in = c < nch;
+        uint32_t amax = 0;
+        if (in) {
+            float w[8];
+            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(p.gamma + c * 8)));
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
+            if (p.y) *reinterpret_cast<uint4 *>(p.y + base + c * 8) = pack_bf16x8(v[i]);
+            amax = amax8(v[i]);
+        }
+        if (p.q) {
+            // the sixteen chunks of a block of 128 are sixteen neighbouring lanes
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, d));
+            if (in) {
+                const float scale = block_scale(amax);
+                *reinterpret_cast<uint2 *>(p.q + base + c * 8) = code8_by(v[i], scale);
+                if ((c & 15) == 0) p.s[row * (size_t)(p.H >> 7) + (c >> 4)] = scale;
+            }
+        }
+    }
+}
+
+static cudaError_t launch_block_norm(const BlockNorm &p, int rows, cudaStream_t st) {
+    const int nch = p.H >> 3, most = rows <= sm_count() ? 1024 : 512;
+    int V = 1;
+    while (V < 8 && nch > most * V) V *= 2;
+    const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
+    const auto kern = nthr <= 512 ? (V == 1   ? k_block_norm<1, 512>
+                                     : V == 2 ? k_block_norm<2, 512>
+                                     : V == 4 ? k_block_norm<4, 512>
+                                              : k_block_norm<8, 512>)
+                                  : (V == 1   ? k_block_norm<1, 1024>
+                                     : V == 2 ? k_block_norm<2, 1024>
+                                     : V == 4 ? k_block_norm<4, 1024>
+                                              : k_block_norm<8, 1024>);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)rows);
+    cfg.blockDim = dim3((unsigned)nthr);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace moe
+
+extern "C" int moe_block_norm(const moe_shape *sh, float eps, float scale, int gates,
+                              const uint16_t *x, const uint16_t *post, const uint16_t *gate,
+                              const uint16_t *res, const uint16_t *gamma, uint16_t *res_out,
+                              uint16_t *y, uint8_t *q, float *s, void *stream) {
+    MOE_TRACE_CALL();
+    moe_sizes z;
+    const int rc = moe_sizes_query(sh, &z);
+    if (rc != MOE_OK) return rc;
+    if (!(eps >= 0.0f) || std::isinf(eps) || !std::isfinite(scale)) return MOE_EINVAL;
+    if (!moe::ok_optional(post) || !moe::ok_optional(gate) || !moe::ok_optional(res) ||
+        !moe::ok_optional(gamma) || !moe::ok_optional(res_out) || !moe::ok_optional(y) ||
+        !moe::ok_optional(q) || !moe::ok_optional(s))
+        return MOE_EINVAL;
+    const int64_t rows = (int64_t)sh->N * sh->T;
+    if (gate && (gates < 1 || rows % gates != 0)) return MOE_EINVAL;
+    if (rows == 0) return MOE_OK;
+    if ((q == nullptr) != (s == nullptr) || (!res_out && !y && !q)) return MOE_EINVAL;
+    if (!moe::ok_buffer(x, z.bytes_x) || ((y || q) && !gamma)) return MOE_EINVAL;
+    if (rows >= ((int64_t)1 << 31)) return MOE_ENOTSUP;
+    moe::BlockNorm p = {};
+    p.H = sh->H;
+    p.per_gate = gate ? (unsigned)(rows / gates) : 1u;
+    p.eps = eps;
+    p.scale = scale;
+    p.x = x;
+    p.post = post;
+    p.gate = gate;
+    p.res = res;
+    p.gamma = gamma;
+    p.res_out = res_out;
+    p.y = y;
+    p.q = q;
+    p.s = s;
+    return moe::launch_block_norm(p, (int)rows, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ECUDA;
+}

@@ -10,17 +10,6 @@
 
 namespace moe {
 
-__device__ __forceinline__ void unpack8(float (&v)[8], const uint4 &w) {
-    v[0] = bf16_lo(w.x);
-    v[1] = bf16_hi(w.x);
-    v[2] = bf16_lo(w.y);
-    v[3] = bf16_hi(w.y);
-    v[4] = bf16_lo(w.z);
-    v[5] = bf16_hi(w.z);
-    v[6] = bf16_lo(w.w);
-    v[7] = bf16_hi(w.w);
-}
-
 // One CTA per row.  A thread holds V chunks of eight elements in registers
 // from the load to the last store, chunk tid + i * blockDim.x, so a row is
 // read once; blockDim.x is a multiple of 32, so the sixteen chunks of a block

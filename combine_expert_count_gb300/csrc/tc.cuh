@@ -109,6 +109,12 @@ __host__ __device__ constexpr uint32_t tc_e4m3_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The same of a k-major bf16 x bf16 -> fp32 product.
+__host__ __device__ constexpr uint32_t tc_bf16_f32(int M, int N) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
 // 1 in one lane of the (whole) warp, 0 in the others.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
@@ -131,6 +137,18 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "setp.ne.u32 p, %4, 0;\n\t"
         "setp.ne.u32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
+        : "memory");
+}
+
+// The same over 16 elements of k of bf16 operands.
+__device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            bool accumulate, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
         : "memory");
 }

@@ -34,6 +34,8 @@ _lib = None
 MOE_OK, MOE_EINVAL, MOE_ENOTSUP, MOE_ECUDA = 0, -1, -2, -3
 MOE_ST_BAD_EXPERT, MOE_ST_CAPACITY, MOE_ST_TIMEOUT = 1, 2, 4
 MOE_FEW_MAX_TOKENS = 64
+MOE_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 EXPORTS = ("moe_sizes_query", "moe_route_count", "moe_exchange", "moe_route", "moe_dispatch_send",
            "moe_dispatch_recv", "moe_combine_send", "moe_combine_recv", "moe_dispatch",
@@ -42,6 +44,7 @@ EXPORTS = ("moe_sizes_query", "moe_route_count", "moe_exchange", "moe_route", "m
            "moe_combine_partial", "moe_expert_standin",
            "moe_e4m3_encode", "moe_dispatch_ll", "moe_expert_standin_ll", "moe_combine_ll",
            "moe_rmsnorm", "moe_expert_gemm", "moe_expert_gemm_swiglu", "moe_layer_few",
+           "moe_linear", "moe_linear_glu", "moe_topk", "moe_block_norm",
            "moe_strerror", "moe_version")
 
 
@@ -117,6 +120,11 @@ def lib() -> ctypes.CDLL:
             h.moe_expert_gemm.argtypes = [sp, I, I] + [V] * 7 + [V]
             h.moe_expert_gemm_swiglu.argtypes = [sp, I, I] + [V] * 8 + [V]
             h.moe_layer_few.argtypes = [sp, I] + [V] * 11 + [V]
+            F = ctypes.c_float
+            h.moe_linear.argtypes = [sp, I, I, I] + [V] * 7 + [V]
+            h.moe_linear_glu.argtypes = [sp, I, I, I] + [V] * 5 + [V]
+            h.moe_topk.argtypes = [sp, I, I, I, I, I, F] + [V] * 4 + [V]
+            h.moe_block_norm.argtypes = [sp, F, F, I] + [V] * 9 + [V]
             h.moe_strerror.argtypes = [I]
             h.moe_strerror.restype = ctypes.c_char_p
             h.moe_version.argtypes = []
@@ -510,6 +518,95 @@ def moe_layer_few(shape, inter: int, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2
         _ptr(h_s, nh // 32, "h_s"), _ptr(out, nx, "out"), _ptr(status, 4, "status"),
         _raw_stream(stream))
     _check(rc, "moe_layer_few")
+
+
+def _on_device(t, nbytes: int, name: str, device: int):
+    """_ptr's address of a tensor on the current device, which the call's kernels run
+    on; no host memory."""
+    if t is not None:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{name}: on device {t.get_device()}, the current one is {device}")
+    return _ptr(t, nbytes, name)
+
+
+def _named(names: dict, value, what: str) -> int:
+    got = names.get(value)
+    if got is None:
+        raise ValueError(f"{what}: {value!r} is none of {', '.join(names)}")
+    return got
+
+
+def moe_linear(shape, n: int, k: int, x, w, y, bias=None, res=None, act: str = "none",
+               status=None, stream=None) -> None:
+    """y = act(x w^T + bias) + res for the N*T rows of ``x`` [N*T][k] and 16-bit
+    weights [n][k]; ``y`` is bf16, or fp32 where its dtype is torch.float32."""
+    sh, d = _as_shape(shape), torch._C._cuda_getDevice()
+    rows, f32 = sh.N * sh.T, y is not None and y.dtype == torch.float32
+    py = _on_device(y, rows * n * (4 if f32 else 2), "y", d)
+    rc = (_lib or lib()).moe_linear(
+        ctypes.byref(sh), n, k, _named(MOE_ACTS, act, "act"),
+        _on_device(x, rows * k * 2, "x", d), _on_device(w, n * k * 2, "w", d),
+        None if bias is None else _on_device(bias, 2 * n, "bias", d),
+        None if res is None else _on_device(res, rows * n * 2, "res", d),
+        None if f32 else py, py if f32 else None,
+        None if status is None else _on_device(status, 4, "status", d), _raw_stream(stream))
+    _check(rc, "moe_linear")
+
+
+def moe_linear_glu(shape, inter: int, k: int, x, w13, h, bias=None, act: str = "silu",
+                   status=None, stream=None) -> None:
+    """h = act(x wg^T + bg) * (x wu^T + bu), bf16 [N*T][inter]: ``w13`` [2*inter][k]
+    and ``bias`` [2*inter] hold the gate's outputs, then the up projection's."""
+    sh, d = _as_shape(shape), torch._C._cuda_getDevice()
+    rows = sh.N * sh.T
+    rc = (_lib or lib()).moe_linear_glu(
+        ctypes.byref(sh), inter, k, _named(MOE_ACTS, act, "act"),
+        _on_device(x, rows * k * 2, "x", d), _on_device(w13, 4 * inter * k, "w13", d),
+        None if bias is None else _on_device(bias, 4 * inter, "bias", d),
+        _on_device(h, rows * inter * 2, "h", d),
+        None if status is None else _on_device(status, 4, "status", d), _raw_stream(stream))
+    _check(rc, "moe_linear_glu")
+
+
+def moe_topk(shape, logits, topk_idx, topk_w, bias=None, score: str = "softmax", groups: int = 1,
+             kept: int = 1, best: int = 1, renorm: bool = True, scale: float = 1.0,
+             stream=None) -> None:
+    """A router's choice of R of E experts and their weights from fp32 ``logits``
+    [N][T][E]: the ``topk_idx`` and ``topk_w`` of the dispatch and combine.  ``bias``
+    [E] is added to the scores for the choice alone; of ``groups`` runs of experts the
+    ``kept`` whose ``best`` largest sum to most take part."""
+    sh, d = _as_shape(shape), torch._C._cuda_getDevice()
+    rows = sh.N * sh.T
+    rc = (_lib or lib()).moe_topk(
+        ctypes.byref(sh), _named(MOE_SCORES, score, "score"), groups, kept, best, bool(renorm),
+        scale, _on_device(logits, rows * sh.E * 4, "logits", d),
+        None if bias is None else _on_device(bias, sh.E * 4, "bias", d),
+        _on_device(topk_idx, rows * sh.R * 4, "topk_idx", d),
+        _on_device(topk_w, rows * sh.R * 4, "topk_w", d), _raw_stream(stream))
+    _check(rc, "moe_topk")
+
+
+def moe_block_norm(shape, x, gamma, eps: float, res_out=None, y=None, q=None, s=None,
+                   post_gamma=None, gate=None, gates: int = 1, scale: float = 1.0, res=None,
+                   stream=None) -> None:
+    """The end of a block: v = ``res`` + ``scale`` * ``gate`` * (``x``, or its norm times
+    ``post_gamma``) into ``res_out``, and v's norm times ``gamma`` as bf16 rows ``y`` and
+    their e4m3 coding (``q``, ``s``), each where a buffer is given.  ``gate`` [gates][H]
+    has a row for each run of N*T / gates rows."""
+    sh, d = _as_shape(shape), torch._C._cuda_getDevice()
+    H = sh.H
+    nx = sh.N * sh.T * H * 2
+
+    def at(t, nbytes, name):
+        return None if t is None else _on_device(t, nbytes, name, d)
+    rc = (_lib or lib()).moe_block_norm(
+        ctypes.byref(sh), eps, scale, gates, _on_device(x, nx, "x", d),
+        at(post_gamma, 2 * H, "post_gamma"), at(gate, 2 * gates * H, "gate"), at(res, nx, "res"),
+        at(gamma, 2 * H, "gamma"), at(res_out, nx, "res_out"), at(y, nx, "y"),
+        at(q, nx // 2, "q"), at(s, nx // 64, "s"), _raw_stream(stream))
+    _check(rc, "moe_block_norm")
 
 
 class MoeLLBuffers:

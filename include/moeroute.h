@@ -522,6 +522,95 @@ int moe_layer_few(const moe_shape *shape, int inter, const uint16_t *x_bf16,
                   const float *w13_s, const uint8_t *w2_q, const float *w2_s, uint8_t *h_q,
                   float *h_s, uint16_t *out_bf16, int32_t *status, void *stream);
 
+/* ---------------------------------------------------------------- around the experts
+ * What else a block of a serving model has next to its experts: the router's
+ * product and choice, a shared expert or another projection with 16-bit weights,
+ * and the block's end.  Rows are the N*T of the shape; its E, R and cap are only
+ * checked where they are not named.  Every pointer is device memory. */
+
+/* Activations of the products, v in fp32. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1      /* max(v, 0) */
+#define MOE_ACT_SILU 2      /* v / (1 + exp(-v)) */
+#define MOE_ACT_GELU 3      /* v (1 + erf(v / sqrt(2))) / 2 */
+#define MOE_ACT_GELU_TANH 4 /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+#define MOE_ACT_SIGMOID 5   /* 1 / (1 + exp(-v)) */
+
+/* Widths of these products: k a multiple of 8 up to 65536, n any up to 2^20
+ * (MOE_ENOTSUP beyond). */
+#define MOE_LINEAR_MAX_N (1 << 20)
+
+/* y = act(x w^T + bias) + res, a product with its epilogue in one kernel:
+ *   x bf16 [N*T][k], w bf16 [n][k], bias bf16 [n] or NULL, res bf16 [N*T][n] or
+ *   NULL, and one of y_bf16 [N*T][n] and y_f32 [N*T][n]
+ * The product, the bias, the activation and the residual are fp32, rounded once.
+ * Products of bf16 values are exact; the tensor cores sum them in fp32.  With
+ * y_f32 (a router's logits, which choose) their sums are taken out every 256 along
+ * k and added there, rounding to nearest.  y_bf16 may be res (each element is read
+ * before it is written, by the same thread); other overlaps of outputs with inputs
+ * are not allowed.  status as for moe_expert_gemm. */
+int moe_linear(const moe_shape *shape, int n, int k, int act, const uint16_t *x_bf16,
+               const uint16_t *w_bf16, const uint16_t *bias_bf16, const uint16_t *res_bf16,
+               uint16_t *y_bf16, float *y_f32, int32_t *status, void *stream);
+
+/* Both projections of a gated feed-forward, the activation and the product of the
+ * two in one kernel:
+ *   h = bf16_rn(act(x wg^T + bg) * (x wu^T + bu))
+ * w13's first `inter` outputs are the gate wg, the next `inter` the up wu (as for
+ * moe_expert_gemm_swiglu; the bias alike):
+ *   x bf16 [N*T][k], w13 bf16 [2*inter][k], bias13 bf16 [2*inter] or NULL,
+ *   h bf16 [N*T][inter]
+ * 2*inter up to MOE_LINEAR_MAX_N. */
+int moe_linear_glu(const moe_shape *shape, int inter, int k, int act, const uint16_t *x_bf16,
+                   const uint16_t *w13_bf16, const uint16_t *bias13_bf16, uint16_t *h_bf16,
+                   int32_t *status, void *stream);
+
+/* A router's choice: the topk_idx and topk_w of the calls above from logits.
+ * Per token, of its E logits l (fp32):
+ *   s_e = exp(l_e) / sum_e' exp(l_e')  (MOE_SCORE_SOFTMAX)
+ *         or 1 / (1 + exp(-l_e))       (MOE_SCORE_SIGMOID)
+ *   c_e = s_e + bias_e: what is compared, in 64 bits; without a bias the logits
+ *         themselves are, whose order is the same
+ *   the experts are `groups` runs of E/groups; a run is worth the sum of its `best`
+ *         (1 or 2) largest c (of s, where there is no bias and best is 2), and the
+ *         `kept` runs worth most are kept
+ *   topk_idx: the R kept experts with the largest c, largest first
+ *   topk_w:   scale * s_e, or scale * s_e / (sum of the chosen s) with renorm; the
+ *         bias is not in it
+ * Equal values go to the lowest index.  A logit of -infinity, or a NaN among c, is
+ * an expert out of service: it comes after all others (its c is -infinity, and its
+ * run's worth with it) and has weight 0.  A NaN logit, or one of +infinity with
+ * MOE_SCORE_SOFTMAX, makes its token's weights NaN; the ids are valid ones all the
+ * same.  bias may be NULL.  1 <= groups <= 32, E % groups == 0, 1 <= kept <= groups,
+ * best <= E/groups and R <= kept * E/groups, else MOE_EINVAL (MOE_ENOTSUP for more
+ * groups).  scale must be finite. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_MAX_GROUPS 32
+int moe_topk(const moe_shape *shape, int score, int groups, int kept, int best, int renorm,
+             float scale, const float *logits, const float *bias, int32_t *topk_idx,
+             float *topk_w, void *stream);
+
+/* The end of a block, in one pass over its rows: the norm after the branch, the
+ * branch's gate and scale, the residual addition, and the next block's norm with its
+ * coding (moe_rmsnorm is the case without the first three).  Per row i:
+ *   b       = (x * rstd(x)) * post_gamma, or x where post_gamma is NULL
+ *   b       = b * gate[i / (N*T / gates)], where gate is given: bf16 [gates][H], a
+ *             row for each run of N*T / gates rows (1: a gate of each channel; N*T:
+ *             of each element); N*T % gates == 0
+ *   v       = res + scale * b    (0 where res is NULL)
+ *   res_out = bf16_rn(v)
+ *   y       = bf16_rn((v * rstd(v)) * gamma),  rstd(v) = 1 / sqrt(mean(v^2) + eps)
+ *   s, q    = the coding of the fp32 values (v * rstd(v)) * gamma, as moe_rmsnorm's
+ * all in fp32.  gamma is needed for y and (q, s) only; q and s go together; at least
+ * one output is needed.  res_out may be x or res, likewise y; other overlaps of
+ * outputs with inputs are not allowed.  eps must be finite and >= 0, scale finite. */
+int moe_block_norm(const moe_shape *shape, float eps, float scale, int gates,
+                   const uint16_t *x_bf16, const uint16_t *post_gamma_bf16,
+                   const uint16_t *gate_bf16, const uint16_t *res_bf16,
+                   const uint16_t *gamma_bf16, uint16_t *res_out_bf16, uint16_t *y_bf16,
+                   uint8_t *q, float *s, void *stream);
+
 /* Static description of an error code or status bit set. */
 const char *moe_strerror(int code);
 
