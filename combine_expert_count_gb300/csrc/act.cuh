@@ -16,18 +16,50 @@ __device__ __forceinline__ float over_one_plus_exp(float v, float z) {  // v / (
     return __fdividef(v, 1.0f + __expf(-z));
 }
 
-template <bool kExact>
-__device__ __forceinline__ float activate(int act, float v) {
+// The probability below v of a standard normal, whose product with v is the gelu:
+// for v < 0 exp(-v^2 / 2) t P(t) with t = 1 / (1 + |v| / 5), else 1 minus that of -v.
+// P is a polynomial of degree six fitted to exp(v^2 / 2) erfc(|v| / sqrt(2)) / (2 t)
+// by least squares with weights that even out its relative error, over |v| from 0 to
+// 14: at most 1.7e-6, 2^-19, in fp32.  The complementary error function itself takes
+// twice the instructions, which a tile with a short k then waits for (512 x 9728 x 64:
+// 15.9 us, 7.4 without an activation).
+__device__ __forceinline__ float normal_below(float v) {
+    const float a = fabsf(v), t = __fdividef(1.0f, __fmaf_rn(0.2f, a, 1.0f));
+    float s = 0.27909577f;
+    s = __fmaf_rn(s, t, -0.38683176f);
+    s = __fmaf_rn(s, t, 0.44694775f);
+    s = __fmaf_rn(s, t, -0.12319261f);
+    s = __fmaf_rn(s, t, 0.13253959f);
+    s = __fmaf_rn(s, t, 0.07109163f);
+    s = __fmaf_rn(s, t, 0.08035023f);
+    s *= t * __expf(-0.5f * a * a);
+    return v > 0.0f ? 1.0f - s : s;
+}
+
+// One activation of all of v: its kind is asked once, so that only its code is fetched.
+template <bool kExact, int n>
+__device__ __forceinline__ void activate(int act, float (&v)[n]) {
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = f(v[i]);
+    };
     switch (act) {
-        case MOE_ACT_RELU: return v > 0.0f || v != v ? v : 0.0f;
-        case MOE_ACT_SILU: return over_one_plus_exp<kExact>(v, v);
-        case MOE_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
-        case MOE_ACT_GELU_TANH:
-            // 2 sqrt(2 / pi), and that times 0.044715
-            return over_one_plus_exp<kExact>(
-                v, v * __fmaf_rn(0.071354816272f, v * v, 1.5957691216057308f));
-        case MOE_ACT_SIGMOID: return over_one_plus_exp<kExact>(1.0f, v);
-        default: return v;
+        case MOE_ACT_RELU:
+            return each([](float a) { return a > 0.0f || a != a ? a : 0.0f; });
+        case MOE_ACT_SILU:
+            return each([](float a) { return over_one_plus_exp<kExact>(a, a); });
+        case MOE_ACT_GELU:
+            return each([](float a) {
+                return kExact ? 0.5f * a * erfcf(a * -0.70710678118654752f) : a * normal_below(a);
+            });
+        case MOE_ACT_GELU_TANH:  // 2 sqrt(2 / pi), and that times 0.044715
+            return each([](float a) {
+                return over_one_plus_exp<kExact>(
+                    a, a * __fmaf_rn(0.071354816272f, a * a, 1.5957691216057308f));
+            });
+        case MOE_ACT_SIGMOID:
+            return each([](float a) { return over_one_plus_exp<kExact>(1.0f, a); });
+        default: return;
     }
 }
 

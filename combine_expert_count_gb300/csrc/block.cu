@@ -11,7 +11,7 @@
 namespace moe {
 
 struct BlockNorm {
-    int H;
+    int H, rows;
     unsigned per_gate;  // rows that share a row of gate
     float eps, scale;
     const uint16_t *x, *post, *gate, *res, *gamma;
@@ -20,12 +20,14 @@ struct BlockNorm {
     float *s;
 };
 
-// The sum over the block of one value a thread; `part` is shared float[32], not in
-// use by anyone else.
-__device__ __forceinline__ float block_sum(float v, float *part) {
+// The sum of one value a thread, over the block or over the warp; `part` is shared
+// float[32], not in use by anyone else.
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float v, float *part) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    if (kWarp) return v;
     if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     float sum = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f;
@@ -34,44 +36,48 @@ __device__ __forceinline__ float block_sum(float v, float *part) {
     return sum;
 }
 
-// One CTA per row, V chunks of eight elements a thread, chunk tid + i * blockDim.x.
-template <int V, int kMost>
-__global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 3 : V == 4 ? 2 : 1) : 1)
-    k_block_norm(const BlockNorm p) {
-    __shared__ float part[2][32];
-    const int tid = threadIdx.x, nthr = blockDim.x, nch = p.H >> 3;
-    const size_t row = blockIdx.x, base = row * (size_t)p.H;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    float v[V][8];
-    uint4 r[V];
-    float acc = 0.0f;
+__device__ __forceinline__ uint4 vec8(const uint16_t *p, int c) {
+    return __ldg(reinterpret_cast<const uint4 *>(p + c * 8));
+}
+
+// A row, the block's or (kWarp) the warp's, from its V chunks of eight elements a
+// thread, chunk tid + i * nthr of them:
+// xr holds x, r the residual, as they were read: unpacked they would take twice the
+// registers while the first sum is waited for.
+template <int V, bool kWarp>
+__device__ __forceinline__ void row_norm(const BlockNorm &p, size_t row, const uint4 (&xr)[V],
+                                         const uint4 (&r)[V], float *part0, float *part1) {
+    const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, nthr = kWarp ? 32 : blockDim.x;
+    const int nch = p.H >> 3;
+    const size_t base = row * (size_t)p.H;
+    float rstd = 1.0f, acc = 0.0f;
+    if (p.post) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = tid + i * nthr;
-        r[i] = make_uint4(0, 0, 0, 0);
-        if (c >= nch) continue;
-        unpack8(v[i], *reinterpret_cast<const uint4 *>(p.x + base + c * 8));
-        if (p.res) r[i] = *reinterpret_cast<const uint4 *>(p.res + base + c * 8);
+        for (int i = 0; i < V; ++i)
+            if (tid + i * nthr < nch) {
+                float w[8];
+                unpack8(w, xr[i]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) acc = __fmaf_rn(v[i][u], v[i][u], acc);
+                for (int u = 0; u < 8; ++u) acc = __fmaf_rn(w[u], w[u], acc);
+            }
+        rstd = __frsqrt_rn(row_sum<kWarp>(acc, part0) / (float)p.H + p.eps);
+        acc = 0.0f;
     }
-    float rstd = 1.0f;
-    if (p.post) rstd = __frsqrt_rn(block_sum(acc, part[0]) / (float)p.H + p.eps);
+    float v[V][8];
     const uint16_t *gate = p.gate ? p.gate + (size_t)((unsigned)row / p.per_gate) * p.H : nullptr;
-    acc = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nthr;
         if (c >= nch) continue;
         float w[8];
+        unpack8(v[i], xr[i]);
         if (p.post) {
-            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(p.post + c * 8)));
+            unpack8(w, vec8(p.post, c));
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
         }
         if (gate) {
-            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(gate + c * 8)));
+            unpack8(w, vec8(gate, c));
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[i][u] *= w[u];
         }
@@ -81,11 +87,10 @@ __global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 3 : V == 4 ? 2
             v[i][u] = __fmaf_rn(p.scale, v[i][u], w[u]);
             acc = __fmaf_rn(v[i][u], v[i][u], acc);
         }
-        if (p.res_out)
-            *reinterpret_cast<uint4 *>(p.res_out + base + c * 8) = pack_bf16x8(v[i]);
+        if (p.res_out) *reinterpret_cast<uint4 *>(p.res_out + base + c * 8) = pack_bf16x8(v[i]);
     }
     if (!p.y && !p.q) return;
-    rstd = __frsqrt_rn(block_sum(acc, part[1]) / (float)p.H + p.eps);
+    rstd = __frsqrt_rn(row_sum<kWarp>(acc, part1) / (float)p.H + p.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nthr;
@@ -93,7 +98,7 @@ __global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 3 : V == 4 ? 2
         uint32_t amax = 0;
         if (in) {
             float w[8];
-            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(p.gamma + c * 8)));
+            unpack8(w, vec8(p.gamma, c));
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
             if (p.y) *reinterpret_cast<uint4 *>(p.y + base + c * 8) = pack_bf16x8(v[i]);
@@ -112,29 +117,64 @@ __global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 3 : V == 4 ? 2
     }
 }
 
-static cudaError_t launch_block_norm(const BlockNorm &p, int rows, cudaStream_t st) {
-    const int nch = p.H >> 3, most = rows <= sm_count() ? 1024 : 512;
-    int V = 1;
-    while (V < 8 && nch > most * V) V *= 2;
-    const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
-    const auto kern = nthr <= 512 ? (V == 1   ? k_block_norm<1, 512>
-                                     : V == 2 ? k_block_norm<2, 512>
-                                     : V == 4 ? k_block_norm<4, 512>
-                                              : k_block_norm<8, 512>)
-                                  : (V == 1   ? k_block_norm<1, 1024>
-                                     : V == 2 ? k_block_norm<2, 1024>
-                                     : V == 4 ? k_block_norm<4, 1024>
-                                              : k_block_norm<8, 1024>);
+// One CTA per row, or one warp for short ones.
+constexpr int kRowWarps = 4;
+template <int V, int kMost, bool kWarp>
+__global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 4 : V == 4 ? 2 : 1) : 1)
+    k_block_norm(const BlockNorm p) {
+    __shared__ float part[2][32];
+    const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, nthr = kWarp ? 32 : blockDim.x;
+    const int nch = p.H >> 3;
+    const size_t row = kWarp ? (size_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5) : blockIdx.x;
+    const size_t base = row * (size_t)p.H;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (kWarp && row >= p.rows) return;
+    uint4 x[V], r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = tid + i * nthr;
+        x[i] = r[i] = make_uint4(0, 0, 0, 0);
+        if (c >= nch) continue;
+        x[i] = *reinterpret_cast<const uint4 *>(p.x + base + c * 8);
+        if (p.res) r[i] = *reinterpret_cast<const uint4 *>(p.res + base + c * 8);
+    }
+    row_norm<V, kWarp>(p, row, x, r, part[0], part[1]);
+}
+
+template <class K>
+static cudaError_t launch(K kern, int grid, int threads, const BlockNorm &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)rows);
-    cfg.blockDim = dim3((unsigned)nthr);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+static cudaError_t launch_block_norm(const BlockNorm &p, cudaStream_t st) {
+    const int nch = p.H >> 3, rows = p.rows, sms = sm_count();
+    if (rows > 2 * sms && nch <= 64) {
+        const auto kern = nch <= 32 ? k_block_norm<1, 128, true> : k_block_norm<2, 128, true>;
+        return launch(kern, (rows + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, p, st);
+    }
+    const int most = rows <= sms ? 1024 : 512;
+    int V = rows > 2 * sms ? 2 : 1;
+    while (V < 8 && nch > most * V) V *= 2;
+    const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
+    const auto kern = nthr <= 512 ? (V == 1   ? k_block_norm<1, 512, false>
+                                     : V == 2 ? k_block_norm<2, 512, false>
+                                     : V == 4 ? k_block_norm<4, 512, false>
+                                              : k_block_norm<8, 512, false>)
+                                  : (V == 1   ? k_block_norm<1, 1024, false>
+                                     : V == 2 ? k_block_norm<2, 1024, false>
+                                     : V == 4 ? k_block_norm<4, 1024, false>
+                                              : k_block_norm<8, 1024, false>);
+    return launch(kern, rows, nthr, p, st);
 }
 
 }  // namespace moe
@@ -160,6 +200,7 @@ extern "C" int moe_block_norm(const moe_shape *sh, float eps, float scale, int g
     if (rows >= ((int64_t)1 << 31)) return MOE_ENOTSUP;
     moe::BlockNorm p = {};
     p.H = sh->H;
+    p.rows = (int)rows;
     p.per_gate = gate ? (unsigned)(rows / gates) : 1u;
     p.eps = eps;
     p.scale = scale;
@@ -172,7 +213,7 @@ extern "C" int moe_block_norm(const moe_shape *sh, float eps, float scale, int g
     p.y = y;
     p.q = q;
     p.s = s;
-    return moe::launch_block_norm(p, (int)rows, reinterpret_cast<cudaStream_t>(stream)) ==
+    return moe::launch_block_norm(p, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? MOE_OK
                : MOE_ECUDA;

@@ -22,7 +22,10 @@ namespace cg = cooperative_groups;
 // each adds up and stores its own of them.
 constexpr int kLinTma = 4, kLinMma = 5, kLinWarps = 6, kLinThreads = 32 * kLinWarps;
 constexpr int kLinTile = 128 * 128;  // bytes of a weight tile of a stage
-constexpr int kLinRun = 4;           // blocks of k between the sums of an fp32 result
+#ifndef F32RUN
+#define F32RUN 8
+#endif
+constexpr int kLinRun = F32RUN;           // blocks of k between the sums of an fp32 result
 
 __host__ __device__ constexpr int lin_stage(int NR, bool pair) {
     return (pair ? 2 : 1) * kLinTile + NR * 128;
@@ -43,62 +46,110 @@ constexpr size_t lin_smem() {
            sizeof(LinShared<lin_stages(NR, kPair)>);
 }
 
-// Four outputs c .. c + 3 of a row from their sums (and the other half's), as far as
-// they are within n.
-template <bool kPair, bool kF32>
-__device__ __forceinline__ void finish4(const Linear &p, size_t row, int c, float4 v, float4 u) {
-    float a[4] = {v.x, v.y, v.z, v.w}, b[4] = {u.x, u.y, u.z, u.w};
-    const int m = min(4, p.n - c);
-    if (m <= 0) return;
-    const bool quads = (p.n & 3) == 0;
-    const size_t at = row * p.n + c;
-    if (p.bias) {
-        if (quads) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.bias + c));
-            a[0] += bf16_lo(w.x), a[1] += bf16_hi(w.x), a[2] += bf16_lo(w.y), a[3] += bf16_hi(w.y);
-            if (kPair) {
-                const uint2 z = __ldg(reinterpret_cast<const uint2 *>(p.bias + p.n + c));
-                b[0] += bf16_lo(z.x), b[1] += bf16_hi(z.x), b[2] += bf16_lo(z.y),
-                    b[3] += bf16_hi(z.y);
-            }
-        } else {
-            for (int i = 0; i < m; ++i) {
-                a[i] += bf16_lo(__ldg(p.bias + c + i));
-                if (kPair) b[i] += bf16_lo(__ldg(p.bias + p.n + c + i));
-            }
-        }
+// The outputs of a CTA's rows from their sums, which lie in shared memory as
+// [half][row][128 outputs] of each part: added in the parts' order.  A lane has eight
+// outputs of kAtOnce rows, 16 lanes a row.
+constexpr int kAtOnce = 4;
+
+template <int NR, bool kPair, bool kF32>
+struct Finish {
+    const Linear &p;
+    uint32_t sums;  // shared-memory address
+    int parts, row0, m, c0;
+
+    __device__ __forceinline__ uint32_t at(int q, int h, int j, int o) const {
+        uint32_t a;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(a)
+            : "r"(sums + ((h * NR + j) * 128 + o) * 4), "r"(q));
+        return a;
     }
+
+    // n is a multiple of 8; rows j, j + step, ...
+    __device__ __forceinline__ void vectors(int j, int step, const uint4 (&bias)[2],
+                                            const uint4 (&res)[kAtOnce]) const {
+        const int o = (threadIdx.x & 15) * 8, c = c0 + o;
+        float a[8 * kAtOnce] = {}, b[kPair ? 8 * kAtOnce : 8] = {};
+#pragma unroll 1
+        for (int q = 0; q < parts; ++q)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a[i] = activate<kF32>(p.act, a[i]);
-        if (kPair) a[i] *= b[i];
-    }
-    if (!kPair && p.res) {
-        if (quads) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(p.res + at);
-            a[0] += bf16_lo(w.x), a[1] += bf16_hi(w.x), a[2] += bf16_lo(w.y), a[3] += bf16_hi(w.y);
-        } else {
-            for (int i = 0; i < m; ++i) a[i] += bf16_lo(p.res[at + i]);
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int r = min(j + i * step, m - 1);
+#pragma unroll
+                for (int h = 0; h < (kPair ? 4 : 2); ++h) {
+                    const float4 f = ld_dsmem4(at(q, h >> 1, r, o + (h & 1) * 4));
+                    float *to = (h >> 1 ? b : a) + 8 * i + (h & 1) * 4;
+                    to[0] += f.x, to[1] += f.y, to[2] += f.z, to[3] += f.w;
+                }
+            }
+        float w[8];
+        if (p.bias) {
+            unpack8(w, bias[0]);
+#pragma unroll
+            for (int i = 0; i < 8 * kAtOnce; ++i) a[i] += w[i & 7];
+        }
+        activate<kF32>(p.act, a);
+        if (kPair) {
+            if (p.bias) {
+                unpack8(w, bias[1]);
+#pragma unroll
+                for (int i = 0; i < 8 * kAtOnce; ++i) b[kPair ? i : 0] += w[i & 7];
+            }
+#pragma unroll
+            for (int i = 0; i < 8 * kAtOnce; ++i) a[i] *= b[kPair ? i : 0];
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int r = j + i * step;
+            if (r >= m || c >= p.n) continue;
+            float *v = a + 8 * i;
+            if (!kPair && p.res) {
+                unpack8(w, res[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += w[e];
+            }
+            const size_t to = (size_t)(row0 + r) * p.n + c;
+            if (kF32) {
+                *reinterpret_cast<float4 *>(p.yf + to) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4 *>(p.yf + to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                *reinterpret_cast<uint4 *>(p.y + to) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            }
         }
     }
-    if (kF32) {
-        if (quads)
-            *reinterpret_cast<float4 *>(p.yf + at) = make_float4(a[0], a[1], a[2], a[3]);
-        else
-            for (int i = 0; i < m; ++i) p.yf[at + i] = a[i];
-    } else {
-        const uint2 o = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-        if (quads)
-            *reinterpret_cast<uint2 *>(p.y + at) = o;
-        else
-            for (int i = 0; i < m; ++i)
-                p.y[at + i] = (uint16_t)((i & 2 ? o.y : o.x) >> (i & 1) * 16);
+
+    // any n: one output of row j a lane at a time
+    __device__ __forceinline__ void scalars(int j) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
+        for (int o = lane; o < 128 && c0 + o < p.n; o += 32) {
+            const int c = c0 + o;
+            float a[1] = {0.0f}, b = 0.0f;
+            for (int q = 0; q < parts; ++q) {
+                a[0] += ld_dsmemf(at(q, 0, j, o));
+                if (kPair) b += ld_dsmemf(at(q, 1, j, o));
+            }
+            if (p.bias) {
+                a[0] += bf16_lo(__ldg(p.bias + c));
+                if (kPair) b += bf16_lo(__ldg(p.bias + p.n + c));
+            }
+            activate<kF32>(p.act, a);
+            if (kPair) a[0] *= b;
+            const size_t to = (size_t)(row0 + j) * p.n + c;
+            if (!kPair && p.res) a[0] += bf16_lo(p.res[to]);
+            if (kF32)
+                p.yf[to] = a[0];
+            else
+                p.y[to] = (uint16_t)pack_bf16x2(a[0], 0.0f);
+        }
     }
-}
+};
 
 template <int NR, bool kPair, bool kF32>
 __global__ void __launch_bounds__(kLinThreads, NR <= 64 ? 2 : 1)
-    k_linear(const Linear p, const __grid_constant__ CUtensorMap map_x,
+    k_linear(const __grid_constant__ Linear p, const __grid_constant__ CUtensorMap map_x,
              const __grid_constant__ CUtensorMap map_w) {
     constexpr int kStages = lin_stages(NR, kPair), kBytes = lin_stage(NR, kPair);
     constexpr int kHalves = kPair ? 2 : 1;
@@ -231,26 +282,42 @@ __global__ void __launch_bounds__(kLinThreads, NR <= 64 ? 2 : 1)
     }
     tc_fence_after();
     if (warp == kLinMma) tc_free<kCols>(tmem);
+    // what the outputs take beside their sums, asked for before those are there
+    const int step = 2 * parts * kLinWarps, c = c0 + (lane & 15) * 8;
+    int j = (part * kLinWarps + warp) * 2 + (lane >> 4);
+    const bool whole = (p.n & 7) == 0, in = whole && c < p.n;
+    uint4 bias[2] = {}, res[kAtOnce] = {};
+    if (in && p.bias) {
+        bias[0] = __ldg(reinterpret_cast<const uint4 *>(p.bias + c));
+        if (kPair) bias[1] = __ldg(reinterpret_cast<const uint4 *>(p.bias + p.n + c));
+    }
+    const auto residual = [&]() {
+        if (!kPair && in && p.res)
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (j + i * step < m)
+                    res[i] = *reinterpret_cast<const uint4 *>(
+                        p.res + (size_t)(row0 + j + i * step) * p.n + c);
+    };
+    residual();
     // where a part gave up the sums are not whole and no part stores any
     if (parts > 1) cluster.sync();
     const int any = ld_dsmem(dsmem_addr(&s.stop, min(lane, parts - 1)));
-    const bool store = !__any_sync(kFull, any);
-    for (int j = part + warp * parts; store && j < m; j += parts * kLinWarps) {
-        float4 v[kHalves];
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-            const float *at = left + (h * NR + j) * 128 + lane * 4;
-            v[h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int q = 0; q < parts; ++q) {
-                const float4 o = *reinterpret_cast<const float4 *>(
-                    parts > 1 ? cluster.map_shared_rank(at, q) : at);
-                v[h].x += o.x;
-                v[h].y += o.y;
-                v[h].z += o.z;
-                v[h].w += o.w;
+    if (!__any_sync(kFull, any)) {
+        const Finish<NR, kPair, kF32> f = {p, smem_addr(left), parts, row0, m, c0};
+        if (whole) {
+#pragma unroll 1
+            for (; j < m; j += kAtOnce * step) {
+                f.vectors(j, step, bias, res);
+                if (j + kAtOnce * step < m) {
+                    j += kAtOnce * step;
+                    residual();
+                    j -= kAtOnce * step;
+                }
             }
+        } else {
+            for (int r = part * kLinWarps + warp; r < m; r += parts * kLinWarps) f.scalars(r);
         }
-        finish4<kPair, kF32>(p, (size_t)row0 + j, c0 + lane * 4, v[0], v[kHalves - 1]);
     }
     if (parts > 1) cluster.sync();  // no part goes while it is read
 }
@@ -310,6 +377,7 @@ static cudaError_t launch_at(const Linear &p, const LinearPlan &plan, cudaStream
 
 cudaError_t launch_linear(const Linear &p, bool pair, cudaStream_t st) {
     const LinearPlan plan = linear_plan(p.rows, p.n, p.k, pair, p.yf != nullptr, sm_count());
+    if (plan.width) return launch_linear_tiles(p, pair, plan, st);
     if (pair) return launch_at<true, false>(p, plan, st);
     return p.yf ? launch_at<false, true>(p, plan, st) : launch_at<false, false>(p, plan, st);
 }

@@ -18,6 +18,9 @@ __device__ __forceinline__ uint32_t align1024(const void *p) { return -smem_addr
 
 // Where this holds for a thread, its waits below run out at once: a library that
 // is compiled with it shows what a stopped kernel leaves.
+#ifndef SLEEPNS
+#define SLEEPNS 20000u
+#endif
 #ifndef MOE_GIVE_UP
 #define MOE_GIVE_UP false
 #endif
@@ -31,7 +34,7 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(SLEEPNS)
         : "memory");
     return ok != 0;
 }
@@ -69,6 +72,13 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int 
         "[%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
         "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
+}
+
+// The tile to L2 alone: a load of it later finds it there.
+__device__ __forceinline__ void tma_prefetch_tile(const CUtensorMap *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map),
+                 "r"(x), "r"(y)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
@@ -186,6 +196,78 @@ __device__ __forceinline__ void tc_free(uint32_t taddr) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
 }
 
+// ------------------------------------------------------------ two CTAs
+
+// What the two CTAs of a cluster do together: both allocate and free tensor memory;
+// loads of both count on a barrier of one (an address of the cluster's shared
+// memory); that one issues products whose 256-row operand lies half in each CTA's
+// shared memory, by row, as does the other operand, and whose sums lie in each CTA's
+// tensor memory, its own rows'.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
+template <int kCols>
+__device__ __forceinline__ void tc_alloc_pair(uint32_t *where) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(where)),
+                 "n"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+template <int kCols>
+__device__ __forceinline__ void tc_free_pair(uint32_t taddr) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols));
+}
+
+// As tma_tile; `bar` is an address of the cluster's shared memory, of either CTA.
+__device__ __forceinline__ void tma_tile_pair(void *dst, const CUtensorMap *map, int x, int y,
+                                              uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Arrives at a barrier of the cluster.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                 bool accumulate, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
+        : "memory");
+}
+
+// As tc_commit, of the pair's products, at `bar` of both CTAs (bits of their ranks).
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar, uint16_t both, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+        "h"(both), "r"(on)
+        : "memory");
+}
+// At this CTA's alone.
+__device__ __forceinline__ void tc_commit_one_of_pair(uint64_t *bar, uint32_t on) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_addr(bar)),
+        "r"(on)
+        : "memory");
+}
+
 // 16 columns of the warp's 32 lanes, one lane's row a thread.  The values are
 // there after tc_wait_ld.
 __device__ __forceinline__ void tc_ld16(uint32_t (&v)[16], uint32_t taddr) {
@@ -204,6 +286,21 @@ __device__ __forceinline__ void tc_wait_ld() {
 // Makes this thread's shared-memory stores visible to the tensor cores and TMA.
 __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Four floats of a cluster's shared memory.
+__device__ __forceinline__ float4 ld_dsmem4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_dsmemf(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // ------------------------------------------------------------ packed fp32

@@ -1,16 +1,19 @@
 // topk.cu -- moe_topk: a router's choice of experts and their weights from logits.
 //
-// A warp has a token: its logits lie in the lanes' registers, lane l holding experts
-// l * 4 .. l * 4 + 3 of every 128.  What chooses is turned into 32-bit integers
-// whose order is the values', and the R largest are taken one after another by the
-// warp's integer maximum.
+// What chooses is turned into 32-bit integers whose order is the values', so that the
+// choice is integer maxima.  Without a bias the integers are the logits themselves,
+// exactly.  With one, c = s + bias comes from fp32; where two neighbours among the
+// first R + 1, or the kept runs' worths and the others', are closer than both their
+// errors, the token's candidates are evaluated and ordered again more exactly (one
+// token in 2000 at 256 experts).  A warp has a token, or, for up to eight of up to 512
+// experts, four.
 //
-// Without a bias the integers are the logits themselves, exactly.  With one, c = s +
-// bias comes from fp32 and may be kCloseUlps off: where two neighbours among the
-// first R + 1 (or the kept runs' worths) are closer than both errors, the token's
-// candidates are evaluated and ordered again in 64 bits (about one token in a
-// thousand at 256 experts; all of it in 64 bits would take the GPU's fp64 units 30
-// times as long as the logits take to arrive).
+// Measured: 32767 tokens, 8 of 128 experts 11.6 us (1.6 TB/s), of 256 16.8 (2.1 TB/s);
+// 2048 tokens, 8 of 256 4.3, with a bias and four of eight runs kept 10.6.  It is bound
+// by instructions: at 128 experts about 150 a token and lane of eight, most of them in
+// the sorting networks (19 exchanges for eight keys, 12 for each further eight and each
+// doubling of the lanes); one token after another by whole warps took 26 us.  Few
+// tokens are one chain of loads, exchanges and exponentials.
 #include <cmath>
 
 #include "check.h"
@@ -23,6 +26,7 @@ namespace moe {
 struct Router {
     int rows, E, R, score, groups, kept, best, renorm, per;
     unsigned per_inv;  // floor(e / per) == (e * per_inv) >> 20 for e < 1024
+    uint32_t ends;     // bit q: expert 32 q + 31 is the last of its run
     float scale;
     const float *logits, *bias;
     int32_t *idx;
@@ -41,13 +45,38 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// How far fp32's c (or sum of two) is from the 64-bit one, by its magnitude: the
-// exponential's argument and result, the quotient and the sum of exponentials are
-// less than 6 * 2^-24 of a score of at most 1 together, the addition 2^-24 of c.
-__device__ __forceinline__ float error_of(float c) {
-    return 0x1p-20f + fabsf(c) * 0x1p-22f;
+// A score as it is compared, with the fast exponential, e^x within (2 + 1.16 |x|) 2^-23
+// of itself, and the fast quotient, within 2^-22.
+__device__ __forceinline__ float score_about(int score, float l, float top, float inv_sum) {
+    return score == MOE_SCORE_SIGMOID ? __fdividef(1.0f, 1.0f + __expf(-l))
+                                      : __expf(l - top) * inv_sum;
 }
 
+// The same of several logits: which score it is, is asked once, and no one waits for
+// another's (32 a lane by themselves, each behind its own branches, took 3 us).
+template <int n>
+__device__ __forceinline__ void scores_about(int score, const float (&l)[n], float top,
+                                             float inv_sum, float (&s)[n]) {
+    if (score == MOE_SCORE_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) s[i] = score_about(MOE_SCORE_SIGMOID, l[i], 0.0f, 0.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) s[i] = score_about(MOE_SCORE_SOFTMAX, l[i], top, inv_sum);
+    }
+}
+
+// How far c is then from the 64-bit one, by its magnitude.  A sigmoid: s (1 - s) of the
+// exponential's error, at most 0.56 * 2^-23, the addition's 2^-24 and the quotient's
+// 2^-22, less than 2^-21 together.  A softmax: at most 2.5 * 2^-23 by the exponential,
+// its argument's rounding less than 2^-24, and the sum of up to 1024 exponentials, of
+// which no more than 32 are added one after another, within 50 * 2^-24: less than
+// 2^-18.  The addition of the bias rounds once.
+__device__ __forceinline__ float error_of(int score, float c) {
+    return (score == MOE_SCORE_SIGMOID ? 0x1p-21f : 0x1p-18f) + fabsf(c) * 0x1p-23f;
+}
+
+// The same score with the accurate ones, for the weights.
 __device__ __forceinline__ float score32(int score, float l, float top, float inv_sum) {
     return score == MOE_SCORE_SIGMOID ? 1.0f / (1.0f + expf(-l)) : expf(l - top) * inv_sum;
 }
@@ -71,22 +100,91 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Experts a lane holds, and the tokens of a CTA by it: shared memory bounds them.
 __host__ __device__ constexpr int topk_warps(int C) { return C <= 16 ? 4 : 2; }
 
-// A warp's part of the 64-bit evaluation.
+// ------------------------------------------------------------ nearer than fp32
+//
+// What fp32 cannot order is evaluated again, in fixed point with 2^-46 as the unit from
+// pairs of fp32 numbers (sigmoid scores; 17 units off at most), and in fp64 where that
+// is not enough either, or not at hand.  The GPU has few fp64 units: a token's
+// candidates take them 4 us, the other way 1.
+
+// A warp's room for it.
 template <int C>
 struct Exact {
-    double c[C * 32];
+    long long c[C * 32];  // or doubles
     uint16_t list[C * 32];
 };
 
-// An expert's c (its score without a bias) in 64 bits.
-__device__ __forceinline__ double value64(const Router &p, const float *l, int e, float top,
-                                          double sum) {
-    const float v = l[e];
-    double c = p.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-(double)v))
-                                            : exp((double)v - (double)top) / sum;
-    if (p.bias) c += (double)p.bias[e];
-    return v != -INFINITY && c == c ? c : -(double)INFINITY;
+__device__ __forceinline__ void two_sum(float &a, float &b) {  // a + b, and what it lost
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    b = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t));
+    a = s;
 }
+
+// 2^(j / 16) as pairs.
+__constant__ float kRootHigh[16] = {
+    0x1p+0f,        0x1.0b5586p+0f, 0x1.172b84p+0f, 0x1.2387a6p+0f, 0x1.306fep+0f,  0x1.3dea64p+0f,
+    0x1.4bfdaep+0f, 0x1.5ab07ep+0f, 0x1.6a09e6p+0f, 0x1.7a1148p+0f, 0x1.8ace54p+0f, 0x1.9c4918p+0f,
+    0x1.ae89fap+0f, 0x1.c199bep+0f, 0x1.d5818ep+0f, 0x1.ea4afap+0f};
+__constant__ float kRootLow[16] = {
+    0.0f,             0x1.9f3122p-25f, -0x1.c15742p-27f, 0x1.ceac48p-25f,
+    0x1.4636e2p-25f,  0x1.824684p-25f, -0x1.593abcp-25f, -0x1.5bd5ecp-27f,
+    0x1.9fcef4p-26f,  -0x1.829fdp-25f, 0x1.15506ep-27f,  0x1.51f848p-27f,
+    -0x1.a94b14p-26f, -0x1.3d56b2p-27f, -0x1.822dbcp-27f, 0x1.52486cp-27f};
+
+// 1 / (1 + exp(-l)) in units of 2^-46.  exp(y) = 2^(n / 16) e^r with |r| <= ln 2 / 32:
+// y - n ln 2 / 16 with that constant in three parts, of which n times the first two are
+// exact; e^r by its series; the sum and the quotient with their remainders.  Beyond 60
+// it is 0 or 1 as far as a unit goes.
+__device__ __forceinline__ long long sigmoid_fixed(float l) {
+    const float y = -fminf(fmaxf(l, -60.0f), 60.0f);
+    const float n = rintf(__fmul_rn(y, 23.083120654223414f));
+    float h = __fmaf_rn(-n, 0x1.62ep-5f, y), e = -__fmul_rn(n, 0x1.0bep-19f);
+    two_sum(h, e);
+    e = __fmaf_rn(-n, 0x1.be8e7cp-31f, e);
+    two_sum(h, e);  // r
+    const float p = __fmul_rn(h, h), pe = __fmaf_rn(h, h, -p);
+    const float cube = __fmul_rn(
+        __fmul_rn(h, p),
+        __fmaf_rn(h, __fmaf_rn(h, __fmaf_rn(h, 1.0f / 720, 1.0f / 120), 1.0f / 24), 1.0f / 6));
+    float low = __fadd_rn(__fmaf_rn(0.5f, pe, cube), __fmaf_rn(e, h, e));
+    float one = 1.0f, r = h, half = __fmul_rn(0.5f, p);
+    two_sum(one, r);
+    two_sum(one, half);  // e^r = one + low
+    low = __fadd_rn(__fadd_rn(r, half), low);
+    const int k = (int)n, j = k & 15;
+    const float th = kRootHigh[j], by = __int_as_float(((k >> 4) + 127) << 23);
+    float eh = __fmul_rn(one, th);
+    float el = __fadd_rn(__fmaf_rn(one, th, -eh), __fmaf_rn(one, kRootLow[j], __fmul_rn(low, th)));
+    eh = __fmul_rn(eh, by);
+    el = __fmul_rn(el, by);
+    float d = 1.0f;
+    two_sum(d, eh);
+    eh = __fadd_rn(eh, el);
+    two_sum(d, eh);  // the denominator, d + eh
+    const float q = __fdiv_rn(1.0f, d);
+    const float rest = __fmul_rn(q, __fmaf_rn(-q, eh, __fmaf_rn(-q, d, 1.0f)));
+    return __float2ll_rn(q * 0x1p46f) + __float2ll_rn(rest * 0x1p46f);
+}
+// Two values of one or two scores each that are so near are not told apart by it.
+constexpr long long kNear = 128, kNone = -(1LL << 62);
+
+// An expert's c (its score without a bias), in either way; a masked one's is lowest.
+template <class T>
+__device__ __forceinline__ T value_exact(const Router &p, const float *l, int e, float top,
+                                         double sum) {
+    const float v = l[e], b = p.bias ? p.bias[e] : 0.0f;
+    if constexpr (T(0.5) == T(0)) {
+        if (v == -INFINITY || !(fabsf(b) < 32768.0f) || v != v) return kNone;
+        return sigmoid_fixed(v) + __float2ll_rn(b * 0x1p46f);
+    } else {
+        double c = p.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-(double)v))
+                                                : exp((double)v - (double)top) / sum;
+        c += (double)b;
+        return v != -INFINITY && c == c ? c : -(double)INFINITY;
+    }
+}
+// Whether fixed point holds the bias (-infinity and NaN are as good as a masked logit).
+__device__ __forceinline__ bool fits(float b) { return fabsf(b) < 32768.0f || b != b || b == -INFINITY; }
 
 __device__ __forceinline__ double sum64(const Router &p, const float *l, float top) {
     if (p.score == MOE_SCORE_SIGMOID) return 1.0;
@@ -97,109 +195,322 @@ __device__ __forceinline__ double sum64(const Router &p, const float *l, float t
     return sum;
 }
 
-// The kept runs in 64 bits, one bit each, by all lanes of a warp.
-__device__ __noinline__ uint32_t kept64(const Router &p, const float *l, double *c, float top) {
+// The kept runs, one bit each, by all lanes of a warp.  False: not told apart.
+template <class T>
+__device__ __noinline__ bool kept_exact(const Router &p, const float *l, long long *room, float top,
+                                        uint32_t *kept) {
+    constexpr bool kFixed = T(0.5) == T(0);
+    T *c = reinterpret_cast<T *>(room);
     const int lane = threadIdx.x & 31;
-    const double sum = sum64(p, l, top);
-    for (int e = lane; e < p.E; e += 32) c[e] = value64(p, l, e, top, sum);
+    const double sum = kFixed ? 1.0 : sum64(p, l, top);
+    bool ok = true;
+    for (int e = lane; e < p.E; e += 32) {
+        c[e] = value_exact<T>(p, l, e, top, sum);
+        if (kFixed && p.bias) ok &= fits(p.bias[e]);
+    }
     __syncwarp();
-    double worth = -(double)INFINITY;
+    const T none = kFixed ? T(kNone) : T(-(double)INFINITY);
+    T worth = none;
     if (lane < p.groups) {
-        double a = worth, b = worth;  // the two largest
+        T a = none, b = none;  // the two largest
         for (int e = lane * p.per; e < (lane + 1) * p.per; ++e) {
-            b = fmax(b, fmin(a, c[e]));
-            a = fmax(a, c[e]);
+            const T x = c[e];
+            b = max(b, min(a, x));
+            a = max(a, x);
         }
-        worth = p.best == 2 ? a + b : a;
+        worth = p.best == 1 ? a : b == none ? none : a + b;
     }
     int before = 0;
+    bool near = false;
     for (int g = 0; g < p.groups; ++g) {
-        const double o = __shfl_sync(kFull, worth, g);
+        const T o = __shfl_sync(kFull, worth, g);
         before += o > worth || (o == worth && g < lane);
+        if (kFixed && g != lane && worth != none && o != none)
+            near |= o - worth <= T(kNear) && worth - o <= T(kNear);
     }
     __syncwarp();
-    return __ballot_sync(kFull, lane < p.groups && before < p.kept);
+    *kept = __ballot_sync(kFull, lane < p.groups && before < p.kept);
+    return __all_sync(kFull, ok && !(near && lane < p.groups));
 }
 
-// The choice in 64 bits, by all lanes of a warp, of the kept experts whose c is
-// `least` or more in fp32: lane r gets the r-th.  Only with a bias.
-__device__ __noinline__ int choose64(const Router &p, const float *l, double *c, uint16_t *list,
-                                     float top, uint32_t kept, float least) {
+// The choice, by all lanes of a warp, of the kept experts whose c is `least` or more in
+// fp32: lane r gets the r-th.  Only with a bias.  False: not told apart.
+template <class T>
+__device__ __noinline__ bool choose_exact(const Router &p, const float *l, long long *room,
+                                          uint16_t *list, float top, uint32_t kept, float least,
+                                          int *mine) {
+    constexpr bool kFixed = T(0.5) == T(0);
+    T *c = reinterpret_cast<T *>(room);
     const int lane = threadIdx.x & 31;
-    const double sum = sum64(p, l, top);
+    const double sum = kFixed ? 1.0 : sum64(p, l, top);
     int n = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {  // listed in the order of their index
         const int e = e0 + lane;
         bool in = e < p.E && (kept >> run_of(p, e) & 1u);
         if (in) {
             const float v = l[e];
-            float c = score32(p.score, v, top, (float)(1.0 / sum)) + p.bias[e];
-            if (v == -INFINITY || c != c) c = -INFINITY;
-            in = c >= least;
+            float x = score_about(p.score, v, top, (float)(1.0 / sum)) + p.bias[e];
+            if (v == -INFINITY || x != x) x = -INFINITY;
+            in = x >= least;
         }
         const unsigned who = __ballot_sync(kFull, in);
         if (in) list[n + __popc(who & ((1u << lane) - 1u))] = (uint16_t)e;
         n += __popc(who);
     }
     __syncwarp();
-    for (int j = lane; j < n; j += 32) c[j] = value64(p, l, list[j], top, sum);
+    bool ok = true;
+    for (int j = lane; j < n; j += 32) {
+        c[j] = value_exact<T>(p, l, list[j], top, sum);
+        if (kFixed) ok &= fits(p.bias[list[j]]);
+    }
     __syncwarp();
-    int mine = 0;
+    const T none = kFixed ? T(kNone) : T(-(double)INFINITY);
     for (int j0 = 0; j0 < n; j0 += 32) {
         const int j = j0 + lane;
         int before = 32;
         if (j < n) {
+            const T x = c[j];
             before = 0;
-            for (int o = 0; o < n; ++o) before += c[o] > c[j] || (c[o] == c[j] && o < j);
+            for (int o = 0; o < n; ++o) {
+                const T y = c[o];
+                before += y > x || (y == x && o < j);
+                if (kFixed && o != j && x != none && y != none)
+                    ok &= y - x > T(kNear) || x - y > T(kNear);
+            }
         }
         for (int o = 0; o < 32; ++o)  // candidate j0 + o goes to the lane of its rank
-            if (__shfl_sync(kFull, before, o) == lane) mine = list[j0 + o];
+            if (__shfl_sync(kFull, before, o) == lane) *mine = list[j0 + o];
     }
-    return mine;
+    __syncwarp();
+    return __all_sync(kFull, ok);
+}
+
+// A lane's logits: v[4 q + j] is expert 128 q + 4 lane + j; -infinity behind the last.
+__device__ __forceinline__ int expert_at(int i) {
+    return (i >> 2) * 128 + (threadIdx.x & 31) * 4 + (i & 3);
+}
+template <int C>
+__device__ __forceinline__ void load_logits(const Router &p, const float *l, float (&v)[C]) {
+    const bool quads = (p.E & 3) == 0;  // then every row starts on 16 bytes
+#pragma unroll
+    for (int q = 0; q < C / 4; ++q) {
+        const int e = expert_at(4 * q);
+        float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (quads) {
+            if (e < p.E) f = __ldg(reinterpret_cast<const float4 *>(l + e));
+        } else {
+            if (e < p.E) f.x = __ldg(l + e);
+            if (e + 1 < p.E) f.y = __ldg(l + e + 1);
+            if (e + 2 < p.E) f.z = __ldg(l + e + 2);
+            if (e + 3 < p.E) f.w = __ldg(l + e + 3);
+        }
+        v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+    }
+}
+
+// What is compared, c or the logits: masked experts last, those behind the last and
+// those of runs that are not kept not there at all.
+template <int C>
+__device__ __forceinline__ void make_keys(const Router &p, const float (&v)[C], float top,
+                                          float inv_sum, uint32_t kept, uint32_t (&key)[C]) {
+    if (p.bias) {
+        float b[C], c[C];
+#pragma unroll
+        for (int q = 0; q < C / 4; ++q) {
+            const int e = expert_at(4 * q);
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if ((p.E & 3) == 0) {
+                if (e < p.E) f = __ldg(reinterpret_cast<const float4 *>(p.bias + e));
+            } else {
+                if (e < p.E) f.x = __ldg(p.bias + e);
+                if (e + 1 < p.E) f.y = __ldg(p.bias + e + 1);
+                if (e + 2 < p.E) f.z = __ldg(p.bias + e + 2);
+                if (e + 3 < p.E) f.w = __ldg(p.bias + e + 3);
+            }
+            b[4 * q] = f.x, b[4 * q + 1] = f.y, b[4 * q + 2] = f.z, b[4 * q + 3] = f.w;
+        }
+        scores_about(p.score, v, top, inv_sum, c);
+#pragma unroll
+        for (int i = 0; i < C; ++i) key[i] = key_of(v[i] == -INFINITY ? v[i] : c[i] + b[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) key[i] = key_of(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        if (expert_at(i) >= p.E) key[i] = 0u;
+    if (kept != ~0u) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (!(kept >> run_of(p, expert_at(i)) & 1u)) key[i] = 0u;
+    }
+}
+
+// What a run's worth is made of: c, or the scores where there is no bias and two are
+// added.
+template <int n>
+__device__ __forceinline__ void run_values(const Router &p, const float (&v)[n],
+                                           const uint32_t (&key)[n], float top, float inv_sum,
+                                           bool scored, float (&c)[n]) {
+    if (scored)
+        scores_about(p.score, v, top, inv_sum, c);
+    else
+#pragma unroll
+        for (int i = 0; i < n; ++i) c[i] = value_of(key[i]);
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+        if (key[i] <= kLowest) c[i] = -INFINITY;
+}
+
+// The runs that are kept, one bit each; keys are of all experts.
+template <int C>
+__device__ __forceinline__ uint32_t kept_runs(const Router &p, const float *l, const float (&v)[C],
+                                              const uint32_t (&key)[C], float top, float inv_sum,
+                                              long long *room) {
+    const int lane = threadIdx.x & 31;
+    float slack = 0.0f;  // both errors of two runs' worths
+    uint32_t mine = 0;   // lane g: the worth of run g
+    const bool sums = p.best == 2, scored = !p.bias && sums;
+    if (p.per >= 4 && p.per <= 128 && (p.per & (p.per - 1)) == 0) {
+        // a run is p.per / 4 neighbouring lanes' quads: their best two by exchanges.  The
+        // way below asks all lanes for each run: 2048 tokens, 256 experts in eight runs
+        // 24.0 us that way, 9.5 this
+        float worths[C];
+        run_values(p, v, key, top, inv_sum, scored, worths);
+#pragma unroll
+        for (int q = 0; q < C / 4; ++q) {
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int i = 4 * q; i < 4 * q + 4; ++i) {
+                b = fmaxf(b, fminf(a, worths[i]));
+                a = fmaxf(a, worths[i]);
+            }
+            for (int d = p.per >> 3; d > 0; d >>= 1) {
+                const float oa = __shfl_xor_sync(kFull, a, d), ob = __shfl_xor_sync(kFull, b, d);
+                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                a = fmaxf(a, oa);
+            }
+            const float worth = sums ? a + b : a;
+            if (worth > -INFINITY)
+                slack = fmaxf(slack, 2.0f * (error_of(p.score, a) +
+                                             (sums ? error_of(p.score, b) : 0.0f)));
+            // to lane g from the first lane of run g
+            const int e = lane * p.per;
+            const float got = __shfl_sync(kFull, worth, (e & 127) >> 2);
+            if (lane < p.groups && (e >> 7) == q) mine = key_of(got);
+        }
+        slack = warp_max(slack);
+    } else {
+        for (int g = 0; g < p.groups; ++g) {
+            uint32_t a = 0, b = 0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                if (run_of(p, expert_at(i)) != g) continue;
+                uint32_t k = key[i];
+                if (scored && k > kLowest) k = key_of(score_about(p.score, v[i], top, inv_sum));
+                b = max(b, min(a, k));
+                a = max(a, k);
+            }
+            const uint32_t first = __reduce_max_sync(kFull, a);
+            uint32_t worth = first;
+            float error = error_of(p.score, value_of(first));
+            if (sums) {
+                const unsigned who = __ballot_sync(kFull, a == first);
+                // the second largest: the others' first, or this lane's second
+                const uint32_t rest = (who & (who - 1)) || a != first ? a : b;
+                const uint32_t second = __reduce_max_sync(kFull, rest);
+                worth = key_of(value_of(first) + value_of(second));
+                error += error_of(p.score, value_of(second));
+            }
+            if (worth > kLowest) slack = fmaxf(slack, 2.0f * error);
+            if (lane == g) mine = worth;
+        }
+    }
+    int before = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const uint32_t o = __shfl_sync(kFull, mine, g);
+        before += o > mine || (o == mine && g < lane);
+    }
+    const bool run = lane < p.groups;
+    uint32_t kept = __ballot_sync(kFull, run && before < p.kept);
+    if (p.bias || sums) {
+        // the least kept and the best of the others
+        const uint32_t in = __reduce_min_sync(kFull, run && before < p.kept ? mine : ~0u);
+        const uint32_t out = __reduce_max_sync(kFull, run && before >= p.kept ? mine : 0u);
+        if (out > kLowest && value_of(in) - value_of(out) <= slack)
+            if (p.score != MOE_SCORE_SIGMOID || !kept_exact<long long>(p, l, room, top, &kept))
+                kept_exact<double>(p, l, room, top, &kept);
+    }
+    return kept;
+}
+
+// The R largest keys, one after another: lane r gets the r-th's expert.  With a bias,
+// whether two neighbours, or the last and the one behind it, are nearer than their
+// errors (close), and the last key that was looked at.
+struct Chosen {
+    int mine;
+    uint32_t last;
+    bool close;
+};
+
+__device__ __forceinline__ bool near(const Router &p, uint32_t last, uint32_t next) {
+    const float a = value_of(last), b = value_of(next);
+    return b > -INFINITY && a - b <= error_of(p.score, a) + error_of(p.score, b);
 }
 
 template <int C>
-__global__ void __launch_bounds__(32 * topk_warps(C)) k_topk(const Router p) {
-    constexpr int kWarps = topk_warps(C);
-    __shared__ Exact<C> exact[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int row = blockIdx.x * kWarps + warp;
-    if (row >= p.rows) return;
-    const float *l = p.logits + (size_t)row * p.E;
-    // v[4 q + j]: expert 128 q + 4 lane + j
-    float v[C];
-    const bool quads = (p.E & 3) == 0;  // then every row starts on 16 bytes
+__device__ __forceinline__ Chosen take_any(const Router &p, uint32_t (&key)[C]) {
+    const int lane = threadIdx.x & 31;
+    Chosen got = {0, ~0u, false};
+    for (int r = 0; r <= p.R; ++r) {
+        if (r == p.R && !p.bias) break;
+        uint32_t m = key[0];
 #pragma unroll
-    for (int q = 0; q < (C + 3) / 4; ++q) {
-        const int e = q * 128 + lane * 4;
-        if (quads) {
-            float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (e < p.E) f = __ldg(reinterpret_cast<const float4 *>(l + e));
-            v[4 * q] = f.x;
-            v[4 * q + 1] = f.y;
-            v[4 * q + 2] = f.z;
-            v[4 * q + 3] = f.w;
-        } else {
+        for (int i = 1; i < C; ++i) m = max(m, key[i]);
+        const uint32_t most = __reduce_max_sync(kFull, m);
+        if (most == 0u) break;  // no one is behind the R
+        if (p.bias && got.last != ~0u) got.close |= near(p, got.last, most);
+        got.last = most;
+        if (r == p.R) break;
+        // its place in the lanes that have it, and of those the lowest
+        int i0 = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * q + j] = e + j < p.E ? __ldg(l + e + j) : -INFINITY;
+        for (int i = C - 1; i >= 0; --i)
+            if (key[i] == most) i0 = i;
+        const unsigned at = m == most ? (unsigned)expert_at(i0) : ~0u;
+        const unsigned first = __reduce_min_sync(kFull, at);
+        if (at == first) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                if (i == i0) key[i] = 0u;
         }
+        if (lane == r) got.mine = (int)first;
     }
-    const auto expert = [&](int i) { return (i >> 2) * 128 + lane * 4 + (i & 3); };
+    return got;
+}
+
+// One token, by all lanes of a warp.
+template <int C>
+__device__ __noinline__ void token_by_warp_apart(const Router &p, int row, Exact<C> &exact);
+template <int C>
+__device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C> &exact) {
+    const int lane = threadIdx.x & 31;
+    const float *l = p.logits + (size_t)row * p.E;
+    float v[C];
+    load_logits(p, l, v);
     bool bad = false;
-    float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
+    for (int i = 0; i < C; ++i)
         bad |= v[i] != v[i] || (p.score == MOE_SCORE_SOFTMAX && v[i] == INFINITY);
-        top = fmaxf(top, v[i]);
-    }
     bad = __any_sync(kFull, bad);
-    top = warp_max(top);
-    // the sum of the exponentials, where a value needs it
-    const bool scores = p.bias || (p.groups > 1 && p.best == 2);
-    float inv_sum = 1.0f;
+    // the softmax's maximum and sum, where a value needs them
+    const bool scores = p.bias || (p.groups > p.kept && p.best == 2);
+    float top = 0.0f, inv_sum = 1.0f;
     if (p.score == MOE_SCORE_SOFTMAX && (scores || !p.renorm)) {
+        top = v[0];
+#pragma unroll
+        for (int i = 1; i < C; ++i) top = fmaxf(top, v[i]);
+        top = warp_max(top);
         float sum = 0.0f;
         if (top > -INFINITY)
 #pragma unroll
@@ -207,138 +518,368 @@ __global__ void __launch_bounds__(32 * topk_warps(C)) k_topk(const Router p) {
         sum = warp_sum(sum);
         inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    // what is compared: c, or the logits; masked experts last, the padding not there
-    uint32_t key[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int e = expert(i);
-        float c = v[i];
-        if (p.bias && e < p.E && v[i] != -INFINITY)
-            c = score32(p.score, v[i], top, inv_sum) + __ldg(p.bias + e);
-        key[i] = e < p.E ? key_of(c) : 0u;
-    }
-    // the kept runs
-    uint32_t kept = 0xffffffffu;
+    uint32_t key[C], kept = ~0u;
+    make_keys(p, v, top, inv_sum, ~0u, key);
     if (p.groups > p.kept) {
-        float slack = 0.0f;  // both errors of two runs' worths
-        uint32_t mine = 0;  // lane g: the worth of run g
-        for (int g = 0; g < p.groups; ++g) {
-            uint32_t a = 0, b = 0;
+        kept = kept_runs(p, l, v, key, top, inv_sum, exact.c);
+        if ((p.per & 3) == 0) {  // a quad is of one run
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                if (run_of(p, expert(i)) != g) continue;
-                uint32_t k = key[i];
-                if (!p.bias && p.best == 2 && k > kLowest)
-                    k = key_of(score32(p.score, v[i], top, inv_sum));
-                b = max(b, min(a, k));
-                a = max(a, k);
-            }
-            const uint32_t first = __reduce_max_sync(kFull, a);
-            uint32_t worth = first;
-            float error = error_of(value_of(first));
-            if (p.best == 2) {
-                const unsigned who = __ballot_sync(kFull, a == first);
-                // the second largest: the others' first, or this lane's second
-                const uint32_t rest = (who & (who - 1)) || a != first ? a : b;
-                const uint32_t second = __reduce_max_sync(kFull, rest);
-                worth = key_of(value_of(first) + value_of(second));
-                error += error_of(value_of(second));
-            }
-            if (worth > kLowest) slack = fmaxf(slack, 2.0f * error);
-            if (lane == g) mine = worth;
-        }
-        int before = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const uint32_t o = __shfl_sync(kFull, mine, g);
-            before += o > mine || (o == mine && g < lane);
-        }
-        const bool run = lane < p.groups;
-        kept = __ballot_sync(kFull, run && before < p.kept);
-        if (p.bias || p.best == 2) {
-            // the least kept and the best of the others
-            const uint32_t in = __reduce_min_sync(kFull, run && before < p.kept ? mine : ~0u);
-            const uint32_t out = __reduce_max_sync(kFull, run && before >= p.kept ? mine : 0u);
-            if (out > kLowest && value_of(in) - value_of(out) <= slack)
-                kept = kept64(p, l, exact[warp].c, top);
-        }
+            for (int q = 0; q < C / 4; ++q)
+                if (!(kept >> run_of(p, expert_at(4 * q)) & 1u))
+                    key[4 * q] = key[4 * q + 1] = key[4 * q + 2] = key[4 * q + 3] = 0u;
+        } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (!(kept >> run_of(p, expert(i)) & 1u)) key[i] = 0u;
+            for (int i = 0; i < C; ++i)
+                if (!(kept >> run_of(p, expert_at(i)) & 1u)) key[i] = 0u;
+        }
     }
-    // the R largest, and with a bias the one behind them
-    int mine = 0;
-    bool close = false;
-    uint32_t last = ~0u;
-    const int rounds = p.bias ? p.R + 1 : p.R;
-    for (int r = 0; r < rounds; ++r) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < C; ++i) m = max(m, key[i]);
-        const uint32_t most = __reduce_max_sync(kFull, m);
-        if (most == 0u) break;  // no one is behind the R
-        if (p.bias && last != ~0u) {
-            const float a = value_of(last), b = value_of(most);
-            close |= b > -INFINITY && a - b <= error_of(a) + error_of(b);
-        }
-        last = most;
-        int at = 0x10000;
-#pragma unroll
-        for (int i = C - 1; i >= 0; --i)
-            if (key[i] == most) at = expert(i);
-        const int e = (int)__reduce_min_sync(kFull, (unsigned)at);
-        if (r == p.R) break;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (expert(i) == e) key[i] = 0u;
-        if (lane == r) mine = e;
-    }
-    if (close) {
+    Chosen got = take_any(p, key);
+    if (got.close) {
         // nothing below the last one by more than both errors can be among the first R
-        const float c = value_of(last);
-        mine = choose64(p, l, exact[warp].c, exact[warp].list, top, kept,
-                        c > -INFINITY ? c - 2.0f * error_of(c) : -INFINITY);
+        const float c = value_of(got.last);
+        const float least = c > -INFINITY ? c - 2.0f * error_of(p.score, c) : -INFINITY;
+        int mine = 0;
+        if (p.score != MOE_SCORE_SIGMOID ||
+            !choose_exact<long long>(p, l, exact.c, exact.list, top, kept, least, &mine))
+            choose_exact<double>(p, l, exact.c, exact.list, top, kept, least, &mine);
+        got.mine = mine;
     }
-    // the weights, lane r the r-th
+    // the weights, lane r the r-th; sums over as many lanes as there may be
+    const int half = p.R > 8 ? 16 : 4;
     const bool chosen = lane < p.R;
-    const float lv = chosen ? __ldg(l + mine) : -INFINITY;
+    const float lv = chosen ? __ldg(l + got.mine) : -INFINITY;
     float s = 0.0f;
     if (p.renorm) {
         // all of them times exp(-m), so that small ones keep their ratios
-        const float m = warp_max(lv);
+        float m = lv;
+        for (int d = half; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
         if (lv > -INFINITY)
             s = p.score == MOE_SCORE_SOFTMAX ? expf(lv - m)
                 : m >= 0.0f                  ? score32(p.score, lv, top, inv_sum)
                                              : expf(lv - m) / (1.0f + expf(lv));
-        const float sum = warp_sum(s);
+        float sum = s;
+        for (int d = half; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
         s = sum > 0.0f ? s / sum : 0.0f;
     } else if (lv > -INFINITY) {
         s = score32(p.score, lv, top, inv_sum);
     }
     if (chosen) {
-        p.idx[(size_t)row * p.R + lane] = mine;
+        p.idx[(size_t)row * p.R + lane] = got.mine;
         p.w[(size_t)row * p.R + lane] = bad ? __uint_as_float(0x7fffffffu) : s * p.scale;
     }
 }
 
 template <int C>
-static cudaError_t launch(const Router &p, cudaStream_t st) {
+__global__ void __launch_bounds__(32 * topk_warps(C)) k_topk(const __grid_constant__ Router p) {
+    constexpr int kWarps = topk_warps(C);
+    __shared__ Exact<C> exact[kWarps];
+    const int warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int row = blockIdx.x * kWarps + warp;
+    if (row < p.rows) token_by_warp(p, row, exact[warp]);
+}
+
+template <int C>
+__device__ __noinline__ void token_by_warp_apart(const Router &p, int row, Exact<C> &exact) {
+    token_by_warp(p, row, exact);
+}
+
+// ------------------------------------------------------------ eight lanes a token
+//
+// Up to eight experts of up to 512, four tokens a warp: lane `sub` of a token's eight
+// holds experts 32 q + 4 sub .. + 3.  The eight largest keys come from sorting networks
+// on the keys alone (two instructions an exchange), eight at a time in a lane and then
+// over the lanes; a key's place is how many of them are larger.  Where keys are equal
+// or too near each other, or runs' worths are, the token goes through the warp's way
+// above, all lanes together.
+
+constexpr int kFastMost = 8, kFastWarps = 4;
+
+__device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b) {  // the larger to a
+    const uint32_t m = max(a, b);
+    b = min(a, b);
+    a = m;
+}
+// Batcher's odd-even merge sort of eight, largest first.
+__device__ __forceinline__ void sort8(uint32_t (&k)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) exchange(k[i], k[i + 1]);
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        exchange(k[i], k[i + 2]);
+        exchange(k[i + 1], k[i + 3]);
+        exchange(k[i + 1], k[i + 2]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) exchange(k[i], k[i + 4]);
+    exchange(k[2], k[4]);
+    exchange(k[3], k[5]);
+#pragma unroll
+    for (int i = 1; i < 7; i += 2) exchange(k[i], k[i + 1]);
+}
+// The eight largest of a first and then a falling row, sorted again.
+__device__ __forceinline__ void resort8(uint32_t (&k)[8]) {
+#pragma unroll
+    for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) exchange(k[i], k[i + d]);
+}
+
+// S: experts a lane holds.
+template <int S>
+__global__ void __launch_bounds__(32 * kFastWarps, S <= 16 ? 8 : S <= 32 ? 6 : 3)
+    k_topk_fast(const __grid_constant__ Router p) {
+    constexpr int Q = S / 4, C = S <= 16 ? 4 : S <= 32 ? 8 : 16;
+    // keys to look up by number, and later the room of the other way
+    union Room {
+        Exact<C> exact;
+        uint32_t key[S][32];
+    };
+    __shared__ Room room[kFastWarps];
+    __shared__ int chosen[kFastWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int row0 = (blockIdx.x * kFastWarps + warp) * 4;
+    if (row0 >= p.rows) return;
+    const int row = row0 + (lane >> 3);
+    const bool there = row < p.rows;
+    const float *l = p.logits + (size_t)(there ? row : row0) * p.E;
+    float v[S];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (32 * q + 4 * sub < p.E) f = __ldg(reinterpret_cast<const float4 *>(l + 32 * q + 4 * sub));
+        v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+    }
+    const auto over = [&](auto f, float x) {  // of the token's lanes
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) x = f(x, __shfl_xor_sync(kFull, x, d));
+        return x;
+    };
+    const auto greater = [](float a, float b) { return fmaxf(a, b); };
+    const auto less = [](float a, float b) { return fminf(a, b); };
+    const auto plus = [](float a, float b) { return a + b; };
+    // tokens whose logits are not numbers, too, go the other way
+    bool slow = false;
+#pragma unroll
+    for (int i = 0; i < S; ++i) slow |= !(v[i] < INFINITY);
+    const bool grouped = p.groups > p.kept, sums = p.best == 2;
+    const bool scored = grouped && sums && !p.bias;
+    float top = 0.0f, inv_sum = 1.0f;
+    if (p.score == MOE_SCORE_SOFTMAX && (p.bias || scored || !p.renorm)) {
+        top = v[0];
+#pragma unroll
+        for (int i = 1; i < S; ++i) top = fmaxf(top, v[i]);
+        top = over(greater, top);
+        float sum[4] = {};
+        if (top > -INFINITY)
+#pragma unroll
+            for (int i = 0; i < S; ++i) sum[i & 3] += expf(v[i] - top);
+        sum[0] = over(plus, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        inv_sum = sum[0] > 0.0f ? 1.0f / sum[0] : 0.0f;
+    }
+    uint32_t key[S];
+    if (p.bias) {
+        float c[S];
+        scores_about(p.score, v, top, inv_sum, c);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int e = 32 * q + 4 * sub;
+            float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (e < p.E) b = __ldg(reinterpret_cast<const float4 *>(p.bias + e));
+            c[4 * q] += b.x, c[4 * q + 1] += b.y, c[4 * q + 2] += b.z, c[4 * q + 3] += b.w;
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i) key[i] = key_of(v[i] == -INFINITY ? v[i] : c[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) key[i] = key_of(v[i]);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)  // E is a multiple of four
+        if (32 * q + 4 * sub >= p.E)
+            key[4 * q] = key[4 * q + 1] = key[4 * q + 2] = key[4 * q + 3] = 0u;
+    if (grouped) {
+        // p.per is a multiple of 32: a run is p.per / 32 whole q, which all lanes share.
+        // worth[q]: of the run that ends with q, else nothing
+        float worth[Q], a = -INFINITY, b = -INFINITY, slack = 0.0f, worths[S];
+        run_values(p, v, key, top, inv_sum, scored, worths);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            float a0 = -INFINITY, b0 = -INFINITY;
+#pragma unroll
+            for (int i = 4 * q; i < 4 * q + 4; ++i) {
+                b0 = fmaxf(b0, fminf(a0, worths[i]));
+                a0 = fmaxf(a0, worths[i]);
+            }
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) {
+                const float oa = __shfl_xor_sync(kFull, a0, d), ob = __shfl_xor_sync(kFull, b0, d);
+                b0 = fmaxf(fminf(a0, oa), fmaxf(b0, ob));
+                a0 = fmaxf(a0, oa);
+            }
+            const bool starts = q == 0 || (p.ends >> (q - 1) & 1u), ends = p.ends >> q & 1u;
+            b = starts ? b0 : fmaxf(fminf(a, a0), fmaxf(b, b0));
+            a = starts ? a0 : fmaxf(a, a0);
+            worth[q] = ends ? (sums ? a + b : a) : -INFINITY;
+            if (worth[q] > -INFINITY)
+                slack = fmaxf(slack, 2.0f * (error_of(p.score, a) +
+                                             (sums ? error_of(p.score, b) : 0.0f)));
+        }
+        // lane sub ranks the runs that end with q = sub, sub + 8
+        uint32_t ends = 0;
+        float least = INFINITY, best = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < (Q + 7) / 8; ++h) {
+            float mine = -INFINITY;
+#pragma unroll
+            for (int q = 8 * h; q < 8 * h + 8; ++q)
+                if (q < Q && q - 8 * h == sub) mine = worth[q < Q ? q : 0];
+            int before = 0;
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                before += worth[q] > mine || (worth[q] == mine && q < 8 * h + sub);
+            // a run without any expert in service may be among the kept: the other way
+            const bool run = mine > -INFINITY, in = run && before < p.kept;
+            ends |= (__ballot_sync(kFull, in) >> (lane & 24) & 0xffu) << (8 * h);
+            if (in) least = fminf(least, mine);
+            if (run && !in) best = fmaxf(best, mine);
+        }
+        least = over(less, least);
+        best = over(greater, best);
+        slow |= __popc(ends) != p.kept;
+        slow |= best > -INFINITY && least - best <= (p.bias || sums ? slack : 0.0f);
+        bool in = false;
+#pragma unroll
+        for (int q = Q - 1; q >= 0; --q) {
+            if (p.ends >> q & 1u) in = ends >> q & 1u;
+            if (!in) key[4 * q] = key[4 * q + 1] = key[4 * q + 2] = key[4 * q + 3] = 0u;
+        }
+    }
+    // the eight largest keys, in order, in every lane of the token
+    uint32_t t[8];
+#pragma unroll
+    for (int g = 0; g < S / 8; ++g) {
+        uint32_t k[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = key[8 * g + i];
+        sort8(k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = g == 0 ? k[i] : max(t[i], k[7 - i]);
+        if (g > 0) resort8(t);
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) {
+        uint32_t k[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = __shfl_xor_sync(kFull, t[7 - i], d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = max(t[i], k[i]);
+        resort8(t);
+    }
+    uint32_t last = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i == p.R - 1) last = t[i];
+        if (i > 0 && i < p.R) slow |= p.bias ? near(p, t[i - 1], t[i]) : t[i] == t[i - 1];
+    }
+    slow |= last <= kLowest;
+    // the keys that are, or may be, among the first R
+    const float c = value_of(last);
+    const uint32_t least = p.bias && last > kLowest ? key_of(c - 2.0f * error_of(p.score, c)) : last;
+    uint64_t hits = 0;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        const bool hit = key[i] >= least;
+        hits |= (uint64_t)hit << i;
+        n += hit;
+    }
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) n += __shfl_xor_sync(kFull, n, d);
+    slow |= n != p.R;
+    const unsigned slows = __ballot_sync(kFull, slow && there);
+    slow = slows >> (lane & 24) & 0xffu;
+    int *mine = chosen[warp] + (lane & 24);
+#pragma unroll
+    for (int i = 0; i < S; ++i) room[warp].key[i][lane] = key[i];
+    if (!slow) {
+        while (hits) {  // each lane its own: what it wrote itself
+            const int i = __ffsll((long long)hits) - 1, e = 32 * (i >> 2) + 4 * sub + (i & 3);
+            hits &= hits - 1;
+            const uint32_t k = room[warp].key[i][lane];
+            int place = 0;
+#pragma unroll
+            for (int o = 0; o < 8; ++o) place += t[o] > k;
+            mine[place & 7] = e;
+        }
+    }
+    __syncwarp();
+    if (!slow && there) {
+        // the weights: the token's lanes are among themselves here
+        const unsigned who = 0xffu << (lane & 24);
+        const int e = sub < p.R ? mine[sub] : 0;
+        const float lv = sub < p.R ? __ldg(l + e) : -INFINITY;
+        float s = 0.0f;
+        if (p.renorm) {
+            float m = lv;
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(who, m, d));
+            if (sub < p.R)
+                s = p.score == MOE_SCORE_SOFTMAX ? expf(lv - m)
+                    : m >= 0.0f                  ? score32(p.score, lv, top, inv_sum)
+                                                 : expf(lv - m) / (1.0f + expf(lv));
+            float sum = s;
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(who, sum, d);
+            s = s / sum;
+        } else if (sub < p.R) {
+            s = score32(p.score, lv, top, inv_sum);
+        }
+        if (sub < p.R) {
+            p.idx[(size_t)row * p.R + sub] = e;
+            p.w[(size_t)row * p.R + sub] = s * p.scale;
+        }
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k)
+        if (slows >> (8 * k) & 0xffu) token_by_warp_apart(p, row0 + k, room[warp].exact);
+}
+
+template <class K>
+static cudaError_t launch(K kern, int tokens, int warps, const Router &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)((p.rows + topk_warps(C) - 1) / topk_warps(C)));
-    cfg.blockDim = dim3(32 * topk_warps(C));
+    cfg.gridDim = dim3((unsigned)(((long long)p.rows + tokens - 1) / tokens));
+    cfg.blockDim = dim3(32 * warps);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_topk<C>, p);
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 static cudaError_t launch_topk(const Router &p, cudaStream_t st) {
-    if (p.E <= 128) return launch<4>(p, st);
-    if (p.E <= 256) return launch<8>(p, st);
-    if (p.E <= 512) return launch<16>(p, st);
-    return launch<32>(p, st);
+    // us with a warp and with eight lanes a token, 256 experts: one token 3.5 and 3.2, 2048
+    // 6.6 and 4.3, 32767 32 and 17; with a bias and four of eight runs 8 tokens 4.7 and
+    // 6.1, 2048 10.6 and 12.2, 8192 17 and 23, 32767 53 and 40: there some tokens go
+    // the warp's way after the other
+    if (p.R <= kFastMost && p.E >= 32 && p.E <= 512 && p.E % 4 == 0 &&
+        (p.groups == p.kept || p.per % 32 == 0) && (!p.bias || p.rows > 96 * sm_count())) {
+        const auto kern = p.E <= 128   ? k_topk_fast<16>
+                          : p.E <= 256 ? k_topk_fast<32>
+                          : p.E <= 384 ? k_topk_fast<48>
+                                       : k_topk_fast<64>;
+        return launch(kern, 4 * kFastWarps, kFastWarps, p, st);
+    }
+    const auto kern = p.E <= 128 ? k_topk<4> : p.E <= 256 ? k_topk<8> : p.E <= 512 ? k_topk<16> : k_topk<32>;
+    const int warps = p.E <= 512 ? topk_warps(16) : topk_warps(32);
+    return launch(kern, warps, warps, p, st);
 }
 
 }  // namespace moe
@@ -361,10 +902,13 @@ extern "C" int moe_topk(const moe_shape *sh, int score, int groups, int kept, in
         !moe::ok_buffer(topk_idx, z.bytes_topk_idx) || !moe::ok_buffer(topk_w, z.bytes_topk_idx))
         return MOE_EINVAL;
     if (rows == 0) return MOE_OK;
-    if (rows >= ((int64_t)1 << 31) - 4) return MOE_ENOTSUP;
+    if (rows >= ((int64_t)1 << 31) - 64) return MOE_ENOTSUP;
     const unsigned inv = ((1u << 20) + per - 1) / per;
-    const moe::Router p = {(int)rows, sh->E,  sh->R, score,  groups, kept,     best,  renorm != 0,
-                           per,       inv,    scale, logits, bias,   topk_idx, topk_w};
+    uint32_t ends = 0;
+    for (int q = 0; q < 32 && 32 * q + 31 < sh->E; ++q)
+        if ((32 * q + 32) % per == 0) ends |= 1u << q;
+    const moe::Router p = {(int)rows, sh->E, sh->R, score, groups, kept, best,     renorm != 0,
+                           per,       inv,   ends,  scale, logits, bias, topk_idx, topk_w};
     return moe::launch_topk(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
                                                                                       : MOE_ECUDA;
 }

@@ -545,7 +545,7 @@ int moe_layer_few(const moe_shape *shape, int inter, const uint16_t *x_bf16,
  *   NULL, and one of y_bf16 [N*T][n] and y_f32 [N*T][n]
  * The product, the bias, the activation and the residual are fp32, rounded once.
  * Products of bf16 values are exact; the tensor cores sum them in fp32.  With
- * y_f32 (a router's logits, which choose) their sums are taken out every 256 along
+ * y_f32 (a router's logits, which choose) their sums are taken out every 512 along
  * k and added there, rounding to nearest.  y_bf16 may be res (each element is read
  * before it is written, by the same thread); other overlaps of outputs with inputs
  * are not allowed.  status as for moe_expert_gemm. */

@@ -6,9 +6,11 @@ Bounds, with u = 2^-24:
   * a product: bf16 products are exact, their sum goes through at most k fp32
     additions in the tensor cores, each of which may truncate (2 u of the sum of
     magnitudes), then at most 8 more of a cluster's parts and the bias: 2 (k + 8) u
-    times the sum of magnitudes.  fp32 results: at most 256 such additions before a
-    sum is taken out, then k / 256 that round: (512 + k / 256 + 16) u;
-  * an activation: its slope is at most 1.13, its value comes with (|v| + 16) 2 u;
+    times the sum of magnitudes.  fp32 results: at most 512 such additions before a
+    sum is taken out, then k / 512 that round: (1024 + k / 512 + 16) u;
+  * an activation: its slope is at most 1.13, its value comes with (|v| + 16) 2 u; a
+    gelu's exponential is of v^2 / 2, which adds v^2 2 u, and where the result is bf16
+    its fitted polynomial is 2^-19 off; for v < 0 that is relative, above it less;
   * norms: the fp32 sum of H squares is at most H additions, the rest twelve
     operations; an error of v moves rstd by at most the mean of v's relative errors;
   * a bf16 result: half a step, at most 2^-8 of the value.
@@ -35,8 +37,12 @@ def act64(name: str, v: torch.Tensor) -> torch.Tensor:
     return torch.sigmoid(v) if name == "sigmoid" else v
 
 
-def act_error(a: torch.Tensor, v: torch.Tensor, err: torch.Tensor) -> torch.Tensor:
-    return 1.13 * err + (v.abs() + 16) * 2 * U * a.abs() + 2.0 ** -119
+def act_error(name: str, a: torch.Tensor, v: torch.Tensor, err: torch.Tensor,
+              f32: bool = False) -> torch.Tensor:
+    rel = (v.abs() + 16) * 2 * U
+    if name == "gelu":
+        rel = rel + v.square() * 2 * U + (0.0 if f32 else 2.0 ** -19)
+    return 1.13 * err + rel * a.abs() + 2.0 ** -119
 
 
 def product64(x, w, bias=None, f32=False):
@@ -45,14 +51,14 @@ def product64(x, w, bias=None, f32=False):
     if bias is not None:
         b = bias.cpu().double()
         p, mag = p + b, mag + b.abs()
-    return p, ((512 + k / 256 + 16) if f32 else 2 * (k + 8)) * U * mag
+    return p, ((1024 + k / 512 + 16) if f32 else 2 * (k + 8)) * U * mag
 
 
 def linear64(x, w, bias=None, res=None, act="none", f32=False):
     """The formula, and the bound on the fp32 value's error before its last rounding."""
     p, err = product64(x, w, bias, f32)
     a = act64(act, p)
-    err = act_error(a, p, err) if act != "none" else err
+    err = act_error(act, a, p, err, f32) if act != "none" else err
     if res is not None:
         r = res.cpu().double()
         a, err = a + r, err + 2 * U * (a.abs() + r.abs())
@@ -63,7 +69,7 @@ def glu64(x, w13, bias=None, act="silu"):
     p, err = product64(x, w13, bias)
     (g, u), (dg, du) = p.chunk(2, -1), err.chunk(2, -1)
     a = act64(act, g)
-    da = act_error(a, g, dg)
+    da = act_error(act, a, g, dg)
     return a * u, da * (u.abs() + du) + a.abs() * du + 2 * U * (a * u).abs()
 
 

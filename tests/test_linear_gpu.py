@@ -37,7 +37,8 @@ def linear(x, w, bias=None, res=None, act="none", f32=False, y=None, **kw):
 SIZES = [(1, 1, 8), (1, 128, 64), (2, 3, 16), (3, 129, 72), (15, 127, 120), (16, 256, 256),
          (17, 100, 40), (31, 384, 4096), (33, 260, 1000), (64, 130, 512), (65, 640, 136),
          (127, 66, 264), (128, 128, 1024), (129, 500, 2056), (200, 1028, 328), (255, 256, 64),
-         (257, 384, 192), (300, 1000, 520), (513, 258, 1288)]
+         (257, 384, 192), (300, 1000, 520), (513, 258, 1288), (260, 33, 8), (1024, 512, 128),
+         (1500, 771, 456), (259, 2570, 3200)]
 
 
 @pytest.mark.parametrize("rows,n,k", SIZES)

@@ -40,7 +40,8 @@ def draw(rows, E, seed, coarse=False):
 @pytest.mark.parametrize("rows,E,R", [(1, 1, 1), (1, 8, 8), (5, 2, 1), (7, 33, 3), (9, 60, 4),
                                       (33, 64, 6), (130, 128, 8), (17, 129, 32), (65, 160, 6),
                                       (50, 256, 8), (3, 257, 7), (20, 384, 8), (31, 511, 9),
-                                      (12, 1000, 32), (40, 1024, 32)])
+                                      (12, 1000, 32), (40, 1024, 32), (66, 32, 1), (31, 36, 8),
+                                      (70, 252, 5), (45, 388, 8), (13, 512, 8), (6, 500, 2)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("coarse", [False, True])
 def test_matches_definition(rows, E, R, score, coarse):
@@ -53,7 +54,9 @@ def test_matches_definition(rows, E, R, score, coarse):
 
 @pytest.mark.parametrize("E,groups,kept,R", [(64, 2, 1, 6), (60, 3, 2, 7), (256, 8, 4, 8),
                                              (256, 32, 5, 8), (160, 8, 3, 6), (1024, 16, 4, 32),
-                                             (66, 11, 4, 9), (300, 4, 4, 5), (64, 32, 3, 6)])
+                                             (66, 11, 4, 9), (300, 4, 4, 5), (64, 32, 3, 6),
+                                             (384, 4, 2, 8), (512, 16, 5, 7), (384, 12, 4, 3),
+                                             (128, 2, 1, 8), (448, 7, 3, 5), (512, 2, 1, 1)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("best", [1, 2])
 def test_runs_of_experts(E, groups, kept, R, score, best):
@@ -87,6 +90,30 @@ def test_values_that_fp32_cannot_tell_apart(score):
                dict(groups=16, kept=2, best=2)):
         check(l, 8, score=score, bias=bias, **kw)
     check(l, 8, score=score, groups=8, kept=3, best=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_values_a_little_apart(score):
+    """Neighbours 2^-20 to 2^-50 apart: below fp32's step, above and below that of the
+    fixed point; large biases, which that does not hold; long batches' way as well."""
+    gen = torch.Generator().manual_seed(7)
+    E, rows = 256, 60
+    l = torch.randn((rows, E), generator=gen)
+    bias = torch.zeros(E)
+    for e in range(0, E, 2):  # twins whose logits differ by a few steps
+        step = 2.0 ** -torch.randint(20, 25, (rows,), generator=gen)
+        l[:, e + 1] = l[:, e] + torch.randint(-2, 3, (rows,), generator=gen) * step
+    for b in (bias, bias + 0.25, bias + 2.0 ** -30 * torch.randn(E, generator=gen), bias + 1e5,
+              bias - 40000.0, 1e3 * torch.randn(E, generator=gen)):
+        for kw in (dict(), dict(groups=8, kept=4, best=2), dict(groups=8, kept=4, best=1)):
+            check(l, 8, score=score, bias=b, **kw)
+    check(l, 8, score=score, groups=8, kept=4, best=2)
+    many = l.repeat(100, 1)  # the way of long batches: the same answers
+    for b in (None, bias + 0.25):
+        few = choose(l, 8, score=score, bias=b, groups=8, kept=4, best=2)
+        long = choose(many, 8, score=score, bias=b, groups=8, kept=4, best=2)
+        for a, c in zip(few, long):
+            assert torch.equal(a.repeat(100, 1), c)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -145,14 +172,14 @@ def test_large_logits():
 
 
 def test_many_tokens_ranks_streams_and_graphs():
-    l, bias = draw(4000, 256, 8)
+    l, bias = draw(4003, 256, 8)
     kw = dict(score="sigmoid", bias=bias, groups=8, kept=4, best=2, scale=2.5)
     idx, w = check(l, 8, **kw)
-    i2, w2 = choose(l, 8, N=4, **kw)
-    assert torch.equal(idx, i2) and torch.equal(w, w2)
+    i2, w2 = choose(l[:4000], 8, N=4, **kw)
+    assert torch.equal(idx[:4000], i2) and torch.equal(w[:4000], w2)
     dl, db = l.cuda(), bias.cuda()
     gi, gw = torch.zeros_like(idx).cuda(), torch.zeros_like(w).cuda()
-    sh, g = m.make_shape(1, 4000, 256, 8, 128), torch.cuda.CUDAGraph()
+    sh, g = m.make_shape(1, 4003, 256, 8, 128), torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         m.moe_topk(sh, dl, gi, gw, **{**kw, "bias": db})
     g.replay()
