@@ -1,7 +1,5 @@
 // linear.cu -- moe_linear and moe_linear_glu: products of bf16 rows and weights with
 // their epilogue.
-#include <cooperative_groups.h>
-
 #include "act.cuh"
 #include "bf16.cuh"
 #include "check.h"
@@ -13,162 +11,101 @@
 
 namespace moe {
 
-namespace cg = cooperative_groups;
-
-// The weights are the 128-row operand of the tensor cores and NR rows of x the other:
-// a lane of tensor memory is an output.  A CTA has 128 outputs (of both halves) of NR
-// rows; a warp brings blocks of 64 along k by TMA into a ring, one issues their
-// products, four take the sums out.  The CTAs of a cluster share k and then the rows:
-// each adds up and stores its own of them.
+// Few rows.  The weights are the 128-row operand of the tensor cores and NR rows of x
+// the other: a lane of tensor memory is an output.  A CTA has 128 outputs, or 64 of the
+// gate and the same 64 of the up projection, of NR rows; a warp brings
+// pairs of blocks of 64 along k by TMA into a ring, one issues their products, four take
+// the sums out.  (A stage costs the warps that load and issue about 300 cycles, whatever
+// it holds: with a block a stage a CTA took no more than 108 GB/s.)  The
+// CTAs of a cluster share k and then the rows: each sends its sums of a row to the part
+// that adds them up and stores the row.
 constexpr int kLinTma = 4, kLinMma = 5, kLinWarps = 6, kLinThreads = 32 * kLinWarps;
-constexpr int kLinTile = 128 * 128;  // bytes of a weight tile of a stage
-#ifndef F32RUN
-#define F32RUN 8
-#endif
-constexpr int kLinRun = F32RUN;           // blocks of k between the sums of an fp32 result
+constexpr int kLinTile = 128 * 128;  // bytes of a weight tile of a block of k
+constexpr int kLinRun = 4;           // stages between the sums of an fp32 result: 512 of k
+constexpr int kLinMostStages = 6;
+constexpr int kAtOnce = 4;           // rows that a warp finishes together
 
-__host__ __device__ constexpr int lin_stage(int NR, bool pair) {
-    return (pair ? 2 : 1) * kLinTile + NR * 128;
-}
-// two CTAs an SM up to 64 rows
-__host__ __device__ constexpr int lin_stages(int NR, bool pair) {
-    return (NR <= 64 ? 111 * 1024 : 220 * 1024) / lin_stage(NR, pair);
-}
-template <int kStages>
-struct alignas(16) LinShared {
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+struct LinShared {
+    uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
-    int stop;
+    int stop, any;  // this part gave up; some part did
 };
-template <int NR, bool kPair>
-constexpr size_t lin_smem() {
-    return 1024 + (size_t)lin_stages(NR, kPair) * lin_stage(NR, kPair) +
-           sizeof(LinShared<lin_stages(NR, kPair)>);
+constexpr int kLinHead = 256;  // bytes: LinShared, before the ring
+static_assert(sizeof(LinShared) <= kLinHead, "");
+
+// two blocks of weights, then two of rows
+__host__ __device__ constexpr int lin_stage(int NR) { return 2 * (kLinTile + NR * 128); }
+// Up to so many rows the parts' sums have room of their own; with more they go where the
+// ring was, once all parts are done with theirs.
+__host__ __device__ constexpr int lin_apart(int NR) { return NR <= 32 ? NR * 512 : 0; }
+__host__ __device__ constexpr int lin_smem(int NR, int stages) {
+    return kLinHead + 1024 + lin_apart(NR) + stages * lin_stage(NR);
 }
 
-// The outputs of a CTA's rows from their sums, which lie in shared memory as
-// [half][row][128 outputs] of each part: added in the parts' order.  A lane has eight
-// outputs of kAtOnce rows, 16 lanes a row.
-constexpr int kAtOnce = 4;
+// kOuts outputs c .. of a row, or as many as there are, from their sums (b: the up
+// projection's).
+template <bool kPair, bool kF32, int kOuts>
+__device__ __forceinline__ void store_outs(const Linear &p, size_t row, int c, const float *a) {
+    const size_t to = row * p.n + c;
+    if (p.n % kOuts == 0) {
+        if constexpr (kF32)
+            *reinterpret_cast<float4 *>(p.yf + to) = make_float4(a[0], a[1], a[2], a[3]);
+        else if constexpr (kPair)
+            *reinterpret_cast<uint32_t *>(p.y + to) = pack_bf16x2(a[0], a[1]);
+        else
+            *reinterpret_cast<uint2 *>(p.y + to) =
+                make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kOuts; ++i) {
+        if (c + i >= p.n) break;
+        if (kF32)
+            p.yf[to + i] = a[i];
+        else
+            p.y[to + i] = (uint16_t)pack_bf16x2(a[i], 0.0f);
+    }
+}
+
+// kOuts bf16 values from `at`, of which those before `end` are there.
+template <int kOuts>
+__device__ __forceinline__ void load_outs(const uint16_t *from, int c, int n, float (&v)[kOuts]) {
+    if (n % kOuts == 0) {
+        if (c >= n) return;
+        const uint32_t lo = *reinterpret_cast<const uint32_t *>(from);
+        v[0] = bf16_lo(lo), v[1] = bf16_hi(lo);
+        if constexpr (kOuts == 4) {
+            const uint32_t hi = *reinterpret_cast<const uint32_t *>(from + 2);
+            v[2] = bf16_lo(hi), v[3] = bf16_hi(hi);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kOuts; ++i)
+        if (c + i < n) v[i] = bf16_lo(from[i]);
+}
 
 template <int NR, bool kPair, bool kF32>
-struct Finish {
-    const Linear &p;
-    uint32_t sums;  // shared-memory address
-    int parts, row0, m, c0;
-
-    __device__ __forceinline__ uint32_t at(int q, int h, int j, int o) const {
-        uint32_t a;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;"
-            : "=r"(a)
-            : "r"(sums + ((h * NR + j) * 128 + o) * 4), "r"(q));
-        return a;
-    }
-
-    // n is a multiple of 8; rows j, j + step, ...
-    __device__ __forceinline__ void vectors(int j, int step, const uint4 (&bias)[2],
-                                            const uint4 (&res)[kAtOnce]) const {
-        const int o = (threadIdx.x & 15) * 8, c = c0 + o;
-        float a[8 * kAtOnce] = {}, b[kPair ? 8 * kAtOnce : 8] = {};
-#pragma unroll 1
-        for (int q = 0; q < parts; ++q)
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                const int r = min(j + i * step, m - 1);
-#pragma unroll
-                for (int h = 0; h < (kPair ? 4 : 2); ++h) {
-                    const float4 f = ld_dsmem4(at(q, h >> 1, r, o + (h & 1) * 4));
-                    float *to = (h >> 1 ? b : a) + 8 * i + (h & 1) * 4;
-                    to[0] += f.x, to[1] += f.y, to[2] += f.z, to[3] += f.w;
-                }
-            }
-        float w[8];
-        if (p.bias) {
-            unpack8(w, bias[0]);
-#pragma unroll
-            for (int i = 0; i < 8 * kAtOnce; ++i) a[i] += w[i & 7];
-        }
-        activate<kF32>(p.act, a);
-        if (kPair) {
-            if (p.bias) {
-                unpack8(w, bias[1]);
-#pragma unroll
-                for (int i = 0; i < 8 * kAtOnce; ++i) b[kPair ? i : 0] += w[i & 7];
-            }
-#pragma unroll
-            for (int i = 0; i < 8 * kAtOnce; ++i) a[i] *= b[kPair ? i : 0];
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int r = j + i * step;
-            if (r >= m || c >= p.n) continue;
-            float *v = a + 8 * i;
-            if (!kPair && p.res) {
-                unpack8(w, res[i]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += w[e];
-            }
-            const size_t to = (size_t)(row0 + r) * p.n + c;
-            if (kF32) {
-                *reinterpret_cast<float4 *>(p.yf + to) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4 *>(p.yf + to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                *reinterpret_cast<uint4 *>(p.y + to) =
-                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-            }
-        }
-    }
-
-    // any n: one output of row j a lane at a time
-    __device__ __forceinline__ void scalars(int j) const {
-        const int lane = threadIdx.x & 31;
-#pragma unroll 1
-        for (int o = lane; o < 128 && c0 + o < p.n; o += 32) {
-            const int c = c0 + o;
-            float a[1] = {0.0f}, b = 0.0f;
-            for (int q = 0; q < parts; ++q) {
-                a[0] += ld_dsmemf(at(q, 0, j, o));
-                if (kPair) b += ld_dsmemf(at(q, 1, j, o));
-            }
-            if (p.bias) {
-                a[0] += bf16_lo(__ldg(p.bias + c));
-                if (kPair) b += bf16_lo(__ldg(p.bias + p.n + c));
-            }
-            activate<kF32>(p.act, a);
-            if (kPair) a[0] *= b;
-            const size_t to = (size_t)(row0 + j) * p.n + c;
-            if (!kPair && p.res) a[0] += bf16_lo(p.res[to]);
-            if (kF32)
-                p.yf[to] = a[0];
-            else
-                p.y[to] = (uint16_t)pack_bf16x2(a[0], 0.0f);
-        }
-    }
-};
-
-template <int NR, bool kPair, bool kF32>
-__global__ void __launch_bounds__(kLinThreads, NR <= 64 ? 2 : 1)
-    k_linear(const __grid_constant__ Linear p, const __grid_constant__ CUtensorMap map_x,
+__global__ void __launch_bounds__(kLinThreads, 1)
+    k_linear(const __grid_constant__ Linear p, int stages, const __grid_constant__ CUtensorMap map_x,
              const __grid_constant__ CUtensorMap map_w) {
-    constexpr int kStages = lin_stages(NR, kPair), kBytes = lin_stage(NR, kPair);
-    constexpr int kHalves = kPair ? 2 : 1;
+    constexpr int kBytes = lin_stage(NR), kOuts = kPair ? 2 : 4;
     constexpr int kAccs = kF32 ? 2 : 1;  // accumulators
-    constexpr int kUsed = kAccs * kHalves * NR, kCols = kUsed < 32 ? 32 : kUsed;
-    static_assert(kHalves * NR * 512 <= kStages * kBytes, "the sums go through the ring");
-    using Shared = LinShared<kStages>;
+    constexpr int kUsed = kAccs * NR, kCols = kUsed < 32 ? 32 : kUsed;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = smem_raw + align1024(smem_raw);
-    Shared &s = *reinterpret_cast<Shared *>(ring + kStages * kBytes);
+    LinShared &s = *reinterpret_cast<LinShared *>(smem_raw);
+    uint8_t *ring = smem_raw + kLinHead + align1024(smem_raw + kLinHead);
+    // sums [part][row / parts][128] of the rows that are this part's
+    float *left = reinterpret_cast<float *>(lin_apart(NR) ? ring + stages * kBytes : ring);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int c0 = blockIdx.y * 128, row0 = blockIdx.x * NR, m = min(NR, p.rows - row0);
-    cg::cluster_group cluster = cg::this_cluster();
-    const int parts = (int)gridDim.z, part = (int)blockIdx.z;
-    const int Kb = (p.k + kLinearBlock - 1) / kLinearBlock;
+    const int c0 = blockIdx.y * (kPair ? 64 : 128), row0 = blockIdx.x * NR;
+    const int m = min(NR, p.rows - row0);
+    const int parts = (int)gridDim.z, part = (int)blockIdx.z, shift = __ffs(parts) - 1;
+    const int Kb = (p.k + 2 * kLinearBlock - 1) / (2 * kLinearBlock);  // stages of k
     const int b0 = (int)((long long)Kb * part / parts), b1 = (int)((long long)Kb * (part + 1) / parts);
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < stages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
         }
@@ -177,102 +114,118 @@ __global__ void __launch_bounds__(kLinThreads, NR <= 64 ? 2 : 1)
             mbar_init(&s.tempty[i], 4);
         }
         mbar_init(&s.drain, 1);
-        s.stop = 0;
+        s.stop = s.any = 0;
         fence_mbar_init();
         tma_prefetch_map(&map_x);
         tma_prefetch_map(&map_w);
     }
     if (warp == kLinMma) tc_alloc<kCols>(&s.tmem);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (parts > 1) cluster_arrive();  // this part is there: others may write to it
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = s.tmem;
     volatile int *stop = &s.stop;
-    float *left = reinterpret_cast<float *>(ring);  // [half][row][128], once the ring is done
     int issued = 0;  // blocks whose loads are under way (TMA warp)
+    float acc[kF32 ? NR : 1] = {};
 
     if (warp == kLinTma) {
         const uint32_t one = elect_one();
+        int st = 0, phase = 1;
         for (int b = b0; b < b1; ++b, ++issued) {
-            const int st = issued % kStages;
-            if (issued >= kStages && !wait_or_stop(&s.empty[st], (issued / kStages - 1) & 1, stop))
-                break;
-            if (!one) continue;
-            uint8_t *w = ring + st * kBytes;
-            mbar_arrive_expect_tx(&s.full[st], kBytes);
-            tma_tile(w, &map_w, b * 128, c0, &s.full[st]);
-            if (kPair) tma_tile(w + kLinTile, &map_w, b * 128, p.n + c0, &s.full[st]);
-            tma_tile(w + kHalves * kLinTile, &map_x, b * 128, row0, &s.full[st]);
+            if (issued >= stages && !wait_or_stop(&s.empty[st], phase, stop)) break;
+            if (one) {
+                uint8_t *w = ring + st * kBytes;
+                mbar_arrive_expect_tx(&s.full[st], kBytes);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // a block behind k's end is zeros
+                    const int at = (2 * b + i) * 128;
+                    tma_tile(w + i * kLinTile, &map_w, at, c0, &s.full[st]);
+                    if (kPair)
+                        tma_tile(w + i * kLinTile + kLinTile / 2, &map_w, at, p.n + c0, &s.full[st]);
+                    tma_tile(w + 2 * kLinTile + i * NR * 128, &map_x, at, row0, &s.full[st]);
+                }
+            }
+            if (++st == stages) st = 0, phase ^= 1;
         }
     } else if (warp == kLinMma) {
         const uint32_t one = elect_one(), idesc = tc_bf16_f32(128, NR);
+        int st = 0, phase = 0;
         for (int it = 0; it < b1 - b0; ++it) {
-            const int st = it % kStages;
             const int run = kF32 ? it / kLinRun : 0, ac = run & 1;
             const bool first = kF32 ? it % kLinRun == 0 : it == 0;
             const bool last = it == b1 - b0 - 1 || (kF32 && it % kLinRun == kLinRun - 1);
             if (first && run >= 2 && !wait_or_stop(&s.tempty[ac], (run / 2 - 1) & 1, stop)) break;
-            if (!wait_or_stop(&s.full[st], (it / kStages) & 1, stop)) break;
+            if (!wait_or_stop(&s.full[st], phase, stop)) break;
             tc_fence_after();
             const uint64_t w = tc_operand(ring + st * kBytes);
-            const uint64_t x = tc_operand(ring + st * kBytes + kHalves * kLinTile);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 32 bytes along k: 2 address units
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h)
-                    tc_mma_bf16(tmem + (ac * kHalves + h) * NR, w + h * (kLinTile >> 4) + kk * 2,
-                                x + kk * 2, idesc, !first || kk > 0, one);
+            const uint64_t x = tc_operand(ring + st * kBytes + 2 * kLinTile);
+            tc_mma_bf16x64(tmem + ac * NR, w, x, idesc, !first, one);
+            tc_mma_bf16x64(tmem + ac * NR, w + (kLinTile >> 4), x + (NR * 128 >> 4), idesc, true, one);
             tc_commit(&s.empty[st], one);
             if (last) tc_commit(&s.tfull[ac], one);
+            if (++st == stages) st = 0, phase ^= 1;
         }
-    } else {
+    } else if constexpr (kF32) {
         const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
-        if constexpr (kF32) {
-            float acc[NR] = {};
-            const int runs = (b1 - b0 + kLinRun - 1) / kLinRun;
-            bool ok = true;
-            for (int run = 0; ok && run < runs; ++run) {
-                const int ac = run & 1;
-                ok = __all_sync(kFull, wait_or_stop(&s.tfull[ac], (run / 2) & 1, stop));
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < NR; j += 16) {
-                    uint32_t v[16];
-                    tc_ld16(v, mine + ac * NR + j);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[j + i] += __uint_as_float(v[i]);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.tempty[ac]);
-            }
-            // the last products are done: the ring is free
-#pragma unroll
-            for (int j = 0; j < NR; ++j)
-                if (j < m) left[j * 128 + tid] = acc[j];
-        } else if (__all_sync(kFull, wait_or_stop(&s.tfull[0], 0, stop))) {
+        const int runs = (b1 - b0 + kLinRun - 1) / kLinRun;
+        for (int run = 0; run < runs; ++run) {
+            const int ac = run & 1;
+            if (!__all_sync(kFull, wait_or_stop(&s.tfull[ac], (run / 2) & 1, stop))) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int j = 0; j < kHalves * NR; j += 16) {
+#pragma unroll
+            for (int j = 0; j < NR; j += 16) {
                 uint32_t v[16];
-                tc_ld16(v, mine + j);
+                tc_ld16(v, mine + ac * NR + j);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) left[(j + i) * 128 + tid] = __uint_as_float(v[i]);
+                for (int i = 0; i < 16; ++i) acc[j + i] += __uint_as_float(v[i]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.tempty[ac]);
+        }
+    } else {
+        wait_or_stop(&s.tfull[0], 0, stop);
+    }
+
+    // ---------------------------------------------------------------- the sums to their rows' parts
+    // what the outputs take beside their sums is asked for before those are there
+    const int c = c0 + lane * kOuts;
+    float bias[kOuts] = {}, bias2[kOuts] = {}, res[kAtOnce][kOuts] = {};
+    if (p.bias) {
+        load_outs(p.bias + c, c, p.n, bias);
+        if (kPair) {
+            if (p.n % kOuts == 0) {
+                load_outs(p.bias + p.n + c, c, p.n, bias2);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kOuts; ++i)
+                    if (c + i < p.n) bias2[i] = bf16_lo(p.bias[p.n + c + i]);
             }
         }
     }
-
+    const int LR = NR >> shift, mine0 = part * LR;  // rows of a part; this one's first
+    const int mm = min(m - mine0, LR);              // as many as there are
+    // of this part's rows r, r + kLinWarps, ...
+    const auto residual = [&](int r) {
+        if (!kPair && p.res)
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int j = r + i * kLinWarps;
+                if (j < mm)
+                    load_outs(p.res + (size_t)(row0 + mine0 + j) * p.n + c, c, p.n, res[i]);
+            }
+    };
+    residual(warp);
     tc_fence_before();
     __syncthreads();
     if (s.stop) {  // a kernel that gave up leaves no copy and no product in flight
         if (warp == kLinTma && lane == 0)
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                mbar_wait(&s.full[i % kStages], (i / kStages) & 1);
+            for (int i = max(0, issued - stages); i < issued; ++i)
+                mbar_wait(&s.full[i % stages], (i / stages) & 1);
         if (warp == kLinMma) {
             tc_commit(&s.drain, elect_one());
             mbar_wait(&s.drain, 0);
@@ -281,45 +234,92 @@ __global__ void __launch_bounds__(kLinThreads, NR <= 64 ? 2 : 1)
         __syncthreads();
     }
     tc_fence_after();
-    if (warp == kLinMma) tc_free<kCols>(tmem);
-    // what the outputs take beside their sums, asked for before those are there
-    const int step = 2 * parts * kLinWarps, c = c0 + (lane & 15) * 8;
-    int j = (part * kLinWarps + warp) * 2 + (lane >> 4);
-    const bool whole = (p.n & 7) == 0, in = whole && c < p.n;
-    uint4 bias[2] = {}, res[kAtOnce] = {};
-    if (in && p.bias) {
-        bias[0] = __ldg(reinterpret_cast<const uint4 *>(p.bias + c));
-        if (kPair) bias[1] = __ldg(reinterpret_cast<const uint4 *>(p.bias + p.n + c));
+    if (parts > 1) {
+        cluster_wait();
+        if (!lin_apart(NR)) cluster_sync();  // all parts are done with their rings
+        if (s.stop && tid < parts) st_dsmem(dsmem_addr(&s.any, tid), 1);
     }
-    const auto residual = [&]() {
-        if (!kPair && in && p.res)
+    if (warp < 4 && !s.stop) {
+        const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
+        // rows j0 .. j0 + 15, of LR or more parts each: their addresses in the cluster
+        const auto leave = [&](int j0, const uint32_t (&v)[16]) {
+            uint32_t to = 0;
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-                if (j + i * step < m)
-                    res[i] = *reinterpret_cast<const uint4 *>(
-                        p.res + (size_t)(row0 + j + i * step) * p.n + c);
-    };
-    residual();
-    // where a part gave up the sums are not whole and no part stores any
-    if (parts > 1) cluster.sync();
-    const int any = ld_dsmem(dsmem_addr(&s.stop, min(lane, parts - 1)));
-    if (!__any_sync(kFull, any)) {
-        const Finish<NR, kPair, kF32> f = {p, smem_addr(left), parts, row0, m, c0};
-        if (whole) {
-#pragma unroll 1
-            for (; j < m; j += kAtOnce * step) {
-                f.vectors(j, step, bias, res);
-                if (j + kAtOnce * step < m) {
-                    j += kAtOnce * step;
-                    residual();
-                    j -= kAtOnce * step;
+            for (int i = 0; i < 16; ++i) {
+                if (j0 + i >= m) return;
+                if (i == 0 || ((j0 + i) & (LR - 1)) == 0) {
+                    const int owner = (j0 + i) / LR, r = (j0 + i) & (LR - 1);
+                    float *at = left + (part * LR + r) * 128 + tid;
+                    to = (parts > 1 ? dsmem_addr(at, owner) : smem_addr(at)) - i * 512;
                 }
+                st_dsmem(to + i * 512, v[i]);
+            }
+        };
+        if constexpr (kF32) {
+#pragma unroll
+            for (int j = 0; j < NR; j += 16) {
+                uint32_t v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[kF32 ? j + i : 0]);
+                leave(j, v);
             }
         } else {
-            for (int r = part * kLinWarps + warp; r < m; r += parts * kLinWarps) f.scalars(r);
+#pragma unroll 1
+            for (int j = 0; j < m; j += 16) {
+                uint32_t v[16];
+                tc_ld16(v, mine + j);
+                tc_wait_ld();
+                leave(j, v);
+            }
         }
     }
-    if (parts > 1) cluster.sync();  // no part goes while it is read
+    tc_fence_before();
+    if (parts > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    tc_fence_after();
+    if (warp == kLinMma) tc_free<kCols>(tmem);
+
+    // ---------------------------------------------------------------- the outputs
+    // where a part gave up the sums are not whole and no part stores any
+    if (s.any || s.stop) return;
+#pragma unroll 1
+    for (int r = warp; r < mm; r += kAtOnce * kLinWarps) {
+        float a[kAtOnce * kOuts] = {}, b[kPair ? kAtOnce * kOuts : 1] = {};
+        for (int q = 0; q < parts; ++q)  // in the parts' order
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int rr = min(r + i * kLinWarps, LR - 1);
+                const float *at = left + (q * LR + rr) * 128 + lane * kOuts;
+                if constexpr (kPair) {
+                    const float2 g = *reinterpret_cast<const float2 *>(at);
+                    const float2 u = *reinterpret_cast<const float2 *>(at + 64);
+                    a[i * 2] += g.x, a[i * 2 + 1] += g.y;
+                    b[i * 2] += u.x, b[i * 2 + 1] += u.y;
+                } else {
+                    const float4 f = *reinterpret_cast<const float4 *>(at);
+                    a[i * 4] += f.x, a[i * 4 + 1] += f.y, a[i * 4 + 2] += f.z, a[i * 4 + 3] += f.w;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < kAtOnce * kOuts; ++i) a[i] += bias[i % kOuts];
+        activate<kF32>(p.act, a);
+        if (kPair)
+#pragma unroll
+            for (int i = 0; i < kAtOnce * kOuts; ++i)
+                a[i] *= b[kPair ? i : 0] + bias2[i % kOuts];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int j = r + i * kLinWarps;
+            if (j >= mm || c >= p.n) continue;
+            if (!kPair)
+#pragma unroll
+                for (int o = 0; o < kOuts; ++o) a[i * kOuts + o] += res[i][o];
+            store_outs<kPair, kF32, kOuts>(p, (size_t)row0 + mine0 + j, c, a + i * kOuts);
+        }
+        residual(r + kAtOnce * kLinWarps);
+    }
 }
 
 // ------------------------------------------------------------ host
@@ -327,17 +327,16 @@ __global__ void __launch_bounds__(kLinThreads, NR <= 64 ? 2 : 1)
 template <int NR, bool kPair, bool kF32>
 static cudaError_t launch_few(const Linear &p, const LinearPlan &plan, cudaStream_t st) {
     const auto kern = k_linear<NR, kPair, kF32>;
-    constexpr size_t kSmem = lin_smem<NR, kPair>();
-    static_assert(kSmem <= (NR <= 64 ? 113 * 1024 : 232448), "CTAs of an SM");
     CUtensorMap map_x, map_w;
     cudaError_t err = tile_map(&map_x, p.x, p.rows, 2 * p.k, NR);
-    if (err == cudaSuccess) err = tile_map(&map_w, p.w, (int64_t)(kPair ? 2 : 1) * p.n, 2 * p.k, 128);
+    if (err == cudaSuccess)
+        err = tile_map(&map_w, p.w, (int64_t)(kPair ? 2 : 1) * p.n, 2 * p.k, kPair ? 64 : 128);
     if (err != cudaSuccess) return err;
     static LaunchMemo memo;
     int done = 0;
     err = memo.get(0, &done, [&](int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -348,31 +347,23 @@ static cudaError_t launch_few(const Linear &p, const LinearPlan &plan, cudaStrea
     attr[1].val.clusterDim.x = 1;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = (unsigned)plan.parts;
-    cfg.gridDim = dim3((unsigned)((p.rows + NR - 1) / NR), (unsigned)((p.n + 127) / 128),
+    const int outs = kPair ? 64 : 128;
+    cfg.gridDim = dim3((unsigned)((p.rows + NR - 1) / NR), (unsigned)((p.n + outs - 1) / outs),
                        (unsigned)plan.parts);
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = (size_t)lin_smem(NR, plan.stages);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p, map_x, map_w);
+    return cudaLaunchKernelEx(&cfg, kern, p, plan.stages, map_x, map_w);
 }
 
 template <bool kPair, bool kF32>
 static cudaError_t launch_at(const Linear &p, const LinearPlan &plan, cudaStream_t st) {
     if (plan.at == 16) return launch_few<16, kPair, kF32>(p, plan, st);
     if (plan.at == 32) return launch_few<32, kPair, kF32>(p, plan, st);
-    if constexpr (kF32) {
-        return launch_few<64, kPair, kF32>(p, plan, st);
-    } else {
-        if (plan.at == 64) return launch_few<64, kPair, kF32>(p, plan, st);
-        if constexpr (kPair) {
-            return launch_few<128, kPair, kF32>(p, plan, st);
-        } else {
-            if (plan.at == 128) return launch_few<128, kPair, kF32>(p, plan, st);
-            return launch_few<256, kPair, kF32>(p, plan, st);
-        }
-    }
+    if (plan.at == 64) return launch_few<64, kPair, kF32>(p, plan, st);
+    return launch_few<128, kPair, kF32>(p, plan, st);
 }
 
 cudaError_t launch_linear(const Linear &p, bool pair, cudaStream_t st) {

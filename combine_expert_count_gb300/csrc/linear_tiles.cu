@@ -18,25 +18,19 @@ namespace moe {
 
 constexpr int kPairRows = 256;               // of a tile, half of them each CTA's
 constexpr int kOpBytes = 128 * 128;          // 128 rows of a block along k
-#ifndef PSTAGES
-#define PSTAGES 5
-#endif
-constexpr int kPairStages = PSTAGES, kPairStageBytes = 2 * kOpBytes;
+constexpr int kPairStages = 5, kPairStageBytes = 2 * kOpBytes;
 constexpr int kOutWarps = 8, kPairTma = 8, kPairMma = 9, kPairWarps = 10;
 constexpr int kPairThreads = 32 * kPairWarps;
 constexpr int kOutStage = 32 * 128;          // a storing warp's staging
 constexpr int kResStage = 2 * 32 * 64;       // and its residual's, two chunks
-#ifndef F32RUN
-#define F32RUN 8
-#endif
-constexpr int kF32Run = F32RUN;                   // blocks of k between the sums of an fp32 result
+constexpr int kF32Run = 8;                   // blocks of k between the sums of an fp32 result
 
 constexpr int kF32Width = 128;               // of its tiles at most: the sums stay in registers
 
 struct alignas(16) PairShared {
     uint64_t full[kPairStages], empty[kPairStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
-    int stop;
+    int stop, any;  // this CTA gave up; one of the cluster's did
 };
 constexpr size_t kPairSmem =
     1024 + (size_t)kPairStages * kPairStageBytes + kOutWarps * (kOutStage + kResStage) + sizeof(PairShared);
@@ -44,10 +38,7 @@ static_assert(kPairSmem <= 232448, "a CTA's shared memory");
 
 // Row tiles whose columns are gone through together, so that the pairs at work at one
 // time share rows and weights in L2.
-#ifndef KPAIRRUN
-#define KPAIRRUN 8
-#endif
-constexpr int kPairRun = KPAIRRUN;
+constexpr int kPairRun = 8;
 
 struct PairTile {
     int row0, c0;  // first row of the pair, first output
@@ -105,11 +96,12 @@ struct Beside {
 
 // Finishes and stores the chunk of outputs c .. of the warp's rows row0 .., rows and
 // outputs (below end) as far as there are any.
-// The sums are those of `parts` CTAs, in the same place of their shared memory.
+// kSplit: the sums are those of `parts` parts, `pitch` bytes from one part's to the
+// next's.
 template <bool kPair, bool kF32, bool kSplit>
 __device__ __forceinline__ void finish(const Linear &p, uint8_t *stage, const Beside<kPair> &by,
                                        size_t row0, int rows, int c, int end, int chunk, int parts,
-                                       int rank) {
+                                       int pitch) {
     constexpr int kOuts = chunk_outs(kPair), kLanes = kOuts / 8, kRows = 32 / kLanes;
     const int lane = threadIdx.x & 31;
     end = min(end, p.n);
@@ -121,16 +113,10 @@ __device__ __forceinline__ void finish(const Linear &p, uint8_t *stage, const Be
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint8_t *at = staged(stage, i * kRows + lane / kLanes, from + h);
-                if constexpr (!kSplit) {
-                    const float4 f = *reinterpret_cast<float4 *>(at);
-                    to[4 * h] = f.x, to[4 * h + 1] = f.y, to[4 * h + 2] = f.z, to[4 * h + 3] = f.w;
-                } else {
-#pragma unroll 1
-                    for (int q = 0; q < parts; ++q) {
-                        const float4 f = ld_dsmem4(dsmem_addr(at, 2 * q + rank));
-                        to[4 * h] += f.x, to[4 * h + 1] += f.y;
-                        to[4 * h + 2] += f.z, to[4 * h + 3] += f.w;
-                    }
+                for (int q = 0; q < (kSplit ? parts : 1); ++q) {
+                    const float4 f = *reinterpret_cast<float4 *>(at + q * pitch);
+                    to[4 * h] += f.x, to[4 * h + 1] += f.y;
+                    to[4 * h + 2] += f.z, to[4 * h + 3] += f.w;
                 }
             }
         };
@@ -185,7 +171,7 @@ __device__ __forceinline__ void finish(const Linear &p, uint8_t *stage, const Be
             uint8_t *place = staged(stage, r, from >> 2) + (from & 3) * 4;
             if (!kSplit) return *reinterpret_cast<float *>(place);
             float sum = 0.0f;
-            for (int q = 0; q < parts; ++q) sum += ld_dsmemf(dsmem_addr(place, 2 * q + rank));
+            for (int q = 0; q < parts; ++q) sum += *reinterpret_cast<float *>(place + q * pitch);
             return sum;
         };
         float a[1] = {get(o) + bias};
@@ -234,7 +220,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(&s.tempty[i], 2 * kOutWarps);
         }
         mbar_init(&s.drain, 1);
-        s.stop = 0;
+        s.stop = s.any = 0;
         fence_mbar_init();
         tma_prefetch_map(&map_x);
         tma_prefetch_map(&map_w);
@@ -249,6 +235,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = s.tmem;
     volatile int *stop = &s.stop;
     int issued = 0;
+    float acc[kAcc];  // fp32 results: the sums of a thread's row and half of the outputs
 
     if (warp == kPairTma) {
         const uint32_t one = elect_one();
@@ -295,10 +282,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     tc_fence_after();
                     const uint64_t x = tc_operand(ring + st * kPairStageBytes);
                     const uint64_t w = tc_operand(ring + st * kPairStageBytes + kOpBytes);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)  // 32 bytes along k: 2 address units
-                        tc_mma_bf16_pair(tmem + ac * 256, x + kk * 2, w + kk * 2, idesc,
-                                         !first || kk > 0, one);
+                    tc_mma_bf16x64_pair(tmem + ac * 256, x, w, idesc, !first, one);
                     tc_commit_pair(&s.empty[st], both, one);
                     if (last) {
                         tc_commit_pair(&s.tfull[ac], both, one);
@@ -314,8 +298,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t back[2] = {dsmem_addr(&s.tempty[0], lead), dsmem_addr(&s.tempty[1], lead)};
         uint8_t *stage = staging + warp * kOutStage;
         uint8_t *residual = staging + kOutWarps * kOutStage + warp * kResStage;
-        // kSplit: the sums stay in the ring, whose last products are done, until all are there
-        const auto place = [&](int c) { return kSplit ? ring + ((half * 4 + c / kOuts) * 4 + quad) * 4096 : stage; };
         bool ok = true;
         int run = 0;
 #pragma unroll 1
@@ -327,8 +309,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             Beside<kPair> by = {};
             by.res = residual;
             if (!kSplit) by.load(p, row0, rows, c0, end, 0);
-            float acc[kAcc] = {};
             if constexpr (kF32) {
+#pragma unroll
+                for (int i = 0; i < kAcc; ++i) acc[i] = 0.0f;
                 for (int b = kb0; b < kb1; b += kF32Run, ++run) {
                     const int ac = run & 1;
                     ok = __all_sync(kFull, wait_or_stop(&s.tfull[ac], (run / 2) & 1, stop));
@@ -351,10 +334,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 ok = __all_sync(kFull, wait_or_stop(&s.tfull[run & 1], (run / 2) & 1, stop));
                 tc_fence_after();
             }
-            if (!ok) break;
+            if (!ok || kSplit) break;
             const auto chunk = [&](int c) {
                 // where an accumulator ends within the 32, what is behind it is not stored
-                uint8_t *to = place(c);
                 uint32_t v[2][16];
                 if constexpr (!kF32) {
                     const uint32_t ac = mine + (run & 1) * 256 + c;
@@ -373,14 +355,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4 *>(staged(to, lane, j)) =
+                    *reinterpret_cast<uint4 *>(staged(stage, lane, j)) =
                         make_uint4(v[j / 4][4 * j % 16], v[j / 4][4 * j % 16 + 1],
                                    v[j / 4][4 * j % 16 + 2], v[j / 4][4 * j % 16 + 3]);
                 __syncwarp();
-                if (kSplit) return;
                 const Beside<kPair> now = by;
                 by.load(p, row0, rows, c0 + c + kOuts, end, c / kOuts + 1);
-                finish<kPair, kF32, false>(p, to, now, row0, rows, c0 + c, end, c / kOuts, 1, 0);
+                finish<kPair, kF32, false>(p, stage, now, row0, rows, c0 + c, end, c / kOuts, 1, 0);
             };
             if constexpr (kF32) {
 #pragma unroll
@@ -408,29 +389,68 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     cluster_sync();  // neither CTA goes while the other may read or signal it
     tc_fence_after();
-    if (warp == kPairMma) tc_free_pair<512>(tmem);
     if constexpr (kSplit) {
+        // All parts are done with their rings: a chunk's sums of 32 rows (unit u) go to
+        // the ring of the part that finishes them, with the other parts'.
+        const int cols = outs >> 1, most = (cols + kOuts - 1) / kOuts, units = 8 * most;
+        const int slots = (units / 8 + parts - 1) / parts * 8;  // units of a part
+        if (s.stop && tid < 2 * parts) st_dsmem(dsmem_addr(&s.any, tid), 1);
+        if (warp < kOutWarps && !s.stop) {
+            const int quad = warp & 3, half = warp >> 2;
+            const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + half * cols;
+            const auto give = [&](int ch, const uint32_t (&v)[32]) {
+                const int u = (half * most + ch) * 4 + quad, slot = u / 8 / parts * 8 + u % 8;
+                uint8_t *to = ring + (part * slots + slot) * 4096;
+                const int owner = 2 * (u / 8 % parts) + rank;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_dsmem4(dsmem_addr(staged(to, lane, j), owner), v[4 * j], v[4 * j + 1],
+                              v[4 * j + 2], v[4 * j + 3]);
+            };
+            uint32_t v[32];
+            if constexpr (kF32) {
+#pragma unroll
+                for (int ch = 0; ch < kAcc / 32; ++ch) {
+                    if (ch >= most) break;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[ch * 32 + i]);
+                    give(ch, v);
+                }
+            } else {
+#pragma unroll 1
+                for (int ch = 0; ch < most; ++ch) {
+                    uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(v);
+                    uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(v + 16);
+                    tc_ld16(lo, mine + ch * kOuts);
+                    tc_ld16(hi, mine + ch * kOuts + (kPair ? outs : 16));
+                    tc_wait_ld();
+                    give(ch, v);
+                }
+            }
+        }
+        tc_fence_before();
+        cluster_sync();
+        tc_fence_after();
         // where a part gave up the sums are not whole and no part stores any
-        const int any = ld_dsmem(dsmem_addr(&s.stop, min(lane, 2 * parts - 1)));
-        const PairTile tile = pair_tile(p, outs, tiles_m, tiles_n, blockIdx.x >> 1);
-        if (warp < kOutWarps && !__any_sync(kFull, any)) {
-            // 32 rows of a chunk each: (half, chunk, quad), as place() has them
-            const int cols = outs >> 1, most = (cols + kOuts - 1) / kOuts;
+        if (warp < kOutWarps && !s.any && !s.stop) {
+            const PairTile tile = pair_tile(p, outs, tiles_m, tiles_n, blockIdx.x >> 1);
             Beside<kPair> by = {};
             by.res = staging + kOutWarps * kOutStage + warp * kResStage;
-            for (int u = part * kOutWarps + warp; u < 2 * most * 4; u += parts * kOutWarps) {
+            for (int slot = warp; slot < slots; slot += 8) {
+                const int u = (slot / 8 * parts + part) * 8 + warp;
+                if (u >= units) break;
                 const int quad = u & 3, ch = (u >> 2) % most, half = (u >> 2) / most;
                 const size_t row0 = (size_t)tile.row0 + rank * 128 + quad * 32;
                 const int rows = (int)min((long long)32, (long long)p.rows - (long long)row0);
                 const int c0 = tile.c0 + half * cols, c = c0 + ch * kOuts;
                 by.load(p, row0, rows, c, c0 + cols, 0);
                 if (!kPair && p.res) asm volatile("cp.async.wait_group 0;" ::: "memory");
-                finish<kPair, kF32, true>(p, ring + ((half * 4 + ch) * 4 + quad) * 4096, by, row0,
-                                          rows, c, c0 + cols, 0, parts, rank);
+                finish<kPair, kF32, true>(p, ring + slot * 4096, by, row0, rows, c, c0 + cols, 0,
+                                          parts, slots * 4096);
             }
         }
-        cluster_sync();  // no part goes while it is read
     }
+    if (warp == kPairMma) tc_free_pair<512>(tmem);
 }
 
 template <bool kPair, bool kF32, bool kSplit>

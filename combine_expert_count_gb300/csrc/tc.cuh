@@ -18,9 +18,6 @@ __device__ __forceinline__ uint32_t align1024(const void *p) { return -smem_addr
 
 // Where this holds for a thread, its waits below run out at once: a library that
 // is compiled with it shows what a stopped kernel leaves.
-#ifndef SLEEPNS
-#define SLEEPNS 20000u
-#endif
 #ifndef MOE_GIVE_UP
 #define MOE_GIVE_UP false
 #endif
@@ -34,7 +31,7 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(SLEEPNS)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
         : "memory");
     return ok != 0;
 }
@@ -72,13 +69,6 @@ __device__ __forceinline__ void tma_tile(void *dst, const CUtensorMap *map, int 
         "[%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
         "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
-}
-
-// The tile to L2 alone: a load of it later finds it there.
-__device__ __forceinline__ void tma_prefetch_tile(const CUtensorMap *map, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map),
-                 "r"(x), "r"(y)
-                 : "memory");
 }
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
@@ -151,15 +141,24 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
-// The same over 16 elements of k of bf16 operands.
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate, uint32_t on) {
+// d (+)= a b^T over 64 elements of k of bf16 operands (four products of 16, their
+// operands 32 bytes, two address units, further each), issued where `on`; `more`: added
+// to what d holds.  One block of instructions: what goes with each product (predicates,
+// operands to uniform registers) is done once.
+__device__ __forceinline__ void tc_mma_bf16x64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               bool more, uint32_t on) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
         "setp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
+        "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\t"
+        "add.u64 a2, %1, 4;\n\tadd.u64 b2, %2, 4;\n\t"
+        "add.u64 a3, %1, 6;\n\tadd.u64 b3, %2, 6;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)more), "r"(on)
         : "memory");
 }
 
@@ -203,8 +202,15 @@ __device__ __forceinline__ void tc_free(uint32_t taddr) {
 // memory); that one issues products whose 256-row operand lies half in each CTA's
 // shared memory, by row, as does the other operand, and whose sums lie in each CTA's
 // tensor memory, its own rows'.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 template <int kCols>
@@ -236,14 +242,21 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
                  : "memory");
 }
 
-__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                                 bool accumulate, uint32_t on) {
+// As tc_mma_bf16x64.
+__device__ __forceinline__ void tc_mma_bf16x64_pair(uint32_t d, uint64_t a, uint64_t b,
+                                                    uint32_t idesc, bool more, uint32_t on) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
         "setp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(on)
+        "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\t"
+        "add.u64 a2, %1, 4;\n\tadd.u64 b2, %2, 4;\n\t"
+        "add.u64 a3, %1, 6;\n\tadd.u64 b3, %2, 6;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)more), "r"(on)
         : "memory");
 }
 
@@ -288,19 +301,16 @@ __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Four floats of a cluster's shared memory.
-__device__ __forceinline__ float4 ld_dsmem4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+// To an address of the cluster's shared memory.  Loads from there would each be waited
+// for (250 cycles); stores are under way together.
+__device__ __forceinline__ void st_dsmem(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ float ld_dsmemf(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_dsmem4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                          uint32_t d) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
 }
 
 // ------------------------------------------------------------ packed fp32
