@@ -520,15 +520,23 @@ def moe_layer_few(shape, inter: int, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2
     _check(rc, "moe_layer_few")
 
 
-def _on_device(t, nbytes: int, name: str, device: int):
-    """_ptr's address of a tensor on the current device, which the call's kernels run
-    on; no host memory."""
-    if t is not None:
-        if not t.is_cuda:
-            raise ValueError(f"{name}: must be a CUDA tensor")
-        if t.get_device() != device:
-            raise ValueError(f"{name}: on device {t.get_device()}, the current one is {device}")
+def _at(t, nbytes: int, name: str, device: int):
+    """The address of a tensor on the current device, which the call's kernels run on;
+    no host memory.  _ptr's checks in the fewest steps: a small call is bound by them."""
+    if (t is not None and t.get_device() == device and t.nbytes >= nbytes
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t is not None and not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t is not None and t.get_device() != device:
+        raise ValueError(f"{name}: on device {t.get_device()}, the current one is {device}")
     return _ptr(t, nbytes, name)
+
+
+def _stream_on(stream, device: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _named(names: dict, value, what: str) -> int:
@@ -544,15 +552,16 @@ def moe_linear(shape, n: int, k: int, x, w, y, bias=None, res=None, act: str = "
     weights [n][k]; ``y`` is bf16, or fp32 where its dtype is torch.float32."""
     sh, d = _as_shape(shape), torch._C._cuda_getDevice()
     rows, f32 = sh.N * sh.T, y is not None and y.dtype == torch.float32
-    py = _on_device(y, rows * n * (4 if f32 else 2), "y", d)
+    py = _at(y, rows * n * (4 if f32 else 2), "y", d)
     rc = (_lib or lib()).moe_linear(
         ctypes.byref(sh), n, k, _named(MOE_ACTS, act, "act"),
-        _on_device(x, rows * k * 2, "x", d), _on_device(w, n * k * 2, "w", d),
-        None if bias is None else _on_device(bias, 2 * n, "bias", d),
-        None if res is None else _on_device(res, rows * n * 2, "res", d),
+        _at(x, rows * k * 2, "x", d), _at(w, n * k * 2, "w", d),
+        None if bias is None else _at(bias, 2 * n, "bias", d),
+        None if res is None else _at(res, rows * n * 2, "res", d),
         None if f32 else py, py if f32 else None,
-        None if status is None else _on_device(status, 4, "status", d), _raw_stream(stream))
-    _check(rc, "moe_linear")
+        None if status is None else _at(status, 4, "status", d), _stream_on(stream, d))
+    if rc:
+        _check(rc, "moe_linear")
 
 
 def moe_linear_glu(shape, inter: int, k: int, x, w13, h, bias=None, act: str = "silu",
@@ -563,11 +572,12 @@ def moe_linear_glu(shape, inter: int, k: int, x, w13, h, bias=None, act: str = "
     rows = sh.N * sh.T
     rc = (_lib or lib()).moe_linear_glu(
         ctypes.byref(sh), inter, k, _named(MOE_ACTS, act, "act"),
-        _on_device(x, rows * k * 2, "x", d), _on_device(w13, 4 * inter * k, "w13", d),
-        None if bias is None else _on_device(bias, 4 * inter, "bias", d),
-        _on_device(h, rows * inter * 2, "h", d),
-        None if status is None else _on_device(status, 4, "status", d), _raw_stream(stream))
-    _check(rc, "moe_linear_glu")
+        _at(x, rows * k * 2, "x", d), _at(w13, 4 * inter * k, "w13", d),
+        None if bias is None else _at(bias, 4 * inter, "bias", d),
+        _at(h, rows * inter * 2, "h", d),
+        None if status is None else _at(status, 4, "status", d), _stream_on(stream, d))
+    if rc:
+        _check(rc, "moe_linear_glu")
 
 
 def moe_topk(shape, logits, topk_idx, topk_w, bias=None, score: str = "softmax", groups: int = 1,
@@ -578,14 +588,15 @@ def moe_topk(shape, logits, topk_idx, topk_w, bias=None, score: str = "softmax",
     [E] is added to the scores for the choice alone; of ``groups`` runs of experts the
     ``kept`` whose ``best`` largest sum to most take part."""
     sh, d = _as_shape(shape), torch._C._cuda_getDevice()
-    rows = sh.N * sh.T
+    rows, E = sh.N * sh.T, sh.E
+    nk = rows * sh.R * 4
     rc = (_lib or lib()).moe_topk(
-        ctypes.byref(sh), _named(MOE_SCORES, score, "score"), groups, kept, best, bool(renorm),
-        scale, _on_device(logits, rows * sh.E * 4, "logits", d),
-        None if bias is None else _on_device(bias, sh.E * 4, "bias", d),
-        _on_device(topk_idx, rows * sh.R * 4, "topk_idx", d),
-        _on_device(topk_w, rows * sh.R * 4, "topk_w", d), _raw_stream(stream))
-    _check(rc, "moe_topk")
+        ctypes.byref(sh), _named(MOE_SCORES, score, "score"), groups, kept, best,
+        1 if renorm else 0, scale, _at(logits, rows * E * 4, "logits", d),
+        None if bias is None else _at(bias, E * 4, "bias", d),
+        _at(topk_idx, nk, "topk_idx", d), _at(topk_w, nk, "topk_w", d), _stream_on(stream, d))
+    if rc:
+        _check(rc, "moe_topk")
 
 
 def moe_block_norm(shape, x, gamma, eps: float, res_out=None, y=None, q=None, s=None,
@@ -595,18 +606,20 @@ def moe_block_norm(shape, x, gamma, eps: float, res_out=None, y=None, q=None, s=
     ``post_gamma``) into ``res_out``, and v's norm times ``gamma`` as bf16 rows ``y`` and
     their e4m3 coding (``q``, ``s``), each where a buffer is given.  ``gate`` [gates][H]
     has a row for each run of N*T / gates rows."""
-    sh, d = _as_shape(shape), torch._C._cuda_getDevice()
-    H = sh.H
-    nx = sh.N * sh.T * H * 2
-
-    def at(t, nbytes, name):
-        return None if t is None else _on_device(t, nbytes, name, d)
+    sh, d, at = _as_shape(shape), torch._C._cuda_getDevice(), _at
+    row = 2 * sh.H
+    nx = sh.N * sh.T * row
     rc = (_lib or lib()).moe_block_norm(
-        ctypes.byref(sh), eps, scale, gates, _on_device(x, nx, "x", d),
-        at(post_gamma, 2 * H, "post_gamma"), at(gate, 2 * gates * H, "gate"), at(res, nx, "res"),
-        at(gamma, 2 * H, "gamma"), at(res_out, nx, "res_out"), at(y, nx, "y"),
-        at(q, nx // 2, "q"), at(s, nx // 64, "s"), _raw_stream(stream))
-    _check(rc, "moe_block_norm")
+        ctypes.byref(sh), eps, scale, gates, at(x, nx, "x", d),
+        None if post_gamma is None else at(post_gamma, row, "post_gamma", d),
+        None if gate is None else at(gate, gates * row, "gate", d),
+        None if res is None else at(res, nx, "res", d),
+        None if gamma is None else at(gamma, row, "gamma", d),
+        None if res_out is None else at(res_out, nx, "res_out", d),
+        None if y is None else at(y, nx, "y", d), None if q is None else at(q, nx // 2, "q", d),
+        None if s is None else at(s, nx // 64, "s", d), _stream_on(stream, d))
+    if rc:
+        _check(rc, "moe_block_norm")
 
 
 class MoeLLBuffers:

@@ -91,7 +91,7 @@ class Device:
         self.nbytes, self.is_cuda, self.device_, self.dtype = n, cuda, device, dtype
 
     def get_device(self):
-        return self.device_
+        return self.device_ if self.is_cuda else -1
 
     def is_contiguous(self):
         return True
@@ -138,7 +138,7 @@ def test_binding_refuses_small_host_and_foreign_tensors(lib, monkeypatch, name):
         def __getattr__(self, fn):
             return lambda *a: launched.append(fn) or m.MOE_OK
     monkeypatch.setattr(m, "_lib", Lib())
-    monkeypatch.setattr(m, "_raw_stream", lambda stream: 0)
+    monkeypatch.setattr(m, "_stream_on", lambda stream, device: 0)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     good = {k: Device(n) for k, n in NEEDS[name].items()}
     CALLS[name](sh, good)
@@ -160,7 +160,7 @@ def test_binding_names_and_output_type(lib, monkeypatch):
             return m.MOE_OK
         moe_topk = moe_linear
     monkeypatch.setattr(m, "_lib", Lib)
-    monkeypatch.setattr(m, "_raw_stream", lambda stream: 0)
+    monkeypatch.setattr(m, "_stream_on", lambda stream, device: 0)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     big = Device(1 << 16)
     m.moe_linear(sh, 64, 64, big, big, Device(256))
