@@ -6,14 +6,15 @@
 #include "check.h"
 #include "coding.cuh"
 #include "launch.h"
+#include "tc.cuh"
 #include "trace.h"
 
 namespace moe {
 
 struct BlockNorm {
     int H, rows;
-    unsigned per_gate;  // rows that share a row of gate
-    float eps, scale;
+    uint64_t gate_of;  // 2^64 / rows that share a row of gate, above it; 0: each has its own
+    float eps, scale, inv_H;
     const uint16_t *x, *post, *gate, *res, *gamma;
     uint16_t *res_out, *y;
     uint8_t *q;
@@ -40,69 +41,95 @@ __device__ __forceinline__ uint4 vec8(const uint16_t *p, int c) {
     return __ldg(reinterpret_cast<const uint4 *>(p + c * 8));
 }
 
+// Eight bf16 values as four pairs of floats; pairs keep the instructions few, which
+// bound this kernel with its threads.
+__device__ __forceinline__ void widen8(uint64_t (&v)[4], const uint4 &w) {
+    v[0] = widen2(w.x), v[1] = widen2(w.y), v[2] = widen2(w.z), v[3] = widen2(w.w);
+}
+__device__ __forceinline__ uint32_t narrow2(uint64_t v) {
+    const float2 f = unpack2(v);
+    return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ uint4 narrow8(const uint64_t (&v)[4]) {
+    return make_uint4(narrow2(v[0]), narrow2(v[1]), narrow2(v[2]), narrow2(v[3]));
+}
+__device__ __forceinline__ uint64_t both(float f) {
+    return pack2(__float_as_uint(f), __float_as_uint(f));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    const float2 f = unpack2(v);
+    return f.x + f.y;
+}
+
 // A row, the block's or (kWarp) the warp's, from its V chunks of eight elements a
-// thread, chunk tid + i * nthr of them:
-// xr holds x, r the residual, as they were read: unpacked they would take twice the
-// registers while the first sum is waited for.
+// thread, chunk tid + i * nthr of them: xr holds x, r the residual, as they were read:
+// unpacked they would take twice the registers while the first sum is waited for.
 template <int V, bool kWarp>
 __device__ __forceinline__ void row_norm(const BlockNorm &p, size_t row, const uint4 (&xr)[V],
                                          const uint4 (&r)[V], float *part0, float *part1) {
     const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, nthr = kWarp ? 32 : blockDim.x;
     const int nch = p.H >> 3;
     const size_t base = row * (size_t)p.H;
-    float rstd = 1.0f, acc = 0.0f;
+    float rstd = 1.0f;
+    uint64_t acc = 0;
     if (p.post) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (tid + i * nthr < nch) {
-                float w[8];
-                unpack8(w, xr[i]);
+                uint64_t w[4];
+                widen8(w, xr[i]);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) acc = __fmaf_rn(w[u], w[u], acc);
+                for (int u = 0; u < 4; ++u) acc = fma2(w[u], w[u], acc);
             }
-        rstd = __frsqrt_rn(row_sum<kWarp>(acc, part0) / (float)p.H + p.eps);
-        acc = 0.0f;
+        rstd = rsqrtf(row_sum<kWarp>(sum2(acc), part0) * p.inv_H + p.eps);
+        acc = 0;
     }
-    float v[V][8];
-    const uint16_t *gate = p.gate ? p.gate + (size_t)((unsigned)row / p.per_gate) * p.H : nullptr;
+    uint64_t v[V][4];
+    const uint16_t *gate = p.gate;
+    if (gate) gate += (p.gate_of ? __umul64hi(row, p.gate_of) : row) * p.H;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nthr;
         if (c >= nch) continue;
-        float w[8];
-        unpack8(v[i], xr[i]);
+        uint64_t w[4];
+        widen8(v[i], xr[i]);
         if (p.post) {
-            unpack8(w, vec8(p.post, c));
+            widen8(w, vec8(p.post, c));
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
+            for (int u = 0; u < 4; ++u) v[i][u] = mul2(mul2(v[i][u], both(rstd)), w[u]);
         }
         if (gate) {
-            unpack8(w, vec8(gate, c));
+            widen8(w, vec8(gate, c));
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[i][u] *= w[u];
+            for (int u = 0; u < 4; ++u) v[i][u] = mul2(v[i][u], w[u]);
         }
-        unpack8(w, r[i]);
+        widen8(w, r[i]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            v[i][u] = __fmaf_rn(p.scale, v[i][u], w[u]);
-            acc = __fmaf_rn(v[i][u], v[i][u], acc);
+        for (int u = 0; u < 4; ++u) {
+            v[i][u] = fma2(both(p.scale), v[i][u], w[u]);
+            acc = fma2(v[i][u], v[i][u], acc);
         }
-        if (p.res_out) *reinterpret_cast<uint4 *>(p.res_out + base + c * 8) = pack_bf16x8(v[i]);
+        if (p.res_out) *reinterpret_cast<uint4 *>(p.res_out + base + c * 8) = narrow8(v[i]);
     }
     if (!p.y && !p.q) return;
-    rstd = __frsqrt_rn(row_sum<kWarp>(acc, part1) / (float)p.H + p.eps);
+    rstd = rsqrtf(row_sum<kWarp>(sum2(acc), part1) * p.inv_H + p.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = tid + i * nthr;
         const bool in = c < nch;
         uint32_t amax = 0;
+        float f[8];
         if (in) {
-            float w[8];
-            unpack8(w, vec8(p.gamma, c));
+            uint64_t w[4];
+            widen8(w, vec8(p.gamma, c));
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
-            if (p.y) *reinterpret_cast<uint4 *>(p.y + base + c * 8) = pack_bf16x8(v[i]);
-            amax = amax8(v[i]);
+            for (int u = 0; u < 4; ++u) {
+                v[i][u] = mul2(mul2(v[i][u], both(rstd)), w[u]);
+                const float2 g = unpack2(v[i][u]);
+                f[2 * u] = g.x, f[2 * u + 1] = g.y;
+            }
+            if (p.y) *reinterpret_cast<uint4 *>(p.y + base + c * 8) = narrow8(v[i]);
+            amax = amax8(f);
         }
         if (p.q) {
             // the sixteen chunks of a block of 128 are sixteen neighbouring lanes
@@ -110,7 +137,7 @@ __device__ __forceinline__ void row_norm(const BlockNorm &p, size_t row, const u
             for (int d = 8; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, d));
             if (in) {
                 const float scale = block_scale(amax);
-                *reinterpret_cast<uint2 *>(p.q + base + c * 8) = code8_by(v[i], scale);
+                *reinterpret_cast<uint2 *>(p.q + base + c * 8) = code8_by(f, scale);
                 if ((c & 15) == 0) p.s[row * (size_t)(p.H >> 7) + (c >> 4)] = scale;
             }
         }
@@ -121,7 +148,7 @@ __device__ __forceinline__ void row_norm(const BlockNorm &p, size_t row, const u
 constexpr int kRowWarps = 4;
 template <int V, int kMost, bool kWarp>
 __global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 4 : V == 4 ? 2 : 1) : 1)
-    k_block_norm(const BlockNorm p) {
+    k_block_norm(const __grid_constant__ BlockNorm p) {
     __shared__ float part[2][32];
     const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, nthr = kWarp ? 32 : blockDim.x;
     const int nch = p.H >> 3;
@@ -201,7 +228,8 @@ extern "C" int moe_block_norm(const moe_shape *sh, float eps, float scale, int g
     moe::BlockNorm p = {};
     p.H = sh->H;
     p.rows = (int)rows;
-    p.per_gate = gate ? (unsigned)(rows / gates) : 1u;
+    if (gate && gates < rows) p.gate_of = ~0ull / (uint64_t)(rows / gates) + 1;
+    p.inv_H = 1.0f / (float)sh->H;
     p.eps = eps;
     p.scale = scale;
     p.x = x;

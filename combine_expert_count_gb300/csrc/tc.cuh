@@ -332,6 +332,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
+// Two products.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// A pair of bf16 values as two floats.
+__device__ __forceinline__ uint64_t widen2(uint32_t w) { return pack2(w << 16, w & 0xffff0000u); }
+
 // Barrier `id` of `n` threads.
 __device__ __forceinline__ void bar_named(int id, int n) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
