@@ -378,8 +378,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     if (s.stop) {  // a kernel that gave up leaves no copy and no product in flight
         if (rank == 0 && warp == kPairTma && lane == 0)
+            // (where the other CTA brought nothing this CTA's copies are there all the same
+            // after the first of these waits)
             for (int i = max(0, issued - kPairStages); i < issued; ++i)
-                mbar_wait(&s.full[i % kPairStages], (i / kPairStages) & 1);
+                if (!mbar_wait(&s.full[i % kPairStages], (i / kPairStages) & 1)) break;
         if (rank == 0 && warp == kPairMma) {
             tc_commit_one_of_pair(&s.drain, elect_one());
             mbar_wait(&s.drain, 0);

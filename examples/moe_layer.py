@@ -4,13 +4,18 @@
                                  [--experts E] [--topk R] [--inter I]
 
 The residual stream goes through moe_rmsnorm (addition and norm in one pass), a
-router picks experts (plain torch here), and the layer runs twice:
+router picks experts (moe_linear's fp32 logits, moe_topk), and the layer runs twice:
 
   * as a batch: moe_dispatch groups the coded rows by expert,
     moe_expert_gemm_swiglu and moe_expert_gemm are the experts, moe_combine
     brings the weighted sums back;
   * for its first tokens alone, as a decode step of a few sequences does:
     moe_layer_few, which reads nothing but the chosen experts' weights.
+
+After the batch a shared expert with 16-bit weights (moe_linear_glu, and moe_linear
+with the routed experts' output as its residual) and the block's end (moe_block_norm:
+the norm after the layer, a gate of each channel, the residual and the next layer's
+norm with its coding) complete the block.
 
 The two use the same coded weights and the same roundings up to the batch's bf16
 expert outputs, so their results agree; the difference is printed, and the time
@@ -64,6 +69,7 @@ def main(argv=None) -> float:
     ap.add_argument("--experts", type=int, default=128)
     ap.add_argument("--topk", type=int, default=8)
     ap.add_argument("--inter", type=int, default=768)
+    ap.add_argument("--shared", type=int, default=0, help="width of the shared expert (--inter's)")
     ap.add_argument("--few", type=int, default=8, help="tokens of the decode step")
     a = ap.parse_args(argv)
     N, T, H, E, R, I = a.ranks, a.tokens, a.hidden, a.experts, a.topk, a.inter
@@ -81,8 +87,15 @@ def main(argv=None) -> float:
     x = torch.empty_like(residual)
     m.moe_rmsnorm(m.make_shape(N, T, E, R, H), attention, gamma, 1e-6, y=x, res=residual,
                   res_out=residual)
-    w, idx = (x @ router.T).float().softmax(-1).topk(R, dim=-1)
-    w, idx = (w / w.sum(-1, keepdim=True)).contiguous(), idx.int().contiguous()
+    rows = m.make_shape(N, T, E, R, H)
+    logits = torch.empty((N, T, E), device="cuda")
+    idx = torch.empty((N, T, R), dtype=torch.int32, device="cuda")
+    w = torch.empty((N, T, R), device="cuda")
+
+    def route():
+        m.moe_linear(rows, E, H, x, router, logits)
+        m.moe_topk(rows, logits, idx, w)
+    route()
 
     # the batch
     buf = m.MoeBuffers(N, T, E, R, H)
@@ -93,6 +106,25 @@ def main(argv=None) -> float:
         buf.combine(idx, w)
     batch_us = graph_us(batch)
     assert int(buf.status.item()) == 0
+
+    # the rest of the block: the shared expert on top of the routed ones, and the end
+    S = a.shared or I
+    s13, s2 = bf16(2 * S, H) / H ** 0.5, bf16(H, S) / S ** 0.5
+    post, gate, after = 1 + bf16(H) / 8, bf16(1, H) / 2, 1 + bf16(H) / 8
+    h = torch.empty((N, T, S), dtype=torch.bfloat16, device="cuda")
+    both, stream, nxt = (torch.empty_like(x) for _ in range(3))
+    nxt_q = torch.empty((N, T, H), dtype=torch.uint8, device="cuda")
+    nxt_s = torch.empty((N, T, H // 128), device="cuda")
+
+    def block():
+        route()
+        batch()
+        m.moe_linear_glu(rows, S, H, x, s13, h)
+        m.moe_linear(rows, H, S, h, s2, both, res=buf.out, status=buf.status)
+        m.moe_block_norm(rows, both, after, 1e-6, res_out=stream, y=nxt, q=nxt_q, s=nxt_s,
+                         post_gamma=post, gate=gate, res=residual)
+    block_us = graph_us(block)
+    assert int(buf.status.item()) == 0 and bool(nxt.isfinite().all())
 
     # its first tokens alone
     few = min(a.few, T, m.MOE_FEW_MAX_TOKENS)
@@ -109,7 +141,8 @@ def main(argv=None) -> float:
 
     off = float((out.float() - buf.out[0, :few].float()).norm() / out.float().norm())
     print(f"{N} ranks x {T} tokens, hidden {H}, {E} experts of {I}, top-{R}: "
-          f"batch {batch_us:.1f} us, {few} tokens alone {few_us:.1f} us, "
+          f"batch {batch_us:.1f} us (with router, shared expert and block end {block_us:.1f}), "
+          f"{few} tokens alone {few_us:.1f} us, "
           f"their outputs differ by {off:.2g} of their norm")
     return off
 
