@@ -9,7 +9,7 @@
 // experts, four.
 //
 // Measured: 32767 tokens, 8 of 128 experts 11.6 us (1.6 TB/s), of 256 16.8 (2.1 TB/s);
-// 2048 tokens, 8 of 256 4.3, with a bias and four of eight runs kept 10.6.  It is bound
+// 2048 tokens, 8 of 256 4.3, with a bias and four of eight runs kept 9.7.  It is bound
 // by instructions: at 128 experts about 150 a token and lane of eight, most of them in
 // the sorting networks (19 exchanges for eight keys, 12 for each further eight and each
 // doubling of the lanes); one token after another by whole warps took 26 us.  Few
@@ -234,15 +234,13 @@ __device__ __noinline__ bool kept_exact(const Router &p, const float *l, long lo
 }
 
 // The choice, by all lanes of a warp, of the kept experts whose c is `least` or more in
-// fp32: lane r gets the r-th.  Only with a bias.  False: not told apart.
-template <class T>
-__device__ __noinline__ bool choose_exact(const Router &p, const float *l, long long *room,
-                                          uint16_t *list, float top, uint32_t kept, float least,
-                                          int *mine) {
-    constexpr bool kFixed = T(0.5) == T(0);
-    T *c = reinterpret_cast<T *>(room);
+// fp32, in 64 bits: lane r gets the r-th.  Only with a bias.
+__device__ __noinline__ void choose64(const Router &p, const float *l, long long *room,
+                                      uint16_t *list, float top, uint32_t kept, float least,
+                                      int *mine) {
+    double *c = reinterpret_cast<double *>(room);
     const int lane = threadIdx.x & 31;
-    const double sum = kFixed ? 1.0 : sum64(p, l, top);
+    const double sum = sum64(p, l, top);
     int n = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {  // listed in the order of their index
         const int e = e0 + lane;
@@ -258,31 +256,19 @@ __device__ __noinline__ bool choose_exact(const Router &p, const float *l, long 
         n += __popc(who);
     }
     __syncwarp();
-    bool ok = true;
-    for (int j = lane; j < n; j += 32) {
-        c[j] = value_exact<T>(p, l, list[j], top, sum);
-        if (kFixed) ok &= fits(p.bias[list[j]]);
-    }
+    for (int j = lane; j < n; j += 32) c[j] = value_exact<double>(p, l, list[j], top, sum);
     __syncwarp();
-    const T none = kFixed ? T(kNone) : T(-(double)INFINITY);
     for (int j0 = 0; j0 < n; j0 += 32) {
         const int j = j0 + lane;
         int before = 32;
         if (j < n) {
-            const T x = c[j];
             before = 0;
-            for (int o = 0; o < n; ++o) {
-                const T y = c[o];
-                before += y > x || (y == x && o < j);
-                if (kFixed && o != j && x != none && y != none)
-                    ok &= y - x > T(kNear) || x - y > T(kNear);
-            }
+            for (int o = 0; o < n; ++o) before += c[o] > c[j] || (c[o] == c[j] && o < j);
         }
         for (int o = 0; o < 32; ++o)  // candidate j0 + o goes to the lane of its rank
             if (__shfl_sync(kFull, before, o) == lane) *mine = list[j0 + o];
     }
     __syncwarp();
-    return __all_sync(kFull, ok);
 }
 
 // A lane's logits: v[4 q + j] is expert 128 q + 4 lane + j; -infinity behind the last.
@@ -444,34 +430,33 @@ __device__ __forceinline__ uint32_t kept_runs(const Router &p, const float *l, c
     return kept;
 }
 
-// The R largest keys, one after another: lane r gets the r-th's expert.  With a bias,
-// whether two neighbours, or the last and the one behind it, are nearer than their
-// errors (close), and the last key that was looked at.
+// The R largest keys, one after another, equal ones by their index: lane r gets the
+// r-th's expert.  With a bias those behind the R-th too that may be before it as far as
+// fp32 knows, n in all, `over` where they are more than the lanes; `least` is as far as
+// they go.
 struct Chosen {
-    int mine;
-    uint32_t last;
-    bool close;
+    int mine, n;
+    float c, least;  // what chose it
+    bool over;
 };
-
-__device__ __forceinline__ bool near(const Router &p, uint32_t last, uint32_t next) {
-    const float a = value_of(last), b = value_of(next);
-    return b > -INFINITY && a - b <= error_of(p.score, a) + error_of(p.score, b);
-}
 
 template <int C>
 __device__ __forceinline__ Chosen take_any(const Router &p, uint32_t (&key)[C]) {
     const int lane = threadIdx.x & 31;
-    Chosen got = {0, ~0u, false};
-    for (int r = 0; r <= p.R; ++r) {
+    Chosen got = {0, 0, -INFINITY, -INFINITY, false};
+    for (int r = 0;; ++r) {
         if (r == p.R && !p.bias) break;
         uint32_t m = key[0];
 #pragma unroll
         for (int i = 1; i < C; ++i) m = max(m, key[i]);
         const uint32_t most = __reduce_max_sync(kFull, m);
-        if (most == 0u) break;  // no one is behind the R
-        if (p.bias && got.last != ~0u) got.close |= near(p, got.last, most);
-        got.last = most;
-        if (r == p.R) break;
+        if (most == 0u) break;  // no one is left
+        const float c = value_of(most);
+        // a masked one is behind all others, by its index
+        if (r >= p.R && (!(c >= got.least) || c == -INFINITY)) break;
+        got.over = r == 32;
+        if (got.over) break;
+        if (r == p.R - 1) got.least = c > -INFINITY ? c - 2.0f * error_of(p.score, c) : -INFINITY;
         // its place in the lanes that have it, and of those the lowest
         int i0 = 0;
 #pragma unroll
@@ -484,9 +469,37 @@ __device__ __forceinline__ Chosen take_any(const Router &p, uint32_t (&key)[C]) 
             for (int i = 0; i < C; ++i)
                 if (i == i0) key[i] = 0u;
         }
-        if (lane == r) got.mine = (int)first;
+        if (lane == r) got.mine = (int)first, got.c = c;
+        got.n = r + 1;
     }
     return got;
+}
+
+// The candidates of take_any in the order of their exact values, in fixed point.  Short,
+// and by the lanes that have them: it is code that one token in 2000 needs, which comes
+// from beyond the caches for it.  False: not told apart.
+__device__ __forceinline__ bool order_fixed(const Router &p, const float *l, uint16_t *list,
+                                            Chosen &got) {
+    const int lane = threadIdx.x & 31;
+    const bool in = lane < got.n;
+    const long long c = in ? value_exact<long long>(p, l, got.mine, 0.0f, 1.0) : kNone;
+    bool ok = !got.over && (!in || fits(p.bias[got.mine]));
+    int before = 0;
+    for (int o = 0; o < got.n; ++o) {
+        const long long y = __shfl_sync(kFull, c, o);
+        before += y > c || (y == c && o < lane);
+        if (o != lane && c != kNone && y != kNone) ok &= y - c > kNear || c - y > kNear;
+    }
+    if (in) list[before] = (uint16_t)got.mine;
+    __syncwarp();
+    if (in) got.mine = list[lane];
+    __syncwarp();
+    return __all_sync(kFull, ok);
+}
+
+__device__ __forceinline__ bool near(const Router &p, uint32_t last, uint32_t next) {
+    const float a = value_of(last), b = value_of(next);
+    return b > -INFINITY && a - b <= error_of(p.score, a) + error_of(p.score, b);
 }
 
 // One token, by all lanes of a warp.
@@ -534,15 +547,17 @@ __device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C>
         }
     }
     Chosen got = take_any(p, key);
-    if (got.close) {
-        // nothing below the last one by more than both errors can be among the first R
-        const float c = value_of(got.last);
-        const float least = c > -INFINITY ? c - 2.0f * error_of(p.score, c) : -INFINITY;
-        int mine = 0;
-        if (p.score != MOE_SCORE_SIGMOID ||
-            !choose_exact<long long>(p, l, exact.c, exact.list, top, kept, least, &mine))
-            choose_exact<double>(p, l, exact.c, exact.list, top, kept, least, &mine);
-        got.mine = mine;
+    if (p.bias) {
+        // neighbours that are nearer than their errors, or some that may be before the R-th
+        const float next = __shfl_down_sync(kFull, got.c, 1);
+        const bool close = lane + 1 < got.n && next > -INFINITY &&
+                           got.c - next <= error_of(p.score, got.c) + error_of(p.score, next);
+        if (__any_sync(kFull, close) || got.over || got.n > p.R)
+            if (p.score != MOE_SCORE_SIGMOID || !order_fixed(p, l, exact.list, got)) {
+                int mine = 0;
+                choose64(p, l, exact.c, exact.list, top, kept, got.least, &mine);
+                got.mine = mine;
+            }
     }
     // the weights, lane r the r-th; sums over as many lanes as there may be
     const int half = p.R > 8 ? 16 : 4;
@@ -866,9 +881,9 @@ static cudaError_t launch(K kern, int tokens, int warps, const Router &p, cudaSt
 
 static cudaError_t launch_topk(const Router &p, cudaStream_t st) {
     // us with a warp and with eight lanes a token, 256 experts: one token 3.5 and 3.2, 2048
-    // 6.6 and 4.3, 32767 32 and 17; with a bias and four of eight runs 8 tokens 4.7 and
-    // 6.1, 2048 10.6 and 12.2, 8192 17 and 23, 32767 53 and 40: there some tokens go
-    // the warp's way after the other
+    // 6.6 and 4.3, 32767 32 and 17; with a bias and four of eight runs 8 tokens 4.6 and
+    // 6.1, 2048 9.7 and 12.2, 8192 16 and 23, 32767 53 and 38: there some tokens go the
+    // warp's way after the other
     if (p.R <= kFastMost && p.E >= 32 && p.E <= 512 && p.E % 4 == 0 &&
         (p.groups == p.kept || p.per % 32 == 0) && (!p.bias || p.rows > 96 * sm_count())) {
         const auto kern = p.E <= 128   ? k_topk_fast<16>
