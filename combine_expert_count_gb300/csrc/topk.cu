@@ -174,7 +174,7 @@ __device__ __forceinline__ T value_exact(const Router &p, const float *l, int e,
                                          double sum) {
     const float v = l[e], b = p.bias ? p.bias[e] : 0.0f;
     if constexpr (T(0.5) == T(0)) {
-        if (v == -INFINITY || !(fabsf(b) < 32768.0f) || v != v) return kNone;
+        if (v == -INFINITY || !(fabsf(b) < 16384.0f) || v != v) return kNone;
         return sigmoid_fixed(v) + __float2ll_rn(b * 0x1p46f);
     } else {
         double c = p.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-(double)v))
@@ -183,8 +183,11 @@ __device__ __forceinline__ T value_exact(const Router &p, const float *l, int e,
         return v != -INFINITY && c == c ? c : -(double)INFINITY;
     }
 }
-// Whether fixed point holds the bias (-infinity and NaN are as good as a masked logit).
-__device__ __forceinline__ bool fits(float b) { return fabsf(b) < 32768.0f || b != b || b == -INFINITY; }
+// Whether fixed point holds the bias, and the difference of two runs' worths (-infinity
+// and NaN are as good as a masked logit).
+__device__ __forceinline__ bool fits(float b) {
+    return fabsf(b) < 16384.0f || b != b || b == -INFINITY;
+}
 
 __device__ __forceinline__ double sum64(const Router &p, const float *l, float top) {
     if (p.score == MOE_SCORE_SIGMOID) return 1.0;
@@ -499,7 +502,8 @@ __device__ __forceinline__ bool order_fixed(const Router &p, const float *l, uin
 
 __device__ __forceinline__ bool near(const Router &p, uint32_t last, uint32_t next) {
     const float a = value_of(last), b = value_of(next);
-    return b > -INFINITY && a - b <= error_of(p.score, a) + error_of(p.score, b);
+    // (two of +infinity, whose difference is NaN, too)
+    return b > -INFINITY && !(a - b > error_of(p.score, a) + error_of(p.score, b));
 }
 
 // One token, by all lanes of a warp.

@@ -148,6 +148,32 @@ def test_bias_of_no_value_takes_an_expert_out():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", ["plain", "infinite", "all infinite", "none", "huge"])
+def test_long_batches_way(score, bias):
+    """Tokens that are repeated until they go eight lanes each: what they get alone, with
+    biases that put several experts at one value, out of service or beyond fixed point."""
+    l, b = draw(40, 64, 12)
+    l[3, 5:] = l[7] = -INF
+    l[11, 8], l[13, 9] = float("nan"), INF
+    l[17] = 0.5
+    if bias == "infinite":
+        b[5], b[40], b[41] = INF, INF, INF
+    elif bias == "all infinite":
+        b[:] = INF
+    elif bias == "none":
+        b[::2], b[1] = -INF, float("nan")
+    elif bias == "huge":
+        b[7], b[9], b[11], b[33:35] = 3e38, -3e38, 2e38, 16383.0
+    rest = [i for i in range(40) if i not in (11, 13)]
+    for kw in (dict(), dict(groups=2, kept=1, best=2), dict(groups=2, kept=1, best=1)):
+        few = choose(l, 6, score=score, bias=b, **kw)
+        check(l[rest], 6, score=score, bias=b, **kw)
+        long = choose(l.repeat(500, 1), 6, score=score, bias=b, **kw)
+        for a, c in zip(few, long):
+            assert torch.equal(a.repeat(500, 1).view(torch.int32), c.view(torch.int32))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_not_a_number_stays_in_its_row(score, with_bias):
     l, bias = draw(9, 64, 4)
