@@ -120,9 +120,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tma_prefetch_map(&map_w);
     }
     if (warp == kLinMma) tc_alloc<kCols>(&s.tmem);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
+    // (not before the tensor memory is this CTA's: the next kernel's may take the rest)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_after();
     if (parts > 1) cluster_arrive();  // this part is there: others may write to it
     asm volatile("griddepcontrol.wait;" ::: "memory");

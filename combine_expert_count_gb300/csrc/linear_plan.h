@@ -90,8 +90,12 @@ inline LinearPlan linear_plan(int64_t rows, int64_t n, int64_t k, bool pair, boo
     best.stages = (kSmem - 1280 - apart) / stage;
     if (best.stages > 6) best.stages = 6;
     if (best.stages > mine) best.stages = (int)mine;
+    // Tensor memory goes with shared memory: CTAs that fit an SM by the one fit by the
+    // other, and none waits for columns that a later kernel's CTAs hold.
+    const int columns = f32 ? 2 * best.at : best.at;
     const int sums = apart ? 1 : (best.at * 512 + stage - 1) / stage;  // their room
-    if (best.stages < sums) best.stages = sums;
+    while (best.stages < sums || 1280 + apart + best.stages * stage < columns * (kSmem / 512))
+        ++best.stages;
     return best;
 }
 

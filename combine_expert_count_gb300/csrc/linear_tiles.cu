@@ -226,9 +226,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tma_prefetch_map(&map_w);
     }
     if (warp == kPairMma) tc_alloc_pair<512>(&s.tmem);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
+    // (not before the tensor memory is this CTA's: the next kernel's may take the rest)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cluster_sync();  // the other CTAs' barriers are there too
     tc_fence_after();
     asm volatile("griddepcontrol.wait;" ::: "memory");

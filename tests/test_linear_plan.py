@@ -47,3 +47,6 @@ def test_what_it_chooses_is_possible():
         stage, apart = 2 * (16384 + p.at * 128), p.at * 512 if p.at <= 32 else 0
         assert 1 <= p.stages <= 6 and 1280 + apart + p.stages * stage <= SMEM
         assert apart or p.stages * stage >= p.at * 512
+        # an SM's 512 columns of tensor memory last for the CTAs that its shared memory holds
+        columns = max(32, p.at * (2 if f32 else 1))
+        assert 233472 // (1024 + 1280 + apart + p.stages * stage) * columns <= 512
