@@ -23,7 +23,7 @@ constexpr int kLinTma = 4, kLinMma = 5, kLinWarps = 6, kLinThreads = 32 * kLinWa
 constexpr int kLinTile = 128 * 128;  // bytes of a weight tile of a block of k
 constexpr int kLinRun = 4;           // stages between the sums of an fp32 result: 512 of k
 constexpr int kLinMostStages = 6;
-constexpr int kAtOnce = 4;           // rows that a warp finishes together
+constexpr int kAtOnce = 4;           // units that a warp finishes together
 
 struct LinShared {
     uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain;
@@ -35,72 +35,66 @@ static_assert(sizeof(LinShared) <= kLinHead, "");
 
 // two blocks of weights, then two of rows
 __host__ __device__ constexpr int lin_stage(int NR) { return 2 * (kLinTile + NR * 128); }
+// The rows of a part: whole groups of four, which go to it together.  Where there are
+// more parts than groups the last parts have none.
+__host__ __device__ constexpr int lin_rows(int NR, int parts) {
+    return NR / parts < 4 ? 4 : NR / parts;
+}
 // Up to so many rows the parts' sums have room of their own; with more they go where the
 // ring was, once all parts are done with theirs.
-__host__ __device__ constexpr int lin_apart(int NR) { return NR <= 32 ? NR * 512 : 0; }
-__host__ __device__ constexpr int lin_smem(int NR, int stages) {
-    return kLinHead + 1024 + lin_apart(NR) + stages * lin_stage(NR);
+__host__ __device__ constexpr int lin_apart(int NR, int parts) {
+    return NR <= kLinearApart ? parts * lin_rows(NR, parts) * 512 : 0;
+}
+__host__ __device__ constexpr int lin_smem(int NR, int parts, int stages) {
+    return kLinHead + 1024 + lin_apart(NR, parts) + stages * lin_stage(NR);
 }
 
-// kOuts outputs c .. of a row, or as many as there are, from their sums (b: the up
-// projection's).
-template <bool kPair, bool kF32, int kOuts>
-__device__ __forceinline__ void store_outs(const Linear &p, size_t row, int c, const float *a) {
+// Two outputs of a row, c and c + 1 of p.n, or as many as there are.
+template <bool kF32>
+__device__ __forceinline__ void store_two(const Linear &p, size_t row, int c, float a, float b) {
     const size_t to = row * p.n + c;
-    if (p.n % kOuts == 0) {
-        if constexpr (kF32)
-            *reinterpret_cast<float4 *>(p.yf + to) = make_float4(a[0], a[1], a[2], a[3]);
-        else if constexpr (kPair)
-            *reinterpret_cast<uint32_t *>(p.y + to) = pack_bf16x2(a[0], a[1]);
+    if ((p.n & 1) == 0) {
+        if (c >= p.n) return;
+        if (kF32)
+            *reinterpret_cast<float2 *>(p.yf + to) = make_float2(a, b);
         else
-            *reinterpret_cast<uint2 *>(p.y + to) =
-                make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+            *reinterpret_cast<uint32_t *>(p.y + to) = pack_bf16x2(a, b);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < kOuts; ++i) {
+    for (int i = 0; i < 2; ++i) {
         if (c + i >= p.n) break;
         if (kF32)
-            p.yf[to + i] = a[i];
+            p.yf[to + i] = i ? b : a;
         else
-            p.y[to + i] = (uint16_t)pack_bf16x2(a[i], 0.0f);
+            p.y[to + i] = (uint16_t)pack_bf16x2(i ? b : a, 0.0f);
     }
 }
 
-// kOuts bf16 values from `at`, of which those before `end` are there.
-template <int kOuts>
-__device__ __forceinline__ void load_outs(const uint16_t *from, int c, int n, float (&v)[kOuts]) {
-    if (n % kOuts == 0) {
-        if (c >= n) return;
-        const uint32_t lo = *reinterpret_cast<const uint32_t *>(from);
-        v[0] = bf16_lo(lo), v[1] = bf16_hi(lo);
-        if constexpr (kOuts == 4) {
-            const uint32_t hi = *reinterpret_cast<const uint32_t *>(from + 2);
-            v[2] = bf16_lo(hi), v[3] = bf16_hi(hi);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < kOuts; ++i)
-        if (c + i < n) v[i] = bf16_lo(from[i]);
+// The residual of the same two, 0 where there is none.
+__device__ __forceinline__ uint32_t load_two(const Linear &p, size_t row, int c) {
+    const uint16_t *from = p.res + row * p.n + c;
+    if ((p.n & 1) == 0) return c < p.n ? *reinterpret_cast<const uint32_t *>(from) : 0u;
+    return (c < p.n ? from[0] : 0u) | (c + 1 < p.n ? (uint32_t)from[1] << 16 : 0u);
 }
 
 template <int NR, bool kPair, bool kF32>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear(const __grid_constant__ Linear p, int stages, const __grid_constant__ CUtensorMap map_x,
              const __grid_constant__ CUtensorMap map_w) {
-    constexpr int kBytes = lin_stage(NR), kOuts = kPair ? 2 : 4;
+    constexpr int kBytes = lin_stage(NR);
     constexpr int kAccs = kF32 ? 2 : 1;  // accumulators
     constexpr int kUsed = kAccs * NR, kCols = kUsed < 32 ? 32 : kUsed;
     extern __shared__ uint8_t smem_raw[];
     LinShared &s = *reinterpret_cast<LinShared *>(smem_raw);
     uint8_t *ring = smem_raw + kLinHead + align1024(smem_raw + kLinHead);
-    // sums [part][row / parts][128] of the rows that are this part's
-    float *left = reinterpret_cast<float *>(lin_apart(NR) ? ring + stages * kBytes : ring);
+    // sums [part][group of four rows][128][4] of the rows that are this part's
+    constexpr bool kApart = NR <= kLinearApart;
+    uint8_t *left = kApart ? ring + stages * kBytes : ring;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c0 = blockIdx.y * (kPair ? 64 : 128), row0 = blockIdx.x * NR;
     const int m = min(NR, p.rows - row0);
-    const int parts = (int)gridDim.z, part = (int)blockIdx.z, shift = __ffs(parts) - 1;
+    const int parts = (int)gridDim.z, part = (int)blockIdx.z;
     const int Kb = (p.k + 2 * kLinearBlock - 1) / (2 * kLinearBlock);  // stages of k
     const int b0 = (int)((long long)Kb * part / parts), b1 = (int)((long long)Kb * (part + 1) / parts);
 
@@ -193,32 +187,38 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
 
     // ---------------------------------------------------------------- the sums to their rows' parts
-    // what the outputs take beside their sums is asked for before those are there
-    const int c = c0 + lane * kOuts;
-    float bias[kOuts] = {}, bias2[kOuts] = {}, res[kAtOnce][kOuts] = {};
-    if (p.bias) {
-        load_outs(p.bias + c, c, p.n, bias);
-        if (kPair) {
-            if (p.n % kOuts == 0) {
-                load_outs(p.bias + p.n + c, c, p.n, bias2);
-            } else {
+    // A unit is four rows of 32 outputs, an output a lane; after their activation two
+    // lanes exchange, so that one has two outputs of the first two rows.
+    constexpr int kAcross = kPair ? 2 : 4;         // units side by side
+    const int LR = lin_rows(NR, parts), shift = __ffs(LR) - 1;  // rows of a part
+    const int mine0 = part * LR;                                 // this one's first
+    const int mm = min(m - mine0, LR);                           // as many as there are
+    const int units = (mm + 3) / 4 * kAcross;
+    const int odd = lane & 1;
+    // what the outputs take beside their sums is asked for before those are there; the
+    // bias of a warp's units, which are kLinWarps apart, is of two places at most
+    float bias[2] = {}, bias2[2] = {};
+    if (p.bias)
 #pragma unroll
-                for (int i = 0; i < kOuts; ++i)
-                    if (c + i < p.n) bias2[i] = bf16_lo(p.bias[p.n + c + i]);
+        for (int i = 0; i < (kPair ? 1 : 2); ++i) {
+            const int c = c0 + (warp + i * kLinWarps) % kAcross * 32 + lane;
+            if (c < p.n) {
+                bias[i] = bf16_lo(p.bias[c]);
+                if (kPair) bias2[i] = bf16_lo(p.bias[p.n + c]);
             }
         }
-    }
-    const int LR = NR >> shift, mine0 = part * LR;  // rows of a part; this one's first
-    const int mm = min(m - mine0, LR);              // as many as there are
-    // of this part's rows r, r + kLinWarps, ...
-    const auto residual = [&](int r) {
+    uint32_t res[kPair ? 1 : kAtOnce][2] = {};
+    const auto residual = [&](int u) {  // of units u, u + kLinWarps, ...
         if (!kPair && p.res)
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                const int j = r + i * kLinWarps;
-                if (j < mm)
-                    load_outs(p.res + (size_t)(row0 + mine0 + j) * p.n + c, c, p.n, res[i]);
-            }
+            for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int v = u + i * kLinWarps, r = v / kAcross * 4 + 2 * odd + h;
+                    if (r < mm)
+                        res[kPair ? 0 : i][h] =
+                            load_two(p, (size_t)row0 + mine0 + r, c0 + v % kAcross * 32 + (lane & 30));
+                }
     };
     residual(warp);
     tc_fence_before();
@@ -237,40 +237,38 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tc_fence_after();
     if (parts > 1) {
         cluster_wait();
-        if (!lin_apart(NR)) cluster_sync();  // all parts are done with their rings
+        if (!kApart) cluster_sync();  // all parts are done with their rings
         if (s.stop && tid < parts) st_dsmem(dsmem_addr(&s.any, tid), 1);
     }
     if (warp < 4 && !s.stop) {
         const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
-        // rows j0 .. j0 + 15, of LR or more parts each: their addresses in the cluster
-        const auto leave = [&](int j0, const uint32_t (&v)[16]) {
-            uint32_t to = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (j0 + i >= m) return;
-                if (i == 0 || ((j0 + i) & (LR - 1)) == 0) {
-                    const int owner = (j0 + i) / LR, r = (j0 + i) & (LR - 1);
-                    float *at = left + (part * LR + r) * 128 + tid;
-                    to = (parts > 1 ? dsmem_addr(at, owner) : smem_addr(at)) - i * 512;
-                }
-                st_dsmem(to + i * 512, v[i]);
-            }
+        uint8_t *const to = left + part * LR * 512 + tid * 16;
+        // rows j .. j + 3 to their part
+        const auto leave = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            if (j >= m) return;
+            uint8_t *const at = to + (j & (LR - 1)) * 512;
+            if (parts > 1)
+                st_dsmem4(dsmem_addr(at, j >> shift), a, b, c, d);
+            else
+                *reinterpret_cast<uint4 *>(at) = make_uint4(a, b, c, d);
         };
         if constexpr (kF32) {
 #pragma unroll
-            for (int j = 0; j < NR; j += 16) {
-                uint32_t v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[kF32 ? j + i : 0]);
-                leave(j, v);
-            }
+            for (int j = 0; j < NR; j += 4)
+                leave(j, __float_as_uint(acc[kF32 ? j : 0]), __float_as_uint(acc[kF32 ? j + 1 : 0]),
+                      __float_as_uint(acc[kF32 ? j + 2 : 0]), __float_as_uint(acc[kF32 ? j + 3 : 0]));
         } else {
 #pragma unroll 1
-            for (int j = 0; j < m; j += 16) {
-                uint32_t v[16];
-                tc_ld16(v, mine + j);
+            for (int j = 0; j < m; j += NR < 32 ? 16 : 32) {
+                uint32_t v[NR < 32 ? 1 : 2][16];
+#pragma unroll
+                for (int h = 0; h < (NR < 32 ? 1 : 2); ++h) tc_ld16(v[h], mine + j + 16 * h);
                 tc_wait_ld();
-                leave(j, v);
+#pragma unroll
+                for (int h = 0; h < (NR < 32 ? 1 : 2); ++h)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        leave(j + 16 * h + i, v[h][i], v[h][i + 1], v[h][i + 2], v[h][i + 3]);
             }
         }
     }
@@ -286,40 +284,48 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // where a part gave up the sums are not whole and no part stores any
     if (s.any || s.stop) return;
 #pragma unroll 1
-    for (int r = warp; r < mm; r += kAtOnce * kLinWarps) {
-        float a[kAtOnce * kOuts] = {}, b[kPair ? kAtOnce * kOuts : 1] = {};
+    for (int u = warp; u < units; u += kAtOnce * kLinWarps) {
+        float a[kAtOnce * 4] = {}, b[kPair ? kAtOnce * 4 : 1] = {};
+        const auto place = [&](int q, int i) {
+            const int v = min(u + i * kLinWarps, units - 1);
+            return left + (q * LR * 32 + v / kAcross * 128 + v % kAcross * 32 + lane) * 16;
+        };
         for (int q = 0; q < parts; ++q)  // in the parts' order
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                const int rr = min(r + i * kLinWarps, LR - 1);
-                const float *at = left + (q * LR + rr) * 128 + lane * kOuts;
+                const uint8_t *at = place(q, i);
+                const float4 f = *reinterpret_cast<const float4 *>(at);
+                a[i * 4] += f.x, a[i * 4 + 1] += f.y, a[i * 4 + 2] += f.z, a[i * 4 + 3] += f.w;
                 if constexpr (kPair) {
-                    const float2 g = *reinterpret_cast<const float2 *>(at);
-                    const float2 u = *reinterpret_cast<const float2 *>(at + 64);
-                    a[i * 2] += g.x, a[i * 2 + 1] += g.y;
-                    b[i * 2] += u.x, b[i * 2 + 1] += u.y;
-                } else {
-                    const float4 f = *reinterpret_cast<const float4 *>(at);
-                    a[i * 4] += f.x, a[i * 4 + 1] += f.y, a[i * 4 + 2] += f.z, a[i * 4 + 3] += f.w;
+                    const float4 g = *reinterpret_cast<const float4 *>(at + 64 * 16);
+                    b[i * 4] += g.x, b[i * 4 + 1] += g.y, b[i * 4 + 2] += g.z, b[i * 4 + 3] += g.w;
                 }
             }
 #pragma unroll
-        for (int i = 0; i < kAtOnce * kOuts; ++i) a[i] += bias[i % kOuts];
+        for (int i = 0; i < kAtOnce * 4; ++i) a[i] += bias[kPair ? 0 : i / 4 & 1];
         activate<kF32>(p.act, a);
         if (kPair)
 #pragma unroll
-            for (int i = 0; i < kAtOnce * kOuts; ++i)
-                a[i] *= b[kPair ? i : 0] + bias2[i % kOuts];
+            for (int i = 0; i < kAtOnce * 4; ++i) a[i] *= b[kPair ? i : 0] + bias2[0];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const int j = r + i * kLinWarps;
-            if (j >= mm || c >= p.n) continue;
-            if (!kPair)
+            const int v = u + i * kLinWarps;
+            if (v >= units) break;
 #pragma unroll
-                for (int o = 0; o < kOuts; ++o) a[i * kOuts + o] += res[i][o];
-            store_outs<kPair, kF32, kOuts>(p, (size_t)row0 + mine0 + j, c, a + i * kOuts);
+            for (int h = 0; h < 2; ++h) {
+                const float other = __shfl_xor_sync(kFull, odd ? a[4 * i + h] : a[4 * i + 2 + h], 1);
+                float lo = odd ? other : a[4 * i + h], hi = odd ? a[4 * i + 2 + h] : other;
+                if (!kPair) {
+                    lo += bf16_lo(res[kPair ? 0 : i][h]);
+                    hi += bf16_hi(res[kPair ? 0 : i][h]);
+                }
+                const int r = v / kAcross * 4 + 2 * odd + h;
+                if (r < mm)
+                    store_two<kF32>(p, (size_t)row0 + mine0 + r, c0 + v % kAcross * 32 + (lane & 30),
+                                    lo, hi);
+            }
         }
-        residual(r + kAtOnce * kLinWarps);
+        residual(u + kAtOnce * kLinWarps);
     }
 }
 
@@ -352,7 +358,7 @@ static cudaError_t launch_few(const Linear &p, const LinearPlan &plan, cudaStrea
     cfg.gridDim = dim3((unsigned)((p.rows + NR - 1) / NR), (unsigned)((p.n + outs - 1) / outs),
                        (unsigned)plan.parts);
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = (size_t)lin_smem(NR, plan.stages);
+    cfg.dynamicSmemBytes = (size_t)lin_smem(NR, plan.parts, plan.stages);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;

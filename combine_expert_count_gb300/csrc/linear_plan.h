@@ -17,6 +17,7 @@ struct LinearPlan {
 
 constexpr int kLinearBlock = 64;  // elements of k in 128 bytes
 constexpr int kSmem = 232448;  // a CTA's, which has an SM for itself
+constexpr int kLinearApart = 64;  // rows of a CTA up to which sums have room beside the ring
 
 // What the kernels take, in ns, from what was measured of them: SMs take in 14.5 MB/us
 // together at most (kFabric) and one 150 KB/us.
@@ -85,7 +86,9 @@ inline LinearPlan linear_plan(int64_t rows, int64_t n, int64_t k, bool pair, boo
                 take(tile_cost(width, 2, tiles, blocks, f32, sms), width, 0, 2);
         }
     if (best.width) return best;
-    const int apart = best.at <= 32 ? best.at * 512 : 0, stage = 2 * (16384 + best.at * 128);
+    const int rows_of = best.at / best.parts < 4 ? 4 : best.at / best.parts;
+    const int apart = best.at <= kLinearApart ? best.parts * rows_of * 512 : 0;
+    const int stage = 2 * (16384 + best.at * 128);
     const int64_t mine = (stages + best.parts - 1) / best.parts;
     best.stages = (kSmem - 1280 - apart) / stage;
     if (best.stages > 6) best.stages = 6;

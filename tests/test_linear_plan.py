@@ -44,7 +44,8 @@ def test_what_it_chooses_is_possible():
         assert p.parts in (1, 2, 4, 8) and p.parts <= stages
         tiles = -(-n // (64 if pair else 128)) * -(-rows // p.at)
         assert p.parts == 1 or tiles * p.parts <= sms
-        stage, apart = 2 * (16384 + p.at * 128), p.at * 512 if p.at <= 32 else 0
+        stage = 2 * (16384 + p.at * 128)
+        apart = max(p.at, 4 * p.parts) * 512 if p.at <= 64 else 0
         assert 1 <= p.stages <= 6 and 1280 + apart + p.stages * stage <= SMEM
         assert apart or p.stages * stage >= p.at * 512
         # an SM's 512 columns of tensor memory last for the CTAs that its shared memory holds
