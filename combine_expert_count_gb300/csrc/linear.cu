@@ -19,7 +19,7 @@ namespace moe {
 // it holds: with a block a stage a CTA took no more than 108 GB/s.)  The
 // CTAs of a cluster share k and then the rows: each sends its sums of a row to the part
 // that adds them up and stores the row.
-constexpr int kLinTma = 4, kLinMma = 5, kLinWarps = 6, kLinThreads = 32 * kLinWarps;
+constexpr int kLinTma = 4, kLinMma = 5, kLinWarps = 8, kLinThreads = 32 * kLinWarps;
 constexpr int kLinTile = 128 * 128;  // bytes of a weight tile of a block of k
 constexpr int kLinRun = 4;           // stages between the sums of an fp32 result: 512 of k
 constexpr int kLinMostStages = 6;
@@ -49,33 +49,31 @@ __host__ __device__ constexpr int lin_smem(int NR, int parts, int stages) {
     return kLinHead + 1024 + lin_apart(NR, parts) + stages * lin_stage(NR);
 }
 
-// Two outputs of a row, c and c + 1 of p.n, or as many as there are.
+// Two neighbouring outputs of a row, `at` elements into y, of which `there` are there.
 template <bool kF32>
-__device__ __forceinline__ void store_two(const Linear &p, size_t row, int c, float a, float b) {
-    const size_t to = row * p.n + c;
+__device__ __forceinline__ void store_two(const Linear &p, size_t at, int there, float a, float b) {
     if ((p.n & 1) == 0) {
-        if (c >= p.n) return;
+        if (there < 2) return;
         if (kF32)
-            *reinterpret_cast<float2 *>(p.yf + to) = make_float2(a, b);
+            *reinterpret_cast<float2 *>(p.yf + at) = make_float2(a, b);
         else
-            *reinterpret_cast<uint32_t *>(p.y + to) = pack_bf16x2(a, b);
+            *reinterpret_cast<uint32_t *>(p.y + at) = pack_bf16x2(a, b);
         return;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (c + i >= p.n) break;
+        if (i >= there) break;
         if (kF32)
-            p.yf[to + i] = i ? b : a;
+            p.yf[at + i] = i ? b : a;
         else
-            p.y[to + i] = (uint16_t)pack_bf16x2(i ? b : a, 0.0f);
+            p.y[at + i] = (uint16_t)pack_bf16x2(i ? b : a, 0.0f);
     }
 }
 
 // The residual of the same two, 0 where there is none.
-__device__ __forceinline__ uint32_t load_two(const Linear &p, size_t row, int c) {
-    const uint16_t *from = p.res + row * p.n + c;
-    if ((p.n & 1) == 0) return c < p.n ? *reinterpret_cast<const uint32_t *>(from) : 0u;
-    return (c < p.n ? from[0] : 0u) | (c + 1 < p.n ? (uint32_t)from[1] << 16 : 0u);
+__device__ __forceinline__ uint32_t load_two(const Linear &p, size_t at, int there) {
+    if ((p.n & 1) == 0) return there == 2 ? *reinterpret_cast<const uint32_t *>(p.res + at) : 0u;
+    return (there > 0 ? p.res[at] : 0u) | (there > 1 ? (uint32_t)p.res[at + 1] << 16 : 0u);
 }
 
 template <int NR, bool kPair, bool kF32>
@@ -163,6 +161,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (last) tc_commit(&s.tfull[ac], one);
             if (++st == stages) st = 0, phase ^= 1;
         }
+    } else if (warp > kLinMma) {
+        // these only help with the outputs
     } else if constexpr (kF32) {
         const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
         const int runs = (b1 - b0 + kLinRun - 1) / kLinRun;
@@ -187,40 +187,33 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
 
     // ---------------------------------------------------------------- the sums to their rows' parts
-    // A unit is four rows of 32 outputs, an output a lane; after their activation two
-    // lanes exchange, so that one has two outputs of the first two rows.
-    constexpr int kAcross = kPair ? 2 : 4;         // units side by side
+    // A warp has 32 outputs of every kStep-th group of four rows, an output a lane; after
+    // their activation two lanes exchange, so that one has two outputs of the first two rows.
+    constexpr int kAcross = kPair ? 2 : 4, kStep = kLinWarps / kAcross;
     const int LR = lin_rows(NR, parts), shift = __ffs(LR) - 1;  // rows of a part
-    const int mine0 = part * LR;                                 // this one's first
-    const int mm = min(m - mine0, LR);                           // as many as there are
-    const int units = (mm + 3) / 4 * kAcross;
-    const int odd = lane & 1;
-    // what the outputs take beside their sums is asked for before those are there; the
-    // bias of a warp's units, which are kLinWarps apart, is of two places at most
-    float bias[2] = {}, bias2[2] = {};
-    if (p.bias)
-#pragma unroll
-        for (int i = 0; i < (kPair ? 1 : 2); ++i) {
-            const int c = c0 + (warp + i * kLinWarps) % kAcross * 32 + lane;
-            if (c < p.n) {
-                bias[i] = bf16_lo(p.bias[c]);
-                if (kPair) bias2[i] = bf16_lo(p.bias[p.n + c]);
-            }
-        }
+    const int mm = min(m - part * LR, LR);                      // as many as there are
+    const int across = warp % kAcross * 32 + lane, g0 = warp / kAcross;
+    const int r0 = g0 * 4 + 2 * (lane & 1), there = p.n - (c0 + (across & ~1));
+    const int two = there < 0 ? 0 : min(there, 2);
+    const size_t y0 = ((size_t)row0 + part * LR + r0) * p.n + c0 + (across & ~1);
+    // what the outputs take beside their sums is asked for before those are there
+    float bias = 0.0f, bias2 = 0.0f;
+    if (p.bias && c0 + across < p.n) {
+        bias = bf16_lo(p.bias[c0 + across]);
+        if (kPair) bias2 = bf16_lo(p.bias[p.n + c0 + across]);
+    }
     uint32_t res[kPair ? 1 : kAtOnce][2] = {};
-    const auto residual = [&](int u) {  // of units u, u + kLinWarps, ...
+    const auto residual = [&](int g) {  // of groups g0 + g, + kStep, ...
         if (!kPair && p.res)
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int v = u + i * kLinWarps, r = v / kAcross * 4 + 2 * odd + h;
-                    if (r < mm)
-                        res[kPair ? 0 : i][h] =
-                            load_two(p, (size_t)row0 + mine0 + r, c0 + v % kAcross * 32 + (lane & 30));
+                    const int r = (g + i * kStep) * 4 + h;
+                    if (r0 + r < mm) res[kPair ? 0 : i][h] = load_two(p, y0 + (size_t)r * p.n, two);
                 }
     };
-    residual(warp);
+    residual(0);
     tc_fence_before();
     __syncthreads();
     if (s.stop) {  // a kernel that gave up leaves no copy and no product in flight
@@ -283,34 +276,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // ---------------------------------------------------------------- the outputs
     // where a part gave up the sums are not whole and no part stores any
     if (s.any || s.stop) return;
+    const uint8_t *sums = left + (g0 * 128 + across) * 16;
 #pragma unroll 1
-    for (int u = warp; u < units; u += kAtOnce * kLinWarps) {
+    for (int g = 0; (g0 + g) * 4 < mm; g += kAtOnce * kStep) {
         float a[kAtOnce * 4] = {}, b[kPair ? kAtOnce * 4 : 1] = {};
-        const auto place = [&](int q, int i) {
-            const int v = min(u + i * kLinWarps, units - 1);
-            return left + (q * LR * 32 + v / kAcross * 128 + v % kAcross * 32 + lane) * 16;
-        };
-        for (int q = 0; q < parts; ++q)  // in the parts' order
+        const uint8_t *at = sums + g * 2048;
+        for (int q = 0; q < parts; ++q, at += LR * 512)  // in the parts' order
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                const uint8_t *at = place(q, i);
-                const float4 f = *reinterpret_cast<const float4 *>(at);
+                if ((g0 + g + i * kStep) * 4 >= mm) break;
+                const float4 f = *reinterpret_cast<const float4 *>(at + i * kStep * 2048);
                 a[i * 4] += f.x, a[i * 4 + 1] += f.y, a[i * 4 + 2] += f.z, a[i * 4 + 3] += f.w;
                 if constexpr (kPair) {
-                    const float4 g = *reinterpret_cast<const float4 *>(at + 64 * 16);
-                    b[i * 4] += g.x, b[i * 4 + 1] += g.y, b[i * 4 + 2] += g.z, b[i * 4 + 3] += g.w;
+                    const float4 e = *reinterpret_cast<const float4 *>(at + i * kStep * 2048 + 64 * 16);
+                    b[i * 4] += e.x, b[i * 4 + 1] += e.y, b[i * 4 + 2] += e.z, b[i * 4 + 3] += e.w;
                 }
             }
 #pragma unroll
-        for (int i = 0; i < kAtOnce * 4; ++i) a[i] += bias[kPair ? 0 : i / 4 & 1];
+        for (int i = 0; i < kAtOnce * 4; ++i) a[i] += bias;
         activate<kF32>(p.act, a);
         if (kPair)
 #pragma unroll
-            for (int i = 0; i < kAtOnce * 4; ++i) a[i] *= b[kPair ? i : 0] + bias2[0];
+            for (int i = 0; i < kAtOnce * 4; ++i) a[i] *= b[kPair ? i : 0] + bias2;
+        const bool odd = lane & 1;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const int v = u + i * kLinWarps;
-            if (v >= units) break;
+            if ((g0 + g + i * kStep) * 4 >= mm) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float other = __shfl_xor_sync(kFull, odd ? a[4 * i + h] : a[4 * i + 2 + h], 1);
@@ -319,13 +310,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     lo += bf16_lo(res[kPair ? 0 : i][h]);
                     hi += bf16_hi(res[kPair ? 0 : i][h]);
                 }
-                const int r = v / kAcross * 4 + 2 * odd + h;
-                if (r < mm)
-                    store_two<kF32>(p, (size_t)row0 + mine0 + r, c0 + v % kAcross * 32 + (lane & 30),
-                                    lo, hi);
+                const int r = (g + i * kStep) * 4 + h;
+                if (r0 + r < mm) store_two<kF32>(p, y0 + (size_t)r * p.n, two, lo, hi);
             }
         }
-        residual(u + kAtOnce * kLinWarps);
+        residual(g + kAtOnce * kStep);
     }
 }
 
