@@ -23,7 +23,6 @@ constexpr int kLinTma = 4, kLinMma = 5, kLinWarps = 8, kLinThreads = 32 * kLinWa
 constexpr int kLinTile = 128 * 128;  // bytes of a weight tile of a block of k
 constexpr int kLinRun = 4;           // stages between the sums of an fp32 result: 512 of k
 constexpr int kLinMostStages = 6;
-constexpr int kAtOnce = 4;           // units that a warp finishes together
 
 struct LinShared {
     uint64_t full[kLinMostStages], empty[kLinMostStages], tfull[2], tempty[2], drain;
@@ -49,30 +48,33 @@ __host__ __device__ constexpr int lin_smem(int NR, int parts, int stages) {
     return kLinHead + 1024 + lin_apart(NR, parts) + stages * lin_stage(NR);
 }
 
-// Two neighbouring outputs of a row, `at` elements into y, of which `there` are there.
-template <bool kF32>
+template <bool b>
+struct Flag {
+    static constexpr bool value = b;
+};
+
+// Two neighbouring outputs of a row, `at` elements into y; kTwo: they are pairs (an even
+// number of outputs), else `there` of them are there.
+template <bool kF32, bool kTwo>
 __device__ __forceinline__ void store_two(const Linear &p, size_t at, int there, float a, float b) {
-    if ((p.n & 1) == 0) {
-        if (there < 2) return;
-        if (kF32)
-            *reinterpret_cast<float2 *>(p.yf + at) = make_float2(a, b);
-        else
-            *reinterpret_cast<uint32_t *>(p.y + at) = pack_bf16x2(a, b);
-        return;
-    }
+    if (kTwo && kF32)
+        *reinterpret_cast<float2 *>(p.yf + at) = make_float2(a, b);
+    else if (kTwo)
+        *reinterpret_cast<uint32_t *>(p.y + at) = pack_bf16x2(a, b);
+    else
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (i >= there) break;
-        if (kF32)
-            p.yf[at + i] = i ? b : a;
-        else
-            p.y[at + i] = (uint16_t)pack_bf16x2(i ? b : a, 0.0f);
-    }
+        for (int i = 0; i < 2; ++i) {
+            if (i >= there) break;
+            if (kF32)
+                p.yf[at + i] = i ? b : a;
+            else
+                p.y[at + i] = (uint16_t)pack_bf16x2(i ? b : a, 0.0f);
+        }
 }
 
 // The residual of the same two, 0 where there is none.
 __device__ __forceinline__ uint32_t load_two(const Linear &p, size_t at, int there) {
-    if ((p.n & 1) == 0) return there == 2 ? *reinterpret_cast<const uint32_t *>(p.res + at) : 0u;
+    if ((p.n & 1) == 0) return there > 0 ? *reinterpret_cast<const uint32_t *>(p.res + at) : 0u;
     return (there > 0 ? p.res[at] : 0u) | (there > 1 ? (uint32_t)p.res[at + 1] << 16 : 0u);
 }
 
@@ -190,11 +192,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // A warp has 32 outputs of every kStep-th group of four rows, an output a lane; after
     // their activation two lanes exchange, so that one has two outputs of the first two rows.
     constexpr int kAcross = kPair ? 2 : 4, kStep = kLinWarps / kAcross;
+    constexpr int kMany = NR / (kPair ? 32 : 16), kAtOnce = kMany < 1 ? 1 : kMany > 4 ? 4 : kMany;
     const int LR = lin_rows(NR, parts), shift = __ffs(LR) - 1;  // rows of a part
     const int mm = min(m - part * LR, LR);                      // as many as there are
     const int across = warp % kAcross * 32 + lane, g0 = warp / kAcross;
     const int r0 = g0 * 4 + 2 * (lane & 1), there = p.n - (c0 + (across & ~1));
-    const int two = there < 0 ? 0 : min(there, 2);
+    const bool even = (p.n & 1) == 0;
     const size_t y0 = ((size_t)row0 + part * LR + r0) * p.n + c0 + (across & ~1);
     // what the outputs take beside their sums is asked for before those are there
     float bias = 0.0f, bias2 = 0.0f;
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = (g + i * kStep) * 4 + h;
-                    if (r0 + r < mm) res[kPair ? 0 : i][h] = load_two(p, y0 + (size_t)r * p.n, two);
+                    if (r0 + r < mm) res[kPair ? 0 : i][h] = load_two(p, y0 + (size_t)r * p.n, there);
                 }
     };
     residual(0);
@@ -276,19 +279,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // ---------------------------------------------------------------- the outputs
     // where a part gave up the sums are not whole and no part stores any
     if (s.any || s.stop) return;
-    const uint8_t *sums = left + (g0 * 128 + across) * 16;
+    const uint8_t *sums = left + across * 16;
 #pragma unroll 1
     for (int g = 0; (g0 + g) * 4 < mm; g += kAtOnce * kStep) {
         float a[kAtOnce * 4] = {}, b[kPair ? kAtOnce * 4 : 1] = {};
-        const uint8_t *at = sums + g * 2048;
-        for (int q = 0; q < parts; ++q, at += LR * 512)  // in the parts' order
+        int at[kAtOnce];  // (one group is taken again where there are no more)
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) at[i] = min(g0 + g + i * kStep, LR / 4 - 1) * 2048;
+        const uint8_t *from = sums;
+        for (int q = 0; q < parts; ++q, from += LR * 512)  // in the parts' order
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                if ((g0 + g + i * kStep) * 4 >= mm) break;
-                const float4 f = *reinterpret_cast<const float4 *>(at + i * kStep * 2048);
+                const float4 f = *reinterpret_cast<const float4 *>(from + at[i]);
                 a[i * 4] += f.x, a[i * 4 + 1] += f.y, a[i * 4 + 2] += f.z, a[i * 4 + 3] += f.w;
                 if constexpr (kPair) {
-                    const float4 e = *reinterpret_cast<const float4 *>(at + i * kStep * 2048 + 64 * 16);
+                    const float4 e = *reinterpret_cast<const float4 *>(from + at[i] + 64 * 16);
                     b[i * 4] += e.x, b[i * 4 + 1] += e.y, b[i * 4 + 2] += e.z, b[i * 4 + 3] += e.w;
                 }
             }
@@ -299,21 +304,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
             for (int i = 0; i < kAtOnce * 4; ++i) a[i] *= b[kPair ? i : 0] + bias2;
         const bool odd = lane & 1;
+        float lo[kAtOnce][2], hi[kAtOnce][2];
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            if ((g0 + g + i * kStep) * 4 >= mm) break;
+        for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float other = __shfl_xor_sync(kFull, odd ? a[4 * i + h] : a[4 * i + 2 + h], 1);
-                float lo = odd ? other : a[4 * i + h], hi = odd ? a[4 * i + 2 + h] : other;
+                lo[i][h] = odd ? other : a[4 * i + h];
+                hi[i][h] = odd ? a[4 * i + 2 + h] : other;
                 if (!kPair) {
-                    lo += bf16_lo(res[kPair ? 0 : i][h]);
-                    hi += bf16_hi(res[kPair ? 0 : i][h]);
+                    lo[i][h] += bf16_lo(res[kPair ? 0 : i][h]);
+                    hi[i][h] += bf16_hi(res[kPair ? 0 : i][h]);
                 }
-                const int r = (g + i * kStep) * 4 + h;
-                if (r0 + r < mm) store_two<kF32>(p, y0 + (size_t)r * p.n, two, lo, hi);
             }
-        }
+        const auto store = [&](auto pairs) {
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (r0 + (g + i * kStep) * 4 + h < mm)
+                        store_two<kF32, pairs.value>(p, y0 + (size_t)((g + i * kStep) * 4 + h) * p.n,
+                                                     there, lo[i][h], hi[i][h]);
+        };
+        if (!even)
+            store(Flag<false>{});
+        else if (there > 0)
+            store(Flag<true>{});
         residual(g + kAtOnce * kStep);
     }
 }
