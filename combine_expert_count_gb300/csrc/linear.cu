@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // A warp has 32 outputs of every kStep-th group of four rows, an output a lane; after
     // their activation two lanes exchange, so that one has two outputs of the first two rows.
     constexpr int kAcross = kPair ? 2 : 4, kStep = kLinWarps / kAcross;
-    constexpr int kMany = NR / (kPair ? 32 : 16), kAtOnce = kMany < 1 ? 1 : kMany > 4 ? 4 : kMany;
+    constexpr int kMany = NR / (kPair ? 32 : 8), kAtOnce = kMany < 1 ? 1 : kMany > 4 ? 4 : kMany;
     const int LR = lin_rows(NR, parts), shift = __ffs(LR) - 1;  // rows of a part
     const int mm = min(m - part * LR, LR);                      // as many as there are
     const int across = warp % kAcross * 32 + lane, g0 = warp / kAcross;
@@ -236,9 +236,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!kApart) cluster_sync();  // all parts are done with their rings
         if (s.stop && tid < parts) st_dsmem(dsmem_addr(&s.any, tid), 1);
     }
-    if (warp < 4 && !s.stop) {
-        const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
-        uint8_t *const to = left + part * LR * 512 + tid * 16;
+    constexpr bool kAll = NR == 128 && !kF32;  // eight warps take the sums out
+    if ((warp < 4 || kAll) && !s.stop) {
+        const uint32_t mine = tmem + ((uint32_t)(warp & 3) * 32 << 16);
+        uint8_t *const to = left + part * LR * 512 + (tid & 127) * 16;
         // rows j .. j + 3 to their part
         const auto leave = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
             if (j >= m) return;
@@ -254,14 +255,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 leave(j, __float_as_uint(acc[kF32 ? j : 0]), __float_as_uint(acc[kF32 ? j + 1 : 0]),
                       __float_as_uint(acc[kF32 ? j + 2 : 0]), __float_as_uint(acc[kF32 ? j + 3 : 0]));
         } else {
+            constexpr int kSets = NR < 32 ? 1 : 2;  // of 16 rows
 #pragma unroll 1
-            for (int j = 0; j < m; j += NR < 32 ? 16 : 32) {
-                uint32_t v[NR < 32 ? 1 : 2][16];
+            for (int j = (warp >> 2) * 32; j < m; j += 16 * kSets * (kAll ? 2 : 1)) {
+                uint32_t v[kSets][16];
 #pragma unroll
-                for (int h = 0; h < (NR < 32 ? 1 : 2); ++h) tc_ld16(v[h], mine + j + 16 * h);
+                for (int h = 0; h < kSets; ++h) tc_ld16(v[h], mine + j + 16 * h);
                 tc_wait_ld();
 #pragma unroll
-                for (int h = 0; h < (NR < 32 ? 1 : 2); ++h)
+                for (int h = 0; h < kSets; ++h)
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
                         leave(j + 16 * h + i, v[h][i], v[h][i + 1], v[h][i + 2], v[h][i + 3]);
