@@ -19,6 +19,8 @@ struct Linear {
 
 // pair: gate and up halves of w.
 cudaError_t launch_linear_tiles(const Linear &p, bool pair, const LinearPlan &plan, cudaStream_t st);
+cudaError_t launch_linear_ragged(const Linear &p, bool pair, const LinearPlan &plan,
+                                 cudaStream_t st);
 cudaError_t launch_linear(const Linear &p, bool pair, cudaStream_t st);
 
 }  // namespace moe
