@@ -48,36 +48,6 @@ __host__ __device__ constexpr int lin_smem(int NR, int parts, int stages) {
     return kLinHead + 1024 + lin_apart(NR, parts) + stages * lin_stage(NR);
 }
 
-template <bool b>
-struct Flag {
-    static constexpr bool value = b;
-};
-
-// Two neighbouring outputs of a row, `at` elements into y; kTwo: they are pairs (an even
-// number of outputs), else `there` of them are there.
-template <bool kF32, bool kTwo>
-__device__ __forceinline__ void store_two(const Linear &p, size_t at, int there, float a, float b) {
-    if (kTwo && kF32)
-        *reinterpret_cast<float2 *>(p.yf + at) = make_float2(a, b);
-    else if (kTwo)
-        *reinterpret_cast<uint32_t *>(p.y + at) = pack_bf16x2(a, b);
-    else
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i >= there) break;
-            if (kF32)
-                p.yf[at + i] = i ? b : a;
-            else
-                p.y[at + i] = (uint16_t)pack_bf16x2(i ? b : a, 0.0f);
-        }
-}
-
-// The residual of the same two, 0 where there is none.
-__device__ __forceinline__ uint32_t load_two(const Linear &p, size_t at, int there) {
-    if ((p.n & 1) == 0) return there > 0 ? *reinterpret_cast<const uint32_t *>(p.res + at) : 0u;
-    return (there > 0 ? p.res[at] : 0u) | (there > 1 ? (uint32_t)p.res[at + 1] << 16 : 0u);
-}
-
 template <int NR, bool kPair, bool kF32>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear(const __grid_constant__ Linear p, int stages, const __grid_constant__ CUtensorMap map_x,
@@ -190,15 +160,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
     // ---------------------------------------------------------------- the sums to their rows' parts
     // A warp has 32 outputs of every kStep-th group of four rows, an output a lane; after
-    // their activation two lanes exchange, so that one has two outputs of the first two rows.
+    // their activation two lanes exchange, so that one has two outputs of the first two
+    // rows (unless their number is odd).
     constexpr int kAcross = kPair ? 2 : 4, kStep = kLinWarps / kAcross;
     constexpr int kMany = NR / (kPair ? 32 : 8), kAtOnce = kMany < 1 ? 1 : kMany > 4 ? 4 : kMany;
     const int LR = lin_rows(NR, parts), shift = __ffs(LR) - 1;  // rows of a part
     const int mm = min(m - part * LR, LR);                      // as many as there are
     const int across = warp % kAcross * 32 + lane, g0 = warp / kAcross;
-    const int r0 = g0 * 4 + 2 * (lane & 1), there = p.n - (c0 + (across & ~1));
     const bool even = (p.n & 1) == 0;
-    const size_t y0 = ((size_t)row0 + part * LR + r0) * p.n + c0 + (across & ~1);
+    const int col = c0 + (even ? across & ~1 : across), r0 = g0 * 4 + (even ? 2 * (lane & 1) : 0);
+    const size_t y0 = ((size_t)row0 + part * LR + r0) * p.n + col;
     // what the outputs take beside their sums is asked for before those are there
     float bias = 0.0f, bias2 = 0.0f;
     if (p.bias && c0 + across < p.n) {
@@ -212,8 +183,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int r = (g + i * kStep) * 4 + h;
-                    if (r0 + r < mm) res[kPair ? 0 : i][h] = load_two(p, y0 + (size_t)r * p.n, there);
+                    const int r = (g + i * kStep) * 4 + (even ? h : 2 * h);
+                    const uint16_t *from = p.res + y0 + (size_t)r * p.n;
+                    uint32_t &to = res[kPair ? 0 : i][h];
+                    if (r0 + r >= mm || col >= p.n) continue;
+                    if (even) {
+                        to = *reinterpret_cast<const uint32_t *>(from);
+                    } else {
+                        to = from[0];
+                        if (r0 + r + 1 < mm) to |= (uint32_t)from[p.n] << 16;
+                    }
                 }
     };
     residual(0);
@@ -306,32 +285,53 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
             for (int i = 0; i < kAtOnce * 4; ++i) a[i] *= b[kPair ? i : 0] + bias2;
         const bool odd = lane & 1;
-        float lo[kAtOnce][2], hi[kAtOnce][2];
+        float v[kAtOnce][2][2];  // of two rows two outputs, or of four rows one
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float other = __shfl_xor_sync(kFull, odd ? a[4 * i + h] : a[4 * i + 2 + h], 1);
-                lo[i][h] = odd ? other : a[4 * i + h];
-                hi[i][h] = odd ? a[4 * i + 2 + h] : other;
+                if (even) {
+                    const float other =
+                        __shfl_xor_sync(kFull, odd ? a[4 * i + h] : a[4 * i + 2 + h], 1);
+                    v[i][h][0] = odd ? other : a[4 * i + h];
+                    v[i][h][1] = odd ? a[4 * i + 2 + h] : other;
+                } else {
+                    v[i][h][0] = a[4 * i + 2 * h];
+                    v[i][h][1] = a[4 * i + 2 * h + 1];
+                }
                 if (!kPair) {
-                    lo[i][h] += bf16_lo(res[kPair ? 0 : i][h]);
-                    hi[i][h] += bf16_hi(res[kPair ? 0 : i][h]);
+                    v[i][h][0] += bf16_lo(res[kPair ? 0 : i][h]);
+                    v[i][h][1] += bf16_hi(res[kPair ? 0 : i][h]);
                 }
             }
-        const auto store = [&](auto pairs) {
+        if (col < p.n && even) {
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (r0 + (g + i * kStep) * 4 + h < mm)
-                        store_two<kF32, pairs.value>(p, y0 + (size_t)((g + i * kStep) * 4 + h) * p.n,
-                                                     there, lo[i][h], hi[i][h]);
-        };
-        if (!even)
-            store(Flag<false>{});
-        else if (there > 0)
-            store(Flag<true>{});
+                for (int h = 0; h < 2; ++h) {
+                    const int r = (g + i * kStep) * 4 + h;
+                    const size_t to = y0 + (size_t)r * p.n;
+                    if (r0 + r >= mm) continue;
+                    if (kF32)
+                        *reinterpret_cast<float2 *>(p.yf + to) = make_float2(v[i][h][0], v[i][h][1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(p.y + to) =
+                            pack_bf16x2(v[i][h][0], v[i][h][1]);
+                }
+        } else if (col < p.n) {
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int r = (g + i * kStep) * 4 + h;
+                    const size_t to = y0 + (size_t)r * p.n;
+                    if (r0 + r >= mm) continue;
+                    if (kF32)
+                        p.yf[to] = v[i][h / 2][h % 2];
+                    else
+                        p.y[to] = (uint16_t)pack_bf16x2(v[i][h / 2][h % 2], 0.0f);
+                }
+        }
         residual(g + kAtOnce * kStep);
     }
 }

@@ -3,6 +3,7 @@
 // ask it.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 namespace moe {
@@ -11,7 +12,7 @@ namespace moe {
 struct LinearPlan {
     int width;   // > 0: pairs of CTAs, tiles of 256 rows by so many weight rows
     int at;      // else: rows of a CTA
-    int parts;   // CTAs (pairs) of a cluster that share its k
+    int parts;   // CTAs of a cluster that share its k, where width is 0
     int stages;  // of a CTA's ring, where width is 0
 };
 
@@ -19,41 +20,45 @@ constexpr int kLinearBlock = 64;  // elements of k in 128 bytes
 constexpr int kSmem = 232448;  // a CTA's, which has an SM for itself
 constexpr int kLinearApart = 64;  // rows of a CTA up to which sums have room beside the ring
 
-// What the kernels take, in ns, from what was measured of them: SMs take in 14.5 MB/us
-// together at most (kFabric) and one 150 KB/us.
-//   Few rows: 2.6 us and 22 ns a row that a CTA has, 0.3 us for sums that cross the
-//   cluster (and 15 ns a row beyond 32, which wait for the ring), and the bytes of a CTA's
-//   stages.
-//   Tiles: 4.5 us and 13 ns an output of the tile, and for each block of 64 along k what
-//   its products take (1.06 ns an output; fp32 results, whose sums are taken out on the
-//   way, a quarter more), 170 ns at least, or its bytes.
-// us estimated and measured: 61 rows of gate/up of 768 by 2048 5.3 and 5.9; 64 x 256 x 7168
-// 5.3 and 5.4; 2048 x 256 x 7168 in fp32 14.6 and 15.7; 200 x 2048 x 2048 11.2 and 10.4; 768 x
-// 7168 x 7168 62 and 61; 2048 x 7168 x 7168 120 and 126.  Of 47
-// sizes, each measured in every way, the choice is within 13% of the best.
-constexpr double kFabric = 14500.0;
-
-inline double few_cost(int at, int parts, int64_t tiles, int64_t stages, int sms) {
+// What the kernels take, in ns, fitted to 1300 measured times of 176 sizes, each of which
+// went every way (an eighth off as a rule); what is chosen is 2% slower than the fastest
+// way on average, 30% at most.
+//   Few rows: 2.5 us and 22 ns a row that a CTA has (24 with fp32 results), 0.5 us for sums
+//   that cross the cluster; the bytes of a CTA's stages at 153 KB/us, or 0.2 us a stage, in
+//   quadrature with the operands at 7.7 MB/us; for each further round of CTAs 2.6 us and 4
+//   ns a row.
+//   Tiles: 2.8 us and 15.6 ns an output of the tile; for each block of 64 along k what its
+//   products take (1.07 ns an output; with fp32 results 4% more), 0.22 us at least, or its
+//   bytes at the pair's share of 15 MB/us; a further tile of the pair's no less than storing
+//   one does (1.9 us and 12.4 ns an output).  Rows of outputs that do not start on 16 bytes
+//   are stored in 1.28 times as long, of an odd number in 1.9 times.
+// us estimated and measured: 61 rows of gate/up of 768 by 2048 5.0 and 5.0; 64 x 256 x 7168
+// 4.8 and 5.2; 2048 x 256 x 7168 in fp32 14.1 and 14.3; 200 x 2048 x 2048 7.0 and 6.9; 509 x
+// 7168 x 7168 39.8 and 40.4; 8191 x 7168 x 7168 520 and 484.
+inline double few_cost(int at, int parts, int64_t tiles, int64_t stages, double bytes, bool f32,
+                       int sms) {
     const int64_t ctas = tiles * parts;
-    const double active = (double)(ctas < sms ? ctas : sms);
-    const double rate = kFabric / active < 150.0 ? kFabric / active : 150.0;
-    const double waves = (double)((ctas + sms - 1) / sms);
-    return 2600.0 + 22.0 * at + (parts == 1 ? 0.0 : at <= 32 ? 300.0 : 300.0 + 15.0 * at) +
-           waves * (double)((stages + parts - 1) / parts) * (32768.0 + 256.0 * at) / rate;
+    const double waves = (double)((ctas + sms - 1) / sms), fed = (32768.0 + 256.0 * at) / 153.0;
+    const double loop =
+        waves * (double)((stages + parts - 1) / parts) * (fed > 200.0 ? fed : 200.0);
+    const double hbm = bytes / 7700.0;
+    return 2500.0 + (f32 ? 24.0 : 22.0) * at + (parts == 1 ? 0.0 : 500.0) +
+           std::sqrt(loop * loop + hbm * hbm) + (waves - 1.0) * (2600.0 + 4.0 * at);
 }
 
-inline double tile_block_ns(int width, double pairs, bool f32) {
-    const double fed = (16384.0 + 64.0 * width) * 2.0 * pairs / kFabric;
-    const double done = 1.06 * width > 170.0 ? 1.06 * width : 170.0;
-    return (fed > done ? fed : done) * (f32 ? 1.25 : 1.0);
-}
-
-inline double tile_cost(int width, int parts, int64_t tiles, int64_t blocks, bool f32, int sms) {
-    const int64_t room = sms / 2, units = tiles * parts, full = units / room, rest = units % room;
-    const double per = (double)((blocks + parts - 1) / parts);
-    return 4500.0 + 13.0 * width + (parts > 1 ? 1500.0 : 0.0) +
-           full * per * tile_block_ns(width, (double)room, f32) +
-           (rest ? per * tile_block_ns(width, (double)rest, f32) : 0.0);
+inline double tile_cost(int width, int64_t n, int64_t tiles, int64_t blocks, bool f32, int sms) {
+    const int64_t room = sms / 2, full = tiles / room, rest = tiles % room;
+    const double stored = width * (n % 8 == 0 ? 1.0 : n % 2 == 0 ? 1.28 : 1.9);
+    const double next = 1900.0 + 12.4 * stored;
+    const auto loop = [&](int64_t pairs) {
+        const double fed = (16384.0 + 64.0 * width) * 2.0 * (double)pairs / 15000.0;
+        const double done = 1.07 * width > 220.0 ? 1.07 * width : 220.0;
+        return (double)blocks * (fed > done ? fed : done) * (f32 ? 1.04 : 1.0);
+    };
+    double cost = 2800.0 + 15.6 * stored;
+    if (full) cost += loop(room) + (double)(full - 1) * (loop(room) > next ? loop(room) : next);
+    if (rest) cost += full && loop(rest) < next ? next : loop(rest);
+    return cost;
 }
 
 // n: outputs (of each half, where there is a pair of them).
@@ -66,24 +71,23 @@ inline LinearPlan linear_plan(int64_t rows, int64_t n, int64_t k, bool pair, boo
         least = cost;
         best = {width, at, parts, 0};
     };
+    const double bytes = 2.0 * (double)k * (double)(rows + (pair ? 2 * n : n));
     const int64_t few_n = (n + (pair ? 63 : 127)) / (pair ? 64 : 128);
     for (int at = 16; at <= 128; at *= 2) {
         const int64_t tiles = few_n * ((rows + at - 1) / at);
-        take(few_cost(at, 1, tiles, stages, sms), 0, at, 1);
+        take(few_cost(at, 1, tiles, stages, bytes, f32, sms), 0, at, 1);
         // clusters that are on the SMs together: of four all but two of them, of eight all
         // but four (of 152 SMs in groups of 16 to 20)
         for (int parts = 2; parts <= 8; parts *= 2)
             if (parts <= stages && tiles * parts <= sms - (parts == 4 ? 8 : parts == 8 ? 32 : 0))
-                take(few_cost(at, parts, tiles, stages, sms), 0, at, parts);
+                take(few_cost(at, parts, tiles, stages, bytes, f32, sms), 0, at, parts);
         if (at >= rows) break;
     }
     if (rows > 128)
         for (int width = pair ? 64 : 32; width <= (f32 ? 128 : 256); width += pair ? 64 : 32) {
             const int64_t outs = pair ? width / 2 : width;
             const int64_t tiles = (n + outs - 1) / outs * ((rows + 255) / 256);
-            take(tile_cost(width, 1, tiles, blocks, f32, sms), width, 0, 1);
-            if (blocks >= 8 && 4 * tiles <= sms - 8)
-                take(tile_cost(width, 2, tiles, blocks, f32, sms), width, 0, 2);
+            take(tile_cost(width, n, tiles, blocks, f32, sms), width, 0, 1);
         }
     if (best.width) return best;
     const int rows_of = best.at / best.parts < 4 ? 4 : best.at / best.parts;

@@ -34,7 +34,7 @@ constexpr int kF32Width = 128;               // of its tiles at most: the sums s
 struct alignas(16) PairShared {
     uint64_t full[kPairStages], empty[kPairStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
-    int stop, any;  // this CTA gave up; one of the cluster's did
+    int stop;  // this CTA gave up
 };
 constexpr size_t kPairSmem =
     1024 + (size_t)kPairStages * kPairStageBytes + kOutWarps * (kOutStage + kResStage) + sizeof(PairShared);
@@ -131,9 +131,9 @@ __device__ __forceinline__ void widen(float (&v)[4], uint2 w) {
 
 // As finish, for any number of outputs that is a multiple of V: V of them a lane, four or
 // eight rows of a lane at a time.  (One row after another a tile of 256 x 256 took 11 us.)
-template <bool kPair, bool kF32, bool kSplit, int V, bool kRes>
+template <bool kPair, bool kF32, int V, bool kRes>
 __device__ __forceinline__ void finish_few(const Linear &p, uint8_t *stage, size_t row0, int rows,
-                                        int c, int end, int parts, int pitch) {
+                                        int c, int end) {
     constexpr int kLanes = chunk_outs(kPair) / V, kRows = 32 / kLanes;  // of a row; rows at a time
     constexpr int kMost = V == 4 ? 4 : 8;  // (of kLanes times altogether)
     static_assert(kLanes % kMost == 0, "whole rounds");
@@ -163,16 +163,14 @@ __device__ __forceinline__ void finish_few(const Linear &p, uint8_t *stage, size
         residual(s + kMost);
         const auto get = [&](float *to, int i, int from) {
             const uint8_t *place = staged(stage, row(s + i), from >> 2) + (from & 3) * 4;
-            for (int q = 0; q < (kSplit ? parts : 1); ++q, place += pitch) {
-                if constexpr (V == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(place);
-                    to[0] += f.x, to[1] += f.y, to[2] += f.z, to[3] += f.w;
-                } else if constexpr (V == 2) {
-                    const float2 f = *reinterpret_cast<const float2 *>(place);
-                    to[0] += f.x, to[1] += f.y;
-                } else {
-                    to[0] += *reinterpret_cast<const float *>(place);
-                }
+            if constexpr (V == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(place);
+                to[0] = f.x, to[1] = f.y, to[2] = f.z, to[3] = f.w;
+            } else if constexpr (V == 2) {
+                const float2 f = *reinterpret_cast<const float2 *>(place);
+                to[0] = f.x, to[1] = f.y;
+            } else {
+                to[0] = *reinterpret_cast<const float *>(place);
             }
         };
 #pragma unroll
@@ -213,12 +211,9 @@ __device__ __forceinline__ void finish_few(const Linear &p, uint8_t *stage, size
 
 // Finishes and stores the chunk of outputs c .. of the warp's rows row0 .., rows and
 // outputs (below end) as far as there are any.
-// kSplit: the sums are those of `parts` parts, `pitch` bytes from one part's to the
-// next's.
-template <bool kPair, bool kF32, bool kSplit, bool kWide>
+template <bool kPair, bool kF32, bool kWide>
 __device__ __forceinline__ void finish(const Linear &p, uint8_t *stage, const Beside<kPair, kWide> &by,
-                                       size_t row0, int rows, int c, int end, int chunk, int parts,
-                                       int pitch) {
+                                       size_t row0, int rows, int c, int end, int chunk) {
     constexpr int kOuts = chunk_outs(kPair), kLanes = kOuts / 8, kRows = 32 / kLanes;
     const int lane = threadIdx.x & 31;
     end = min(end, p.n);
@@ -229,12 +224,9 @@ __device__ __forceinline__ void finish(const Linear &p, uint8_t *stage, const Be
         const auto get = [&](float *to, int i, int from) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint8_t *at = staged(stage, i * kRows + lane / kLanes, from + h);
-                for (int q = 0; q < (kSplit ? parts : 1); ++q) {
-                    const float4 f = *reinterpret_cast<float4 *>(at + q * pitch);
-                    to[4 * h] += f.x, to[4 * h + 1] += f.y;
-                    to[4 * h + 2] += f.z, to[4 * h + 3] += f.w;
-                }
+                const float4 f =
+                    *reinterpret_cast<float4 *>(staged(stage, i * kRows + lane / kLanes, from + h));
+                to[4 * h] = f.x, to[4 * h + 1] = f.y, to[4 * h + 2] = f.z, to[4 * h + 3] = f.w;
             }
         };
         float w[8] = {};
@@ -280,9 +272,9 @@ __device__ __forceinline__ void finish(const Linear &p, uint8_t *stage, const Be
     // rows that do not all start on 16 bytes
     const auto few = [&](auto V) {
         if (!kPair && p.res)
-            finish_few<kPair, kF32, kSplit, V.value, !kPair>(p, stage, row0, rows, c, end, parts, pitch);
+            finish_few<kPair, kF32, V.value, !kPair>(p, stage, row0, rows, c, end);
         else
-            finish_few<kPair, kF32, kSplit, V.value, false>(p, stage, row0, rows, c, end, parts, pitch);
+            finish_few<kPair, kF32, V.value, false>(p, stage, row0, rows, c, end);
     };
     if ((p.n & 3) == 0)
         few(Number<4>{});
@@ -293,9 +285,8 @@ __device__ __forceinline__ void finish(const Linear &p, uint8_t *stage, const Be
 }
 
 // width: weight rows of a tile (both halves together), a multiple of 32, or of 64 for
-// kPair.  kSplit: the pairs of a cluster share the k of its one tile, and then its
-// outputs: each adds up and stores its own of them.
-template <bool kPair, bool kF32, bool kSplit, bool kWide>
+// kPair.
+template <bool kPair, bool kF32, bool kWide>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_linear_tiles(const __grid_constant__ Linear p, int width, int tiles_m, int tiles_n,
                    const __grid_constant__ CUtensorMap map_x,
@@ -309,12 +300,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         *reinterpret_cast<PairShared *>(staging + kOutWarps * (kOutStage + kResStage));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x & 1, pairs = gridDim.x >> 1;
-    const int parts = kSplit ? gridDim.z : 1, part = kSplit ? blockIdx.z : 0;
-    const int lead = 2 * part;  // the cluster's rank of the CTA that issues the pair's products
     const int tiles = tiles_m * tiles_n, outs = kPair ? width >> 1 : width;
     const int Kb = (p.k + kLinearBlock - 1) / kLinearBlock;
-    const int kb0 = kSplit ? (int)((long long)Kb * part / parts) : 0;
-    const int kb1 = kSplit ? (int)((long long)Kb * (part + 1) / parts) : Kb;
 
     if (tid == 0) {
         for (int i = 0; i < kPairStages; ++i) {
@@ -326,7 +313,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(&s.tempty[i], 2 * kOutWarps);
         }
         mbar_init(&s.drain, 1);
-        s.stop = s.any = 0;
+        s.stop = 0;
         fence_mbar_init();
         tma_prefetch_map(&map_x);
         tma_prefetch_map(&map_w);
@@ -354,14 +341,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int xrow = tile.row0 + rank * 128;
             const int wrow = kPair ? rank * p.n + tile.c0 : tile.c0 + rank * half;
 #pragma unroll 1
-            for (int b = kb0; b < kb1; ++b, ++issued) {
+            for (int b = 0; b < Kb; ++b, ++issued) {
                 const int st = issued % kPairStages;
                 if (issued >= kPairStages &&
                     !(ok = wait_or_stop(&s.empty[st], (issued / kPairStages - 1) & 1, stop)))
                     break;
                 if (!one) continue;
                 uint8_t *x = ring + st * kPairStageBytes;
-                const uint32_t bar = dsmem_addr(&s.full[st], lead);
+                const uint32_t bar = dsmem_addr(&s.full[st], 0);
                 if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
                 tma_tile_pair(x, &map_x, b * 128, xrow, bar);
                 tma_tile_pair(x + kOpBytes, &map_w, b * 128, wrow, bar);
@@ -373,15 +360,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else if (warp == kPairMma) {
         if (rank == 0) {
             const uint32_t one = elect_one(), idesc = tc_bf16_f32(kPairRows, width);
-            const uint16_t both = (uint16_t)(3 << lead);
+            const uint16_t both = 3;
             bool ok = true;
             int it = 0, run = 0;  // blocks, and accumulators filled
             for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
 #pragma unroll 1
-                for (int b = kb0; b < kb1; ++b, ++it) {
+                for (int b = 0; b < Kb; ++b, ++it) {
                     const int st = it % kPairStages, ac = run & 1;
-                    const bool first = kF32 ? (b - kb0) % kF32Run == 0 : b == kb0;
-                    const bool last = b == kb1 - 1 || (kF32 && (b - kb0) % kF32Run == kF32Run - 1);
+                    const bool first = kF32 ? b % kF32Run == 0 : b == 0;
+                    const bool last = b == Kb - 1 || (kF32 && b % kF32Run == kF32Run - 1);
                     if (first && run >= 2 &&
                         !(ok = wait_or_stop(&s.tempty[ac], (run / 2 - 1) & 1, stop)))
                         break;
@@ -402,7 +389,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int quad = warp & 3, half = warp >> 2;  // lanes 32 quad ..; half of the outputs
         const int cols = outs >> 1;
         const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + half * cols;
-        const uint32_t back[2] = {dsmem_addr(&s.tempty[0], lead), dsmem_addr(&s.tempty[1], lead)};
+        const uint32_t back[2] = {dsmem_addr(&s.tempty[0], 0), dsmem_addr(&s.tempty[1], 0)};
         uint8_t *stage = staging + warp * kOutStage;
         uint8_t *residual = staging + kOutWarps * kOutStage + warp * kResStage;
         bool ok = true;
@@ -415,11 +402,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int c0 = tile.c0 + half * cols, end = c0 + cols;
             Beside<kPair, kWide> by = {};
             by.res = residual;
-            if (!kSplit) by.load(p, row0, rows, c0, end, 0);
+            by.load(p, row0, rows, c0, end, 0);
             if constexpr (kF32) {
 #pragma unroll
                 for (int i = 0; i < kAcc; ++i) acc[i] = 0.0f;
-                for (int b = kb0; b < kb1; b += kF32Run, ++run) {
+                for (int b = 0; b < Kb; b += kF32Run, ++run) {
                     const int ac = run & 1;
                     ok = __all_sync(kFull, wait_or_stop(&s.tfull[ac], (run / 2) & 1, stop));
                     if (!ok) break;
@@ -441,7 +428,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 ok = __all_sync(kFull, wait_or_stop(&s.tfull[run & 1], (run / 2) & 1, stop));
                 tc_fence_after();
             }
-            if (!ok || kSplit) break;
+            if (!ok) break;
             const auto chunk = [&](int c) {
                 // where an accumulator ends within the 32, what is behind it is not stored
                 uint32_t v[2][16];
@@ -468,7 +455,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 const Beside<kPair, kWide> now = by;
                 by.load(p, row0, rows, c0 + c + kOuts, end, c / kOuts + 1);
-                finish<kPair, kF32, false, kWide>(p, stage, now, row0, rows, c0 + c, end, c / kOuts, 1, 0);
+                finish<kPair, kF32, kWide>(p, stage, now, row0, rows, c0 + c, end, c / kOuts);
             };
             if constexpr (kF32) {
 #pragma unroll
@@ -498,73 +485,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     cluster_sync();  // neither CTA goes while the other may read or signal it
     tc_fence_after();
-    if constexpr (kSplit) {
-        // All parts are done with their rings: a chunk's sums of 32 rows (unit u) go to
-        // the ring of the part that finishes them, with the other parts'.
-        const int cols = outs >> 1, most = (cols + kOuts - 1) / kOuts, units = 8 * most;
-        const int slots = (units / 8 + parts - 1) / parts * 8;  // units of a part
-        if (s.stop && tid < 2 * parts) st_dsmem(dsmem_addr(&s.any, tid), 1);
-        if (warp < kOutWarps && !s.stop) {
-            const int quad = warp & 3, half = warp >> 2;
-            const uint32_t mine = tmem + ((uint32_t)(quad * 32) << 16) + half * cols;
-            const auto give = [&](int ch, const uint32_t (&v)[32]) {
-                const int u = (half * most + ch) * 4 + quad, slot = u / 8 / parts * 8 + u % 8;
-                uint8_t *to = ring + (part * slots + slot) * 4096;
-                const int owner = 2 * (u / 8 % parts) + rank;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    st_dsmem4(dsmem_addr(staged(to, lane, j), owner), v[4 * j], v[4 * j + 1],
-                              v[4 * j + 2], v[4 * j + 3]);
-            };
-            uint32_t v[32];
-            if constexpr (kF32) {
-#pragma unroll
-                for (int ch = 0; ch < kAcc / 32; ++ch) {
-                    if (ch >= most) break;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[ch * 32 + i]);
-                    give(ch, v);
-                }
-            } else {
-#pragma unroll 1
-                for (int ch = 0; ch < most; ++ch) {
-                    uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(v);
-                    uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(v + 16);
-                    tc_ld16(lo, mine + ch * kOuts);
-                    tc_ld16(hi, mine + ch * kOuts + (kPair ? outs : 16));
-                    tc_wait_ld();
-                    give(ch, v);
-                }
-            }
-        }
-        tc_fence_before();
-        cluster_sync();
-        tc_fence_after();
-        // where a part gave up the sums are not whole and no part stores any
-        if (warp < kOutWarps && !s.any && !s.stop) {
-            const PairTile tile = pair_tile(p, outs, tiles_m, tiles_n, blockIdx.x >> 1);
-            Beside<kPair, kWide> by = {};
-            by.res = staging + kOutWarps * kOutStage + warp * kResStage;
-            for (int slot = warp; slot < slots; slot += 8) {
-                const int u = (slot / 8 * parts + part) * 8 + warp;
-                if (u >= units) break;
-                const int quad = u & 3, ch = (u >> 2) % most, half = (u >> 2) / most;
-                const size_t row0 = (size_t)tile.row0 + rank * 128 + quad * 32;
-                const int rows = (int)min((long long)32, (long long)p.rows - (long long)row0);
-                const int c0 = tile.c0 + half * cols, c = c0 + ch * kOuts;
-                by.load(p, row0, rows, c, c0 + cols, 0);
-                if (kWide && !kPair && p.res) asm volatile("cp.async.wait_group 0;" ::: "memory");
-                finish<kPair, kF32, true, kWide>(p, ring + slot * 4096, by, row0, rows, c, c0 + cols, 0,
-                                          parts, slots * 4096);
-            }
-        }
-    }
     if (warp == kPairMma) tc_free_pair<512>(tmem);
 }
 
-template <bool kPair, bool kF32, bool kSplit, bool kWide>
+template <bool kPair, bool kF32, bool kWide>
 static cudaError_t launch_tiles(const Linear &p, const LinearPlan &plan, cudaStream_t st) {
-    const auto kern = k_linear_tiles<kPair, kF32, kSplit, kWide>;
+    const auto kern = k_linear_tiles<kPair, kF32, kWide>;
     const int width = plan.width;
     CUtensorMap map_x, map_w;
     cudaError_t err = tile_map(&map_x, p.x, p.rows, 2 * p.k, 128);
@@ -591,9 +517,8 @@ static cudaError_t launch_tiles(const Linear &p, const LinearPlan &plan, cudaStr
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = (unsigned)plan.parts;
-    cfg.gridDim = dim3((unsigned)(2 * (kSplit || tiles < pairs ? tiles : pairs)), 1,
-                       (unsigned)plan.parts);
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = st;
@@ -604,13 +529,9 @@ static cudaError_t launch_tiles(const Linear &p, const LinearPlan &plan, cudaStr
 
 template <bool kWide>
 static cudaError_t launch_all(const Linear &p, bool pair, const LinearPlan &plan, cudaStream_t st) {
-    if (plan.parts > 1)
-        return pair   ? launch_tiles<true, false, true, kWide>(p, plan, st)
-               : p.yf ? launch_tiles<false, true, true, kWide>(p, plan, st)
-                      : launch_tiles<false, false, true, kWide>(p, plan, st);
-    return pair   ? launch_tiles<true, false, false, kWide>(p, plan, st)
-           : p.yf ? launch_tiles<false, true, false, kWide>(p, plan, st)
-                  : launch_tiles<false, false, false, kWide>(p, plan, st);
+    return pair   ? launch_tiles<true, false, kWide>(p, plan, st)
+           : p.yf ? launch_tiles<false, true, kWide>(p, plan, st)
+                  : launch_tiles<false, false, kWide>(p, plan, st);
 }
 
 }  // namespace moe

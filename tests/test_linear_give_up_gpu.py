@@ -38,7 +38,7 @@ def product(rows, n, k, pair=False, f32=False, status=True):
 @pytest.mark.parametrize("rows,n,k,pair,f32,want", [
     (16, 1000, 2048, False, False, "16/8"), (61, 768, 2048, True, False, "32/4"),
     (61, 7167, 3592, False, False, "64/2"), (1000, 255, 3592, False, True, "64/4"),
-    (200, 2044, 3592, True, False, "tiles/2"),
+    (200, 2048, 7168, True, False, "128/2"),
 ])
 @pytest.mark.parametrize("status", [True, False])
 def test_no_part_of_a_cluster_stores(giving_up, rows, n, k, pair, f32, want, status):  # noqa: F811
@@ -51,7 +51,7 @@ def test_no_part_of_a_cluster_stores(giving_up, rows, n, k, pair, f32, want, sta
 @pytest.mark.parametrize("f32", [False, True])
 def test_others_store_theirs(giving_up, f32):  # noqa: F811
     """Few rows, no clusters: the second CTA's 64 rows are not there, the others are."""
-    rows, n, k = (5202, 1, 160) if f32 else (150, 18433, 64)
+    rows, n, k = (5474, 1, 328) if f32 else (150, 18433, 64)
     p = plan(rows, n, k, False, f32, sms())
     assert not p.width and p.parts == 1
     y, st, (want, err) = product(rows, n, k, False, f32)
@@ -65,7 +65,7 @@ def test_others_store_theirs(giving_up, f32):  # noqa: F811
 def test_a_pairs_second_cta(giving_up):  # noqa: F811
     """Tiles: the first pair's second CTA brings no block beyond its ring, so the pair's
     products end; whatever is stored is right."""
-    rows, n, k = 700, 3001, 1032
+    rows, n, k = 717, 3565, 1064
     assert way(plan(rows, n, k, False, False, sms())) == "tiles"
     y, st, (want, err) = product(rows, n, k)
     assert st == m.MOE_ST_TIMEOUT
@@ -75,7 +75,7 @@ def test_a_pairs_second_cta(giving_up):  # noqa: F811
 
 
 def test_the_next_call_is_right(path):  # noqa: F811
-    sizes = [(16, 1000, 2048, False), (200, 2044, 3592, True), (700, 3001, 1032, False)]
+    sizes = [(16, 1000, 2048, False), (200, 2048, 7168, True), (717, 3565, 1064, False)]
     with pytest.MonkeyPatch.context() as mp:
         m.lib()
         mp.setattr(m, "_LIB_PATH", path)

@@ -37,33 +37,39 @@ def run(rows, n, k, pair, f32, act, with_bias, with_res, seed=0):
 
 
 @pytest.mark.parametrize("rows,n,k,pair,f32,want", [
-    (7, 19457, 128, False, False, "16"), (1, 1, 8, True, False, "16"), (1, 1, 8, False, True, "16"),
-    (13, 7160, 1032, False, False, "16/2"), (622, 1, 416, True, False, "16/2"),
-    (611, 1, 448, False, True, "16/2"), (9, 4099, 648, False, False, "16/4"),
-    (1, 1, 432, True, False, "16/4"), (1, 1, 400, False, True, "16/4"),
-    (16, 1000, 2048, False, False, "16/8"), (3, 257, 4104, False, True, "16/8"),
-    (5, 70, 1416, True, False, "16/8"), (31, 12292, 520, False, False, "32"),
-    (2611, 1, 8, False, True, "32"), (2469, 1, 8, True, False, "32"),
-    (30, 6001, 2056, False, False, "32/2"), (1228, 1, 696, False, True, "32/2"),
-    (1428, 1, 920, True, False, "32/2"), (61, 768, 2048, True, False, "32/4"),
-    (593, 1, 832, False, False, "32/4"), (1018, 1, 816, False, True, "32/4"),
-    (190, 250, 3336, False, True, "32/8"), (257, 1, 1608, False, False, "32/8"),
-    (260, 1, 1632, True, False, "32/8"), (60, 18433, 256, False, False, "64"),
-    (96, 7168, 1032, False, False, "64"), (5557, 1, 152, True, False, "64"),
-    (5202, 1, 160, False, True, "64"), (61, 7167, 3592, False, False, "64/2"),
-    (2790, 1, 2248, False, True, "64/2"), (2463, 1, 2616, True, False, "64/2"),
-    (1559, 1, 3896, False, False, "64/4"), (1000, 255, 3592, False, True, "64/4"),
-    (1153, 1, 3928, True, False, "64/4"), (897, 1, 6912, False, True, "64/8"),
-    (922, 2, 7792, False, False, "64/8"), (481, 1, 7864, True, False, "64/8"),
-    (330, 3606, 272, False, False, "128"), (226, 5632, 272, False, True, "128"),
-    (6525, 75, 264, True, False, "128"), (127, 7166, 7176, False, False, "128/2"),
-    (65, 7686, 4128, False, True, "128/2"), (70, 3547, 3880, True, False, "128/2"),
-    (2356, 1, 5544, False, False, "128/4"), (2047, 250, 7176, False, True, "128/4"),
-    (2382, 1, 6984, True, False, "128/4"), (129, 40000, 64, False, False, "tiles"),
-    (700, 3001, 1032, False, False, "tiles"), (2538, 1426, 8, False, False, "tiles"),
-    (1100, 1032, 520, True, False, "tiles"), (9000, 130, 1160, False, True, "tiles"),
-    (200, 2044, 3592, True, False, "tiles/2"), (250, 7168, 7168, False, False, "tiles/2"),
-    (7638, 1, 1816, False, True, "tiles/2"),
+    (7, 19457, 128, False, False, "16"), (1, 1, 8, True, False, "16"),
+    (1, 1, 8, False, True, "16"), (13, 7160, 1032, False, False, "16/2"),
+    (622, 1, 696, True, False, "16/2"), (595, 1, 720, False, True, "16/2"),
+    (9, 4099, 648, False, False, "16/4"), (1, 1, 432, True, False, "16/4"),
+    (1, 1, 400, False, True, "16/4"), (16, 1000, 2048, False, False, "16/8"),
+    (3, 257, 4104, False, True, "16/8"), (5, 70, 1416, True, False, "16/8"),
+    (31, 12292, 520, False, False, "32"), (2611, 1, 8, False, True, "32"),
+    (2469, 1, 8, True, False, "32"), (30, 6001, 2056, False, False, "32/2"),
+    (1223, 1, 1224, False, True, "32/2"), (1468, 1, 1176, True, False, "32/2"),
+    (61, 768, 2048, True, False, "32/4"), (593, 1, 832, False, False, "32/4"),
+    (1018, 1, 816, False, True, "32/4"), (190, 250, 3336, False, True, "32/8"),
+    (257, 1, 1608, False, False, "32/8"), (260, 1, 1632, True, False, "32/8"),
+    (60, 18433, 256, False, False, "64"), (96, 7168, 1032, False, False, "64"),
+    (5557, 1, 152, True, False, "64"), (5474, 1, 328, False, True, "64"),
+    (61, 7167, 3592, False, False, "64/2"), (2790, 1, 2248, False, True, "64/2"),
+    (2463, 1, 2616, True, False, "64/2"), (1559, 1, 3896, False, False, "64/4"),
+    (1000, 255, 3592, False, True, "64/4"), (1153, 1, 3928, True, False, "64/4"),
+    (897, 1, 6912, False, True, "64/8"), (922, 2, 7792, False, False, "64/8"),
+    (481, 1, 7864, True, False, "64/8"), (328, 3383, 288, False, False, "128"),
+    (257, 5981, 280, False, True, "128"), (6525, 75, 264, True, False, "128"),
+    (127, 7166, 7176, False, False, "128/2"), (65, 7686, 4128, False, True, "128/2"),
+    (70, 3547, 3880, True, False, "128/2"), (2536, 1, 5320, False, False, "128/4"),
+    (2047, 250, 7176, False, True, "128/4"), (2530, 1, 7096, True, False, "128/4"),
+    (129, 40000, 64, False, False, "tiles"), (717, 3565, 1064, False, False, "tiles"),
+    (2538, 1426, 8, False, False, "tiles"), (1100, 1032, 520, True, False, "tiles"),
+    (9000, 130, 1160, False, True, "tiles"), (1155, 4, 7904, False, False, "128/8"),
+    (593, 156, 8000, False, True, "128/8"), (1171, 3, 7704, True, False, "128/8"),
+    # tiles whose outputs' rows start on 8, 4 and 2 bytes
+    (1629, 260, 272, False, False, "tiles"), (1647, 258, 256, False, False, "tiles"),
+    (1603, 263, 264, False, False, "tiles"), (1132, 1428, 816, False, True, "tiles"),
+    (1404, 2594, 400, False, True, "tiles"), (1931, 1451, 888, False, True, "tiles"),
+    (834, 3028, 448, True, False, "tiles"), (854, 3482, 840, True, False, "tiles"),
+    (1229, 1883, 1080, True, False, "tiles"),
 ])
 def test_way(rows, n, k, pair, f32, want):
     assert way(plan(rows, n, k, pair, f32, sms())) == want
