@@ -23,27 +23,49 @@ constexpr int kLinearApart = 64;  // rows of a CTA up to which sums have room be
 // What the kernels take, in ns, fitted to 1300 measured times of 176 sizes, each of which
 // went every way (an eighth off as a rule); what is chosen is 2% slower than the fastest
 // way on average, 30% at most.
-//   Few rows: 2.5 us and 22 ns a row that a CTA has (24 with fp32 results), 0.5 us for sums
-//   that cross the cluster; the bytes of a CTA's stages at 153 KB/us, or 0.2 us a stage, in
-//   quadrature with the operands at 7.7 MB/us; for each further round of CTAs 2.6 us and 4
-//   ns a row.
+//   Few rows: 2.3 us and 24 ns a row that a CTA has (26 with fp32 results), 0.5 us for sums
+//   that cross the cluster; the bytes of a CTA's stages at 163 KB/us, or 0.28 us a stage, in
+//   quadrature with the operands at 7.1 MB/us; for each further round of CTAs 2.7 us and 22
+//   ns a row, or half that where two fit an SM.
 //   Tiles: 2.8 us and 15.6 ns an output of the tile; for each block of 64 along k what its
 //   products take (1.07 ns an output; with fp32 results 4% more), 0.22 us at least, or its
 //   bytes at the pair's share of 15 MB/us; a further tile of the pair's no less than storing
 //   one does (1.9 us and 12.4 ns an output).  Rows of outputs that do not start on 16 bytes
 //   are stored in 1.28 times as long, of an odd number in 1.9 times.
 // us estimated and measured: 61 rows of gate/up of 768 by 2048 5.0 and 5.0; 64 x 256 x 7168
-// 4.8 and 5.2; 2048 x 256 x 7168 in fp32 14.1 and 14.3; 200 x 2048 x 2048 7.0 and 6.9; 509 x
+// 4.7 and 5.2; 2048 x 256 x 7168 in fp32 13.5 and 14.3; 200 x 2048 x 2048 7.0 and 6.9; 509 x
 // 7168 x 7168 39.8 and 40.4; 8191 x 7168 x 7168 520 and 484.
+// A CTA's shared memory without its ring, a stage's, and its stages.
+inline int few_fixed(int at, int parts) {
+    const int rows = at / parts < 4 ? 4 : at / parts;
+    return 1280 + (at <= kLinearApart ? parts * rows * 512 : 0);
+}
+inline int few_stage(int at) { return 2 * (16384 + at * 128); }
+inline int few_stages(int at, int parts, int64_t stages, bool f32) {
+    const int fixed = few_fixed(at, parts), stage = few_stage(at);
+    const int64_t mine = (stages + parts - 1) / parts;
+    int got = (kSmem - fixed) / stage;
+    if (got > 6) got = 6;
+    if (got > mine) got = (int)mine;
+    // Tensor memory goes with shared memory: CTAs that fit an SM by the one fit by the
+    // other, and none waits for columns that a later kernel's CTAs hold.
+    const int columns = f32 ? 2 * at : at;
+    const int sums = at <= kLinearApart ? 1 : (at * 512 + stage - 1) / stage;  // their room
+    while (got < sums || fixed + got * stage < columns * (kSmem / 512)) ++got;
+    return got;
+}
+
 inline double few_cost(int at, int parts, int64_t tiles, int64_t stages, double bytes, bool f32,
                        int sms) {
     const int64_t ctas = tiles * parts;
-    const double waves = (double)((ctas + sms - 1) / sms), fed = (32768.0 + 256.0 * at) / 153.0;
+    const int smem = few_fixed(at, parts) + few_stages(at, parts, stages, f32) * few_stage(at);
+    const double waves = (double)((ctas + sms - 1) / sms), fed = (32768.0 + 256.0 * at) / 163.0;
     const double loop =
-        waves * (double)((stages + parts - 1) / parts) * (fed > 200.0 ? fed : 200.0);
-    const double hbm = bytes / 7700.0;
-    return 2500.0 + (f32 ? 24.0 : 22.0) * at + (parts == 1 ? 0.0 : 500.0) +
-           std::sqrt(loop * loop + hbm * hbm) + (waves - 1.0) * (2600.0 + 4.0 * at);
+        waves * (double)((stages + parts - 1) / parts) * (fed > 280.0 ? fed : 280.0);
+    const double hbm = bytes / 7100.0;
+    return 2300.0 + (f32 ? 26.0 : 24.0) * at + (parts == 1 ? 0.0 : 500.0) +
+           std::sqrt(loop * loop + hbm * hbm) +
+           (waves - 1.0) * (2700.0 + 22.0 * at) * (2 * (smem + 1024) <= 233472 ? 0.5 : 1.0);
 }
 
 inline double tile_cost(int width, int64_t n, int64_t tiles, int64_t blocks, bool f32, int sms) {
@@ -90,19 +112,7 @@ inline LinearPlan linear_plan(int64_t rows, int64_t n, int64_t k, bool pair, boo
             take(tile_cost(width, n, tiles, blocks, f32, sms), width, 0, 1);
         }
     if (best.width) return best;
-    const int rows_of = best.at / best.parts < 4 ? 4 : best.at / best.parts;
-    const int apart = best.at <= kLinearApart ? best.parts * rows_of * 512 : 0;
-    const int stage = 2 * (16384 + best.at * 128);
-    const int64_t mine = (stages + best.parts - 1) / best.parts;
-    best.stages = (kSmem - 1280 - apart) / stage;
-    if (best.stages > 6) best.stages = 6;
-    if (best.stages > mine) best.stages = (int)mine;
-    // Tensor memory goes with shared memory: CTAs that fit an SM by the one fit by the
-    // other, and none waits for columns that a later kernel's CTAs hold.
-    const int columns = f32 ? 2 * best.at : best.at;
-    const int sums = apart ? 1 : (best.at * 512 + stage - 1) / stage;  // their room
-    while (best.stages < sums || 1280 + apart + best.stages * stage < columns * (kSmem / 512))
-        ++best.stages;
+    best.stages = few_stages(best.at, best.parts, stages, f32);
     return best;
 }
 

@@ -57,16 +57,15 @@ def run(rows, n, k, pair, f32, act, with_bias, with_res, seed=0):
     (897, 1, 6912, False, True, "64/8"), (922, 2, 7792, False, False, "64/8"),
     (481, 1, 7864, True, False, "64/8"), (328, 3383, 288, False, False, "128"),
     (257, 5981, 280, False, True, "128"), (6525, 75, 264, True, False, "128"),
-    (127, 7166, 7176, False, False, "128/2"), (65, 7686, 4128, False, True, "128/2"),
+    (127, 7166, 7176, False, False, "128/2"), (5697, 52, 3800, False, True, "128/2"),
     (70, 3547, 3880, True, False, "128/2"), (2536, 1, 5320, False, False, "128/4"),
     (2047, 250, 7176, False, True, "128/4"), (2530, 1, 7096, True, False, "128/4"),
     (129, 40000, 64, False, False, "tiles"), (717, 3565, 1064, False, False, "tiles"),
     (2538, 1426, 8, False, False, "tiles"), (1100, 1032, 520, True, False, "tiles"),
-    (9000, 130, 1160, False, True, "tiles"), (1155, 4, 7904, False, False, "128/8"),
-    (593, 156, 8000, False, True, "128/8"), (1171, 3, 7704, True, False, "128/8"),
+    (9000, 130, 1160, False, True, "tiles"),
     # tiles whose outputs' rows start on 8, 4 and 2 bytes
     (1629, 260, 272, False, False, "tiles"), (1647, 258, 256, False, False, "tiles"),
-    (1603, 263, 264, False, False, "tiles"), (1132, 1428, 816, False, True, "tiles"),
+    (3623, 259, 208, False, False, "tiles"), (1132, 1428, 816, False, True, "tiles"),
     (1404, 2594, 400, False, True, "tiles"), (1931, 1451, 888, False, True, "tiles"),
     (834, 3028, 448, True, False, "tiles"), (854, 3482, 840, True, False, "tiles"),
     (1229, 1883, 1080, True, False, "tiles"),
