@@ -1,5 +1,14 @@
 // block.cu -- moe_block_norm: the norm after a branch, its gate and scale, the
 // residual addition, the next norm and its block-128 e4m3 coding in one pass.
+//
+// A row stays in its CTA's registers, as it was read, through both sums of squares: HBM is
+// read and written once.  Measured with every input and output: 32767 rows of 7168 333 us
+// (6.4 TB/s), 2048 rows 27 with bf16 out only (4.3 TB/s: a batch of 2048 is 3.4 rounds of
+// CTAs, and each waits for its loads and two sums), one row 3.2.  At 82% of the warps it is
+// bound by loads in flight and by the sums' barriers, no longer by instructions (pairs of
+// floats and no division: 351 us before).  Slower: rows by bulk copies one to three ahead in
+// CTAs that stay (437 to 580 us), both sums in one round (425 to 444; v's square from x's,
+// the products' and the residual's sums), 896 threads with a chunk each (476).
 #include <cmath>
 
 #include "bf16.cuh"

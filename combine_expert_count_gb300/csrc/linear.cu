@@ -13,12 +13,23 @@ namespace moe {
 
 // Few rows.  The weights are the 128-row operand of the tensor cores and NR rows of x
 // the other: a lane of tensor memory is an output.  A CTA has 128 outputs, or 64 of the
-// gate and the same 64 of the up projection, of NR rows; a warp brings
-// pairs of blocks of 64 along k by TMA into a ring, one issues their products, four take
-// the sums out.  (A stage costs the warps that load and issue about 300 cycles, whatever
-// it holds: with a block a stage a CTA took no more than 108 GB/s.)  The
-// CTAs of a cluster share k and then the rows: each sends its sums of a row to the part
-// that adds them up and stores the row.
+// gate and the same 64 of the up projection, of NR rows; a warp brings pairs of blocks
+// of 64 along k by TMA into a ring, one issues their products, four take the sums out, and
+// two more help with the outputs.  (A stage costs the warps that load and issue about 300
+// cycles, whatever it holds: with a block a stage a CTA took no more than 108 GB/s.)  The
+// CTAs of a cluster share k and then the rows: each sends its sums of four rows at a
+// time to the part that adds them up, in the parts' order, and stores them.
+//
+// What bounds it, and what it measured: one row, its weights.  1 x 7168 x 2048 takes 7.9 us
+// (3.7 TB/s), gate and up of 2048 by 7168 11.8 (5.0 TB/s): about 2 us pass before the first
+// bytes are here, 5 and 9 with weights on the way, and 1 with sums and outputs.  61 rows of
+// gate and up of 768 by 2048 5.0 us, 100 x 7168 x 2048 10.6, 2048 x 256 x 7168 14.3 in fp32
+// (13.3 in bf16): there a CTA's operands arrive for 7.6 us (120 GB/s an SM, which is what an
+// SM takes in), 1.8 us go with sending 48 KB of sums across the cluster (14 bytes a clock),
+// 2 with waiting for each other's and 1 with the outputs.  Word by word, instead of by
+// vectors of four rows, the sums took 2.9 us, and read from the other CTAs' memory by those
+// that add them up 20.  The sums of 128 rows wait until the ring is free: with room of
+// their own, and a stage less, the fp32 case took 15.7.
 constexpr int kLinTma = 4, kLinMma = 5, kLinWarps = 8, kLinThreads = 32 * kLinWarps;
 constexpr int kLinTile = 128 * 128;  // bytes of a weight tile of a block of k
 constexpr int kLinRun = 4;           // stages between the sums of an fp32 result: 512 of k
@@ -30,30 +41,20 @@ struct LinShared {
     int stop, any;  // this part gave up; some part did
 };
 constexpr int kLinHead = 256;  // bytes: LinShared, before the ring
-static_assert(sizeof(LinShared) <= kLinHead, "");
-
-// two blocks of weights, then two of rows
-__host__ __device__ constexpr int lin_stage(int NR) { return 2 * (kLinTile + NR * 128); }
+static_assert(sizeof(LinShared) <= kLinHead, "its place before the ring");
+static_assert(kLinHead + 1024 == kFewHead && kLinTile == kFewTile, "the plan's");
 // The rows of a part: whole groups of four, which go to it together.  Where there are
 // more parts than groups the last parts have none.
-__host__ __device__ constexpr int lin_rows(int NR, int parts) {
+__device__ __forceinline__ int lin_rows(int NR, int parts) {
     return NR / parts < 4 ? 4 : NR / parts;
-}
-// Up to so many rows the parts' sums have room of their own; with more they go where the
-// ring was, once all parts are done with theirs.
-__host__ __device__ constexpr int lin_apart(int NR, int parts) {
-    return NR <= kLinearApart ? parts * lin_rows(NR, parts) * 512 : 0;
-}
-__host__ __device__ constexpr int lin_smem(int NR, int parts, int stages) {
-    return kLinHead + 1024 + lin_apart(NR, parts) + stages * lin_stage(NR);
 }
 
 template <int NR, bool kPair, bool kF32>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear(const __grid_constant__ Linear p, int stages, const __grid_constant__ CUtensorMap map_x,
              const __grid_constant__ CUtensorMap map_w) {
-    constexpr int kBytes = lin_stage(NR);
-    constexpr int kAccs = kF32 ? 2 : 1;  // accumulators
+    constexpr int kBytes = 2 * (kLinTile + NR * 128);  // two blocks of weights, then two of rows
+    constexpr int kAccs = kF32 ? 2 : 1;                // accumulators
     constexpr int kUsed = kAccs * NR, kCols = kUsed < 32 ? 32 : kUsed;
     extern __shared__ uint8_t smem_raw[];
     LinShared &s = *reinterpret_cast<LinShared *>(smem_raw);
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 template <int NR, bool kPair, bool kF32>
 static cudaError_t launch_few(const Linear &p, const LinearPlan &plan, cudaStream_t st) {
     const auto kern = k_linear<NR, kPair, kF32>;
+    static_assert(few_stage(NR) == 2 * (kLinTile + NR * 128), "the kernel's");
     CUtensorMap map_x, map_w;
     cudaError_t err = tile_map(&map_x, p.x, p.rows, 2 * p.k, NR);
     if (err == cudaSuccess)
@@ -365,7 +367,7 @@ static cudaError_t launch_few(const Linear &p, const LinearPlan &plan, cudaStrea
     cfg.gridDim = dim3((unsigned)((p.rows + NR - 1) / NR), (unsigned)((p.n + outs - 1) / outs),
                        (unsigned)plan.parts);
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = (size_t)lin_smem(NR, plan.parts, plan.stages);
+    cfg.dynamicSmemBytes = (size_t)(few_fixed(NR, plan.parts) + plan.stages * few_stage(NR));
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;

@@ -18,7 +18,11 @@ struct LinearPlan {
 
 constexpr int kLinearBlock = 64;  // elements of k in 128 bytes
 constexpr int kSmem = 232448;  // a CTA's, which has an SM for itself
-constexpr int kLinearApart = 64;  // rows of a CTA up to which sums have room beside the ring
+constexpr int kFewHead = 1280;   // bytes before the ring of a CTA of few rows, at most
+constexpr int kFewTile = 16384;  // of weights in a block
+// Up to so many rows the parts' sums have room of their own; with more they go where the
+// ring was, once all parts are done with theirs.
+constexpr int kLinearApart = 64;
 
 // What the kernels take, in ns, fitted to 1300 measured times of 176 sizes, each of which
 // went every way (an eighth off as a rule); what is chosen is 2% slower than the fastest
@@ -38,9 +42,9 @@ constexpr int kLinearApart = 64;  // rows of a CTA up to which sums have room be
 // A CTA's shared memory without its ring, a stage's, and its stages.
 inline int few_fixed(int at, int parts) {
     const int rows = at / parts < 4 ? 4 : at / parts;
-    return 1280 + (at <= kLinearApart ? parts * rows * 512 : 0);
+    return kFewHead + (at <= kLinearApart ? parts * rows * 512 : 0);
 }
-inline int few_stage(int at) { return 2 * (16384 + at * 128); }
+constexpr int few_stage(int at) { return 2 * (kFewTile + at * 128); }
 inline int few_stages(int at, int parts, int64_t stages, bool f32) {
     const int fixed = few_fixed(at, parts), stage = few_stage(at);
     const int64_t mine = (stages + parts - 1) / parts;
@@ -59,7 +63,7 @@ inline double few_cost(int at, int parts, int64_t tiles, int64_t stages, double 
                        int sms) {
     const int64_t ctas = tiles * parts;
     const int smem = few_fixed(at, parts) + few_stages(at, parts, stages, f32) * few_stage(at);
-    const double waves = (double)((ctas + sms - 1) / sms), fed = (32768.0 + 256.0 * at) / 163.0;
+    const double waves = (double)((ctas + sms - 1) / sms), fed = few_stage(at) / 163.0;
     const double loop =
         waves * (double)((stages + parts - 1) / parts) * (fed > 280.0 ? fed : 280.0);
     const double hbm = bytes / 7100.0;
