@@ -17,6 +17,8 @@ path:  ``dispatch`` = moe_dispatch (or route_count, exchange, dispatch_send,
 dispatch_recv);  ``experts`` = moe_expert_gemm_swiglu, moe_expert_gemm;
 ``combine`` = moe_combine (or combine_send, combine_recv).  ``moe_rmsnorm``
 makes x before it, and ``moe_layer_few`` is the whole of it for a few tokens.
+The rest of a block is ``moe_linear`` and ``moe_topk`` (a router), ``moe_linear_glu``
+(a shared expert's first half) and ``moe_block_norm`` (the end).
 """
 from __future__ import annotations
 

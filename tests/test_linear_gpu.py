@@ -97,7 +97,9 @@ def test_rows_see_only_their_own():
     assert y[7].isnan().all() and y[:, 130].isnan().all() and not y[69, :130].isfinite().any()
 
 
-@pytest.mark.parametrize("rows,n,k", [(3, 130, 264), (33, 512, 2048), (300, 258, 136)])
+@pytest.mark.parametrize("rows,n,k", [(3, 130, 264), (33, 512, 2048), (300, 258, 136), (5, 33, 1032),
+                                      (100, 1001, 2048), (1629, 260, 272), (1647, 258, 256),
+                                      (3623, 259, 208), (1608, 264, 272)])
 def test_residual_in_place(rows, n, k):
     x, w, bias, res, _ = inputs(rows, n, k)
     want = linear(x, w, bias, res, "silu")
