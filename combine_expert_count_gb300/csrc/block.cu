@@ -2,11 +2,11 @@
 // residual addition, the next norm and its block-128 e4m3 coding in one pass.
 //
 // A row stays in its CTA's registers, as it was read, through both sums of squares: HBM is
-// read and written once.  Measured with every input and output: 32767 rows of 7168 333 us
-// (6.4 TB/s), 2048 rows 27 with bf16 out only (4.3 TB/s: a batch of 2048 is 3.4 rounds of
+// read and written once.  Measured with every input and output: 32767 rows of 7168 323 us
+// (6.6 TB/s), 2048 rows 27 with bf16 out only (4.3 TB/s: a batch of 2048 is 3.4 rounds of
 // CTAs, and each waits for its loads and two sums), one row 3.2.  At 82% of the warps it is
 // bound by loads in flight and by the sums' barriers, no longer by instructions (pairs of
-// floats and no division: 351 us before).  Slower: rows by bulk copies one to three ahead in
+// floats and no division: 332 us; 351 before).  Slower: rows by bulk copies one to three ahead in
 // CTAs that stay (437 to 580 us), both sums in one round (425 to 444; v's square from x's,
 // the products' and the residual's sums), 896 threads with a chunk each (476).
 #include <cmath>
@@ -22,6 +22,7 @@ namespace moe {
 
 struct BlockNorm {
     int H, rows;
+    int ahead;  // rows from one's own to the one that is brought to L2 (kAhead)
     uint64_t gate_of;  // 2^64 / rows that share a row of gate, above it; 0: each has its own
     float eps, scale, inv_H;
     const uint16_t *x, *post, *gate, *res, *gamma;
@@ -153,9 +154,14 @@ __device__ __forceinline__ void row_norm(const BlockNorm &p, size_t row, const u
     }
 }
 
+// `bytes` from p on, both multiples of 16, to L2.
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // One CTA per row, or one warp for short ones.
 constexpr int kRowWarps = 4;
-template <int V, int kMost, bool kWarp>
+template <int V, int kMost, bool kWarp, bool kAhead>
 __global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 4 : V == 4 ? 2 : 1) : 1)
     k_block_norm(const __grid_constant__ BlockNorm p) {
     __shared__ float part[2][32];
@@ -175,6 +181,11 @@ __global__ void __launch_bounds__(kMost, kMost == 512 ? (V <= 2 ? 4 : V == 4 ? 2
         x[i] = *reinterpret_cast<const uint4 *>(p.x + base + c * 8);
         if (p.res) r[i] = *reinterpret_cast<const uint4 *>(p.res + base + c * 8);
     }
+    if (kAhead && tid == 0 && row + p.ahead < p.rows) {
+        const size_t next = base + (size_t)p.ahead * p.H;
+        prefetch_l2(p.x + next, 2 * p.H);
+        if (p.res) prefetch_l2(p.res + next, 2 * p.H);
+    }
     row_norm<V, kWarp>(p, row, x, r, part[0], part[1]);
 }
 
@@ -192,24 +203,31 @@ static cudaError_t launch(K kern, int grid, int threads, const BlockNorm &p, cud
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-static cudaError_t launch_block_norm(const BlockNorm &p, cudaStream_t st) {
+static cudaError_t launch_block_norm(BlockNorm p, cudaStream_t st) {
     const int nch = p.H >> 3, rows = p.rows, sms = sm_count();
     if (rows > 2 * sms && nch <= 64) {
-        const auto kern = nch <= 32 ? k_block_norm<1, 128, true> : k_block_norm<2, 128, true>;
+        const auto kern =
+            nch <= 32 ? k_block_norm<1, 128, true, false> : k_block_norm<2, 128, true, false>;
         return launch(kern, (rows + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, p, st);
     }
     const int most = rows <= sms ? 1024 : 512;
     int V = rows > 2 * sms ? 2 : 1;
     while (V < 8 && nch > most * V) V *= 2;
     const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
-    const auto kern = nthr <= 512 ? (V == 1   ? k_block_norm<1, 512, false>
-                                     : V == 2 ? k_block_norm<2, 512, false>
-                                     : V == 4 ? k_block_norm<4, 512, false>
-                                              : k_block_norm<8, 512, false>)
-                                  : (V == 1   ? k_block_norm<1, 1024, false>
-                                     : V == 2 ? k_block_norm<2, 1024, false>
-                                     : V == 4 ? k_block_norm<4, 1024, false>
-                                              : k_block_norm<8, 1024, false>);
+    // CTAs of rows wider than 4096 leave warps of an SM without work, and their loads wait:
+    // each brings a later row to L2.  us without and with it: 32767 rows of 7168 332 and 323, of
+    // 4096 182 and 185; 8192 of 4608 58.0 and 57.6, of 8192 99 and 96, of 12288 165 and 150; 2048
+    // of 7168 27.7 and 27.2.  Rows four times as far ahead, and farther: 330 to 420.
+    p.ahead = sms;
+    const auto kern = nthr <= 512 ? (V == 1     ? k_block_norm<1, 512, false, false>
+                                     : nch <= 512 ? k_block_norm<2, 512, false, false>
+                                     : V == 2   ? k_block_norm<2, 512, false, true>
+                                     : V == 4   ? k_block_norm<4, 512, false, true>
+                                                : k_block_norm<8, 512, false, true>)
+                                  : (V == 1   ? k_block_norm<1, 1024, false, false>
+                                     : V == 2 ? k_block_norm<2, 1024, false, false>
+                                     : V == 4 ? k_block_norm<4, 1024, false, false>
+                                              : k_block_norm<8, 1024, false, false>);
     return launch(kern, rows, nthr, p, st);
 }
 

@@ -51,7 +51,8 @@ def check(got, x, gamma, eps=EPS, **kw):
 
 
 @pytest.mark.parametrize("rows,H", [(1, 128), (1, 7168), (3, 256), (6, 2048), (129, 1408),
-                                    (2050, 384), (5, 8192), (2, 65536), (1001, 7168), (3, 8320)])
+                                    (2050, 384), (5, 8192), (2, 65536), (1001, 7168), (3, 8320),
+                                    (200, 4224), (330, 8192), (310, 12288), (160, 33024)])
 def test_matches_formula(rows, H):
     x, gamma, post, gate, res = inputs(rows, H)
     for kw in (dict(), dict(post=post), dict(post=post, gate=gate, scale=0.5, res=res),
