@@ -566,7 +566,11 @@ __device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C>
     // the weights, lane r the r-th; sums over as many lanes as there may be
     const int half = p.R > 8 ? 16 : 4;
     const bool chosen = lane < p.R;
-    const float lv = chosen ? __ldg(l + got.mine) : -INFINITY;
+    float lv = chosen ? __ldg(l + got.mine) : -INFINITY;
+    if (p.bias) {  // one that its bias takes out of service is as good as masked
+        const float b = chosen ? __ldg(p.bias + got.mine) : 0.0f;
+        if (!(b > -INFINITY)) lv = -INFINITY;
+    }
     float s = 0.0f;
     if (p.renorm) {
         // all of them times exp(-m), so that small ones keep their ratios

@@ -577,13 +577,14 @@ int moe_linear_glu(const moe_shape *shape, int inter, int k, int act, const uint
  *   topk_idx: the R kept experts with the largest c, largest first
  *   topk_w:   scale * s_e, or scale * s_e / (sum of the chosen s) with renorm; the
  *         bias is not in it
- * Equal values go to the lowest index.  A logit of -infinity, or a NaN among c, is
- * an expert out of service: it comes after all others (its c is -infinity, and its
- * run's worth with it) and has weight 0.  A NaN logit, or one of +infinity with
- * MOE_SCORE_SOFTMAX, makes its token's weights NaN; the ids are valid ones all the
- * same.  bias may be NULL.  1 <= groups <= 32, E % groups == 0, 1 <= kept <= groups,
- * best <= E/groups and R <= kept * E/groups, else MOE_EINVAL (MOE_ENOTSUP for more
- * groups).  scale must be finite. */
+ * Equal values go to the lowest index.  A logit of -infinity, or a c that is -infinity
+ * or NaN (by its bias), is an expert out of service: it comes after all others (its c
+ * is -infinity, and its run's worth with it), has weight 0 and no part in the sum of
+ * renorm.  A NaN logit, or one of +infinity with MOE_SCORE_SOFTMAX, makes its token's
+ * weights NaN; the ids are valid ones all the same.  bias may be NULL.
+ * 1 <= groups <= 32, E % groups == 0, 1 <= kept <= groups, best <= E/groups and
+ * R <= kept * E/groups, else MOE_EINVAL (MOE_ENOTSUP for more groups).  scale must be
+ * finite. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
 #define MOE_MAX_GROUPS 32

@@ -103,7 +103,8 @@ def topk64(logits, R, bias=None, score="softmax", groups=1, kept=1, best=1, reno
         keep = np.argsort(-g, kind="stable")[:kept]
         e = np.sort(np.concatenate([np.arange(k * per, (k + 1) * per) for k in keep]))
         idx[i] = e[np.argsort(-c[i][e], kind="stable")[:R]]
-        lc = l[i, idx[i]]
+        # out of service, by the logit or by the bias: no weight, and none taken
+        lc = np.where(c[i, idx[i]] == -np.inf, -np.inf, l[i, idx[i]])
         chosen = np.where(lc == -np.inf, 0.0, s[i, idx[i]])
         if renorm and np.isfinite(lc.max()) and (score == "softmax" or lc.max() < 0):
             # the ratios of values that may be 0 by themselves

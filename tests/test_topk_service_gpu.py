@@ -1,0 +1,55 @@
+"""moe_topk where few experts are in service, for short batches (a warp a token) and long
+ones (eight lanes)."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from .test_topk_gpu import INF, check, choose, draw
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+LONG = 15000  # rows that go eight lanes each, with a bias as well
+
+
+def both_ways(l, R, **kw):
+    """The answer for l's rows, which long batches of them get too."""
+    idx, w = check(l, R, **kw)
+    times = -(-LONG // l.shape[0])
+    many = choose(l.repeat(times, 1), R, **kw)
+    for a, b in zip((idx, w), many):
+        assert torch.equal(a.repeat(times, 1).view(torch.int32), b.view(torch.int32))
+    return idx, w
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("off", [NAN, -INF])
+def test_a_bias_that_takes_an_expert_out_leaves_it_no_weight(score, renorm, off):
+    """Fewer experts in service than places: the others fill them, by their index, with
+    weight 0, and take nothing from those in service."""
+    l, bias = draw(40, 64, 21)
+    bias[5:] = off
+    bias[3] = -INF
+    l[7, 0] = l[8, :5] = -INF
+    for kw in (dict(), dict(scale=2.5), dict(groups=2, kept=1, best=1)):
+        idx, w = both_ways(l, 8, score=score, renorm=renorm, bias=bias, **kw)
+        out = (idx == 3) | (idx > 4) | (torch.gather(l, 1, idx.long()) == -INF)
+        assert (out.sum(-1) >= 4).all() and (w[out] == 0).all() and w.isfinite().all()
+        if renorm:
+            some = (~out).any(-1)
+            total = w.double().sum(-1)[some] / kw.get("scale", 1.0)
+            assert some.sum() == 39 and (total - 1).abs().max() < 8 * 2.0 ** -23
+    l, bias = draw(3, 32, 5)  # all experts are chosen
+    bias[4], bias[9] = -INF, NAN
+    idx, w = check(l, 32, score=score, renorm=renorm, bias=bias)
+    assert (idx[:, 30:] == torch.tensor([4, 9])).all() and (w[:, 30:] == 0).all()
+    assert (w[:, :30] > 0).all()
+
+
+def test_no_expert_in_service():
+    l, bias = draw(5, 32, 6)
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            idx, w = choose(l, 4, score=score, renorm=renorm, bias=torch.full((32,), NAN))
+            assert (idx == torch.arange(4)).all() and (w == 0).all()
