@@ -551,7 +551,9 @@ __device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C>
         }
     }
     Chosen got = take_any(p, key);
-    if (p.bias) {
+    // (a softmax that is no number has nothing to be ordered by more exactly: all of its
+    // exact values are NaN)
+    if (p.bias && !(bad && p.score == MOE_SCORE_SOFTMAX)) {
         // neighbours that are nearer than their errors, or some that may be before the R-th
         const float next = __shfl_down_sync(kFull, got.c, 1);
         const bool close = lane + 1 < got.n && next > -INFINITY &&

@@ -581,7 +581,7 @@ int moe_linear_glu(const moe_shape *shape, int inter, int k, int act, const uint
  * or NaN (by its bias), is an expert out of service: it comes after all others (its c
  * is -infinity, and its run's worth with it), has weight 0 and no part in the sum of
  * renorm.  A NaN logit, or one of +infinity with MOE_SCORE_SOFTMAX, makes its token's
- * weights NaN; the ids are valid ones all the same.  bias may be NULL.
+ * weights NaN; the ids are R different ones all the same.  bias may be NULL.
  * 1 <= groups <= 32, E % groups == 0, 1 <= kept <= groups, best <= E/groups and
  * R <= kept * E/groups, else MOE_EINVAL (MOE_ENOTSUP for more groups).  scale must be
  * finite. */

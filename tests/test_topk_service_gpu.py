@@ -1,10 +1,11 @@
-"""moe_topk where few experts are in service, for short batches (a warp a token) and long
-ones (eight lanes)."""
+"""moe_topk where few experts are in service or tokens are not numbers, for short batches
+(a warp a token) and long ones (eight lanes)."""
 from __future__ import annotations
 
 import pytest
 import torch
 
+from . import _dense as d
 from .test_topk_gpu import INF, check, choose, draw
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,23 @@ def test_no_expert_in_service():
         for renorm in (True, False):
             idx, w = choose(l, 4, score=score, renorm=renorm, bias=torch.full((32,), NAN))
             assert (idx == torch.arange(4)).all() and (w == 0).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,R", [(64, 6), (257, 8), (1000, 32)])
+def test_not_a_number_gets_different_experts(score, E, R):
+    """A token that is not a number has ids that differ, whatever the biases: equal ones
+    send it to where near values are ordered again."""
+    l, b = draw(9, E, 31)
+    l[2, 5], l[6, 9], l[7] = NAN, INF, NAN
+    for bias in (torch.zeros(E), torch.full((E,), 0.25), 2.0 ** -24 * b):
+        for rows in (9, LONG):
+            many = l.repeat(-(-rows // 9), 1)
+            idx, w = choose(many, R, score=score, bias=bias)
+            s = idx.sort(-1).values
+            assert (s[:, 1:] > s[:, :-1]).all() and s.min() >= 0 and s.max() < E
+            assert w[2::9].isnan().all() and w[7::9].isnan().all()
+            rest = [0, 1, 3, 4, 5, 8]
+            want, ww = d.topk64(l[rest], R, score=score, bias=bias)
+            assert torch.equal(idx[rest], want)
+            d.assert_f32(w[rest], ww, d.topk_error(l[rest], ww))
