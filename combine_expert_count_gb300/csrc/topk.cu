@@ -76,6 +76,14 @@ __device__ __forceinline__ float error_of(int score, float c) {
     return (score == MOE_SCORE_SIGMOID ? 0x1p-21f : 0x1p-18f) + fabsf(c) * 0x1p-23f;
 }
 
+// A run's worth by its two largest values is compared by its half: the sum itself may be
+// past fp32 where the biases are not.  worth_slack: the errors of two runs' worths
+// together, by the values of one (half of each value's twice; or its first value's twice).
+__device__ __forceinline__ float half_sum(float a, float b) { return 0.5f * a + 0.5f * b; }
+__device__ __forceinline__ float worth_slack(int score, bool sums, float a, float b) {
+    return error_of(score, a) + error_of(score, sums ? b : a);
+}
+
 // The same score with the accurate ones, for the weights.
 __device__ __forceinline__ float score32(int score, float l, float top, float inv_sum) {
     return score == MOE_SCORE_SIGMOID ? 1.0f / (1.0f + expf(-l)) : expf(l - top) * inv_sum;
@@ -357,7 +365,7 @@ __device__ __forceinline__ uint32_t kept_runs(const Router &p, const float *l, c
                                               const uint32_t (&key)[C], float top, float inv_sum,
                                               long long *room) {
     const int lane = threadIdx.x & 31;
-    float slack = 0.0f;  // both errors of two runs' worths
+    float slack = 0.0f;  // of two runs' worths
     uint32_t mine = 0;   // lane g: the worth of run g
     const bool sums = p.best == 2, scored = !p.bias && sums;
     if (p.per >= 4 && p.per <= 128 && (p.per & (p.per - 1)) == 0) {
@@ -379,10 +387,8 @@ __device__ __forceinline__ uint32_t kept_runs(const Router &p, const float *l, c
                 b = fmaxf(fminf(a, oa), fmaxf(b, ob));
                 a = fmaxf(a, oa);
             }
-            const float worth = sums ? a + b : a;
-            if (worth > -INFINITY)
-                slack = fmaxf(slack, 2.0f * (error_of(p.score, a) +
-                                             (sums ? error_of(p.score, b) : 0.0f)));
+            const float worth = sums ? half_sum(a, b) : a;
+            if (worth > -INFINITY) slack = fmaxf(slack, worth_slack(p.score, sums, a, b));
             // to lane g from the first lane of run g
             const int e = lane * p.per;
             const float got = __shfl_sync(kFull, worth, (e & 127) >> 2);
@@ -401,17 +407,17 @@ __device__ __forceinline__ uint32_t kept_runs(const Router &p, const float *l, c
                 a = max(a, k);
             }
             const uint32_t first = __reduce_max_sync(kFull, a);
-            uint32_t worth = first;
-            float error = error_of(p.score, value_of(first));
+            uint32_t worth = first, second = first;
             if (sums) {
                 const unsigned who = __ballot_sync(kFull, a == first);
                 // the second largest: the others' first, or this lane's second
                 const uint32_t rest = (who & (who - 1)) || a != first ? a : b;
-                const uint32_t second = __reduce_max_sync(kFull, rest);
-                worth = key_of(value_of(first) + value_of(second));
-                error += error_of(p.score, value_of(second));
+                second = __reduce_max_sync(kFull, rest);
+                worth = key_of(half_sum(value_of(first), value_of(second)));
             }
-            if (worth > kLowest) slack = fmaxf(slack, 2.0f * error);
+            if (worth > kLowest)
+                slack = fmaxf(slack,
+                              worth_slack(p.score, sums, value_of(first), value_of(second)));
             if (lane == g) mine = worth;
         }
     }
@@ -749,10 +755,8 @@ __global__ void __launch_bounds__(32 * kFastWarps, S <= 16 ? 8 : S <= 32 ? 6 : 3
             const bool starts = q == 0 || (p.ends >> (q - 1) & 1u), ends = p.ends >> q & 1u;
             b = starts ? b0 : fmaxf(fminf(a, a0), fmaxf(b, b0));
             a = starts ? a0 : fmaxf(a, a0);
-            worth[q] = ends ? (sums ? a + b : a) : -INFINITY;
-            if (worth[q] > -INFINITY)
-                slack = fmaxf(slack, 2.0f * (error_of(p.score, a) +
-                                             (sums ? error_of(p.score, b) : 0.0f)));
+            worth[q] = ends ? (sums ? half_sum(a, b) : a) : -INFINITY;
+            if (worth[q] > -INFINITY) slack = fmaxf(slack, worth_slack(p.score, sums, a, b));
         }
         // lane sub ranks the runs that end with q = sub, sub + 8
         uint32_t ends = 0;

@@ -1,5 +1,5 @@
-"""moe_topk where few experts are in service or tokens are not numbers, for short batches
-(a warp a token) and long ones (eight lanes)."""
+"""moe_topk where few experts are in service, tokens are not numbers or biases are as
+large as fp32 goes, for short batches (a warp a token) and long ones (eight lanes)."""
 from __future__ import annotations
 
 import pytest
@@ -9,7 +9,7 @@ from . import _dense as d
 from .test_topk_gpu import INF, check, choose, draw
 
 pytestmark = pytest.mark.gpu
-NAN = float("nan")
+NAN, LEAST = float("nan"), torch.finfo(torch.float32).min
 LONG = 15000  # rows that go eight lanes each, with a bias as well
 
 
@@ -74,3 +74,22 @@ def test_not_a_number_gets_different_experts(score, E, R):
             want, ww = d.topk64(l[rest], R, score=score, bias=bias)
             assert torch.equal(idx[rest], want)
             d.assert_f32(w[rest], ww, d.topk_error(l[rest], ww))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_runs_whose_worth_is_past_fp32(score):
+    """Two values of a run that are finite in fp32, whose sum is not: c is compared in 64
+    bits."""
+    l, _ = draw(23, 128, 41)
+    high = torch.zeros(128)
+    high[3], high[5], high[40], high[41], high[70], high[71] = 2e38, 2e38, 3e38, 3e38, 3e38, 2.9e38
+    low = torch.zeros(128)
+    low[:32], low[32:64], low[64:96], low[96:124] = -INF, LEAST, -3e38, -INF
+    part = torch.full((128,), LEAST)
+    part[::2] = -3.2e38
+    for bias in (high, low, part, -high, torch.full((128,), LEAST)):
+        for kept in (1, 2, 3):
+            both_ways(l, 8, score=score, bias=bias, groups=4, kept=kept, best=2)
+    for bias, kept in ((low, 2), (low, 3), (part, 1)):
+        check(l, 30, score=score, bias=bias, groups=4, kept=kept, best=2)
+        check(l[:, :120], 17, score=score, bias=bias[:120], groups=5, kept=kept, best=2)  # runs of 24
