@@ -48,7 +48,7 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
 }
 
 __device__ __forceinline__ uint4 vec8(const uint16_t *p, int c) {
-    return __ldg(reinterpret_cast<const uint4 *>(p + c * 8));
+    return *reinterpret_cast<const uint4 *>(p + c * 8);
 }
 
 // Eight bf16 values as four pairs of floats; pairs keep the instructions few, which

@@ -91,8 +91,8 @@ struct Beside {
         const int lane = threadIdx.x & 31, at = c + (lane % kLanes) * 8;
         const bool in = at < min(end, p.n);
         if (in && p.bias) {
-            bias[0] = __ldg(reinterpret_cast<const uint4 *>(p.bias + at));
-            if (kPair) bias[kPair ? 1 : 0] = __ldg(reinterpret_cast<const uint4 *>(p.bias + p.n + at));
+            bias[0] = *reinterpret_cast<const uint4 *>(p.bias + at);
+            if (kPair) bias[kPair ? 1 : 0] = *reinterpret_cast<const uint4 *>(p.bias + p.n + at);
         }
         if (!kPair && p.res) {
             if (in)

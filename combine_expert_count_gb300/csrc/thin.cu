@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
         ids = reinterpret_cast<int *>(ring);  // the ring is not in use yet
         int bad = 0;
         for (int i = tid; i < A; i += kThinThreads) {
-            ids[i] = __ldg(p.idx + i);
+            ids[i] = p.idx[i];
             bad |= (unsigned)ids[i] >= (unsigned)p.E;
         }
         if (blockIdx.x == 0 && blockIdx.y == 0 && part == 0) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
     } else if constexpr (kMode == Thin::kDown) {
         for (int i = tid; i < 2 * p.E; i += kThinThreads) who[i] = 0;
         for (int i = tid; i < p.ntok * 128; i += kThinThreads) sums[i] = 0.0f;
-        for (int i = tid; i < A; i += kThinThreads) ids[i] = __ldg(p.idx + i);
+        for (int i = tid; i < A; i += kThinThreads) ids[i] = p.idx[i];
         __syncthreads();
         for (int i = tid; i < A; i += kThinThreads) {
             const int t = i / p.R;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             if (again) continue;
             float w = 0.0f;
             for (int q = i; q < t * p.R + p.R; ++q)
-                if (ids[q] == x) w += __ldg(p.topk_w + q);
+                if (ids[q] == x) w += p.topk_w[q];
             const unsigned below = (1u << (t & 31)) - 1u;
             const int at = place[x] + (t < 32 ? __popc(who[2 * x] & below)
                                               : __popc(who[2 * x]) + __popc(who[2 * x + 1] & below));

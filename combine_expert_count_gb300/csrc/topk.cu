@@ -600,8 +600,10 @@ __device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C>
     }
 }
 
+// (us with the compiler's own choice of registers, which spills, and with these: 2048 tokens,
+// 8 of 384 with a bias 8.0 and 7.2, 8 of 256 with a bias and runs 9.8 and 8.5)
 template <int C>
-__global__ void __launch_bounds__(32 * topk_warps(C)) k_topk(const __grid_constant__ Router p) {
+__global__ void __launch_bounds__(32 * topk_warps(C), C <= 8 ? 8 : 5) k_topk(const __grid_constant__ Router p) {
     constexpr int kWarps = topk_warps(C);
     __shared__ Exact<C> exact[kWarps];
     const int warp = threadIdx.x >> 5;
