@@ -164,22 +164,22 @@ struct GroupedDest {
     int32_t *grp_src;
 };
 
-// Send row and grouped row of assignment k of token tok (-1: none).
+// Send row and grouped row of assignment k of token tok (-1: none).  By plain loads: behind
+// PdlGate the routing kernel wrote them while this one was there already.
 template <bool kGrouped>
 __device__ __forceinline__ void dest_rows(long long tok, int k, int T, int R, long long TR,
-                                          const int32_t *__restrict__ slot_row,
-                                          const GroupedDest &gd, long long &row,
+                                          const int32_t *slot_row, const GroupedDest &gd, long long &row,
                                           long long &grow) {
     const long long s = div_nonneg(tok, T);
-    const int sr = __ldg(slot_row + tok * R + k);
+    const int sr = slot_row[tok * R + k];
     row = (sr >= 0 && sr < TR) ? s * TR + sr : -1;
     grow = -1;
     if (kGrouped && row >= 0) {
-        const int e = __ldg(gd.idx + tok * R + k);
+        const int e = gd.idx[tok * R + k];
         if ((unsigned)e < (unsigned)gd.E) {
             const int Er = gd.E / gd.N, r = e / Er, j = e - r * Er;
-            const int g = __ldg(gd.seg_off + ((size_t)r * Er + j) * gd.N + s) +
-                          (sr - __ldg(gd.eso + (size_t)s * (gd.E + 1) + e));
+            const int g = gd.seg_off[((size_t)r * Er + j) * gd.N + s] +
+                          (sr - gd.eso[(size_t)s * (gd.E + 1) + e]);
             if (g >= 0 && g < gd.cap) grow = (long long)r * gd.cap + g;
         }
     }
@@ -220,7 +220,7 @@ __device__ __forceinline__ void publish_row(const Signal &sg, int g, int target)
 template <Dest kDest, bool kHostX, bool kSignal = false, class Gate = NoGate>
 __device__ __forceinline__ int quant_pack_body(
     int T, int R, int H, int P, long long tok0, long long nitems, const uint16_t *__restrict__ x,
-    const int32_t *__restrict__ slot_row, uint8_t *__restrict__ send_q, float *__restrict__ send_s,
+    const int32_t *slot_row, uint8_t *__restrict__ send_q, float *__restrict__ send_s,
     int32_t *__restrict__ send_tok, int32_t *__restrict__ status, const GroupedDest &gd,
     const LLDest &ll, const Signal &sg, long long cta, long long ncta, const Gate &gate = Gate()) {
     constexpr bool kGrouped = kDest == Dest::kSendGrouped;
@@ -462,7 +462,7 @@ __device__ __forceinline__ int quant_pack_body(
 template <Dest kDest, bool kHostX, bool kPdl = false>
 __global__ void __maxnreg__(MOE_QUANT_MAXNREG)
     k_quant_pack_staged(int T, int R, int H, int P, long long tok0, long long nitems,
-                        const uint16_t *__restrict__ x, const int32_t *__restrict__ slot_row,
+                        const uint16_t *__restrict__ x, const int32_t *slot_row,
                         uint8_t *__restrict__ send_q, float *__restrict__ send_s,
                         int32_t *__restrict__ send_tok, int32_t *__restrict__ status,
                         const GroupedDest gd, const LLDest ll) {
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(256, MOE_LL_RANKED_MINB)
 template <bool kHostX>
 __global__ void __launch_bounds__(256, MOE_SIG_MINB)
     k_dispatch_signalled(int T, int R, int H, int P, long long nitems,
-                         const uint16_t *__restrict__ x, const int32_t *__restrict__ slot_row,
+                         const uint16_t *__restrict__ x, const int32_t *slot_row,
                          uint8_t *__restrict__ send_q, float *__restrict__ send_s,
                          int32_t *__restrict__ send_tok, int32_t *__restrict__ status,
                          const DispatchMapT<true> pull, const Signal sg, int32_t *done) {

@@ -91,7 +91,7 @@ __device__ __forceinline__ int2 group_rows(const Product &p, int e) {
     if (!p.grp_off) return make_int2(0, p.cap);
     const int Er = p.E / p.N, r = e / Er, j = e - r * Er;
     const int32_t *off = p.grp_off + (size_t)r * (Er + 1) + j;
-    const int b = min(max(__ldg(off), 0), p.cap), t = min(max(__ldg(off + 1), b), p.cap);
+    const int b = min(max(off[0], 0), p.cap), t = min(max(off[1], b), p.cap);
     return make_int2(b, t - b);
 }
 

@@ -28,8 +28,7 @@ constexpr int norm_ctas(int V, int most) { return most == 512 ? (V <= 2 ? 4 : V 
 
 template <int V, int kMost>
 __global__ void __launch_bounds__(kMost, norm_ctas(V, kMost)) k_rmsnorm(int H, float eps, const uint16_t *x,
-                                                   const uint16_t *res,
-                                                   const uint16_t *__restrict__ gamma,
+                                                   const uint16_t *res, const uint16_t *gamma,
                                                    uint16_t *res_out, uint16_t *y,
                                                    uint8_t *__restrict__ q, float *__restrict__ s) {
     __shared__ float wsum[32];
@@ -69,7 +68,7 @@ __global__ void __launch_bounds__(kMost, norm_ctas(V, kMost)) k_rmsnorm(int H, f
         uint32_t amax = 0;
         if (in) {
             float w[8];
-            unpack8(w, __ldg(reinterpret_cast<const uint4 *>(gamma + c * 8)));
+            unpack8(w, *reinterpret_cast<const uint4 *>(gamma + c * 8));
 #pragma unroll
             for (int u = 0; u < 8; ++u) v[i][u] = (v[i][u] * rstd) * w[u];
             if (y) *reinterpret_cast<uint4 *>(y + base + c * 8) = pack_bf16x8(v[i]);

@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kThinThreads, 2)
             int b = 0, c = 0;
             if (x < p.E && p.grp_off) {
                 const int32_t *off = p.grp_off + (size_t)(x / Er) * (Er + 1) + x % Er;
-                b = min(max(__ldg(off), 0), p.cap);
-                c = min(max(__ldg(off + 1), b), p.cap) - b;
+                b = min(max(off[0], 0), p.cap);
+                c = min(max(off[1], b), p.cap) - b;
             } else if (x < p.E) {
                 c = p.cap;
             }

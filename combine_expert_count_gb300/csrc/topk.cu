@@ -282,24 +282,26 @@ __device__ __noinline__ void choose64(const Router &p, const float *l, long long
     __syncwarp();
 }
 
-// A lane's logits: v[4 q + j] is expert 128 q + 4 lane + j; -infinity behind the last.
+// A lane's logits or biases: v[4 q + j] is expert 128 q + 4 lane + j; `none` behind the
+// last.  By plain loads: the kernel before may write them while this one waits for it.
 __device__ __forceinline__ int expert_at(int i) {
     return (i >> 2) * 128 + (threadIdx.x & 31) * 4 + (i & 3);
 }
 template <int C>
-__device__ __forceinline__ void load_logits(const Router &p, const float *l, float (&v)[C]) {
+__device__ __forceinline__ void load_row(const Router &p, const float *l, float none,
+                                         float (&v)[C]) {
     const bool quads = (p.E & 3) == 0;  // then every row starts on 16 bytes
 #pragma unroll
     for (int q = 0; q < C / 4; ++q) {
         const int e = expert_at(4 * q);
-        float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        float4 f = make_float4(none, none, none, none);
         if (quads) {
-            if (e < p.E) f = __ldg(reinterpret_cast<const float4 *>(l + e));
+            if (e < p.E) f = *reinterpret_cast<const float4 *>(l + e);
         } else {
-            if (e < p.E) f.x = __ldg(l + e);
-            if (e + 1 < p.E) f.y = __ldg(l + e + 1);
-            if (e + 2 < p.E) f.z = __ldg(l + e + 2);
-            if (e + 3 < p.E) f.w = __ldg(l + e + 3);
+            if (e < p.E) f.x = l[e];
+            if (e + 1 < p.E) f.y = l[e + 1];
+            if (e + 2 < p.E) f.z = l[e + 2];
+            if (e + 3 < p.E) f.w = l[e + 3];
         }
         v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
     }
@@ -308,24 +310,11 @@ __device__ __forceinline__ void load_logits(const Router &p, const float *l, flo
 // What is compared, c or the logits: masked experts last, those behind the last and
 // those of runs that are not kept not there at all.
 template <int C>
-__device__ __forceinline__ void make_keys(const Router &p, const float (&v)[C], float top,
-                                          float inv_sum, uint32_t kept, uint32_t (&key)[C]) {
+__device__ __forceinline__ void make_keys(const Router &p, const float (&v)[C],
+                                          const float (&b)[C], float top, float inv_sum,
+                                          uint32_t kept, uint32_t (&key)[C]) {
     if (p.bias) {
-        float b[C], c[C];
-#pragma unroll
-        for (int q = 0; q < C / 4; ++q) {
-            const int e = expert_at(4 * q);
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if ((p.E & 3) == 0) {
-                if (e < p.E) f = __ldg(reinterpret_cast<const float4 *>(p.bias + e));
-            } else {
-                if (e < p.E) f.x = __ldg(p.bias + e);
-                if (e + 1 < p.E) f.y = __ldg(p.bias + e + 1);
-                if (e + 2 < p.E) f.z = __ldg(p.bias + e + 2);
-                if (e + 3 < p.E) f.w = __ldg(p.bias + e + 3);
-            }
-            b[4 * q] = f.x, b[4 * q + 1] = f.y, b[4 * q + 2] = f.z, b[4 * q + 3] = f.w;
-        }
+        float c[C];
         scores_about(p.score, v, top, inv_sum, c);
 #pragma unroll
         for (int i = 0; i < C; ++i) key[i] = key_of(v[i] == -INFINITY ? v[i] : c[i] + b[i]);
@@ -519,8 +508,9 @@ template <int C>
 __device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C> &exact) {
     const int lane = threadIdx.x & 31;
     const float *l = p.logits + (size_t)row * p.E;
-    float v[C];
-    load_logits(p, l, v);
+    float v[C], b[C] = {};
+    load_row(p, l, -INFINITY, v);
+    if (p.bias) load_row(p, p.bias, 0.0f, b);
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < C; ++i)
@@ -542,7 +532,7 @@ __device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C>
         inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
     uint32_t key[C], kept = ~0u;
-    make_keys(p, v, top, inv_sum, ~0u, key);
+    make_keys(p, v, b, top, inv_sum, ~0u, key);
     if (p.groups > p.kept) {
         kept = kept_runs(p, l, v, key, top, inv_sum, exact.c);
         if ((p.per & 3) == 0) {  // a quad is of one run
@@ -574,9 +564,9 @@ __device__ __forceinline__ void token_by_warp(const Router &p, int row, Exact<C>
     // the weights, lane r the r-th; sums over as many lanes as there may be
     const int half = p.R > 8 ? 16 : 4;
     const bool chosen = lane < p.R;
-    float lv = chosen ? __ldg(l + got.mine) : -INFINITY;
+    float lv = chosen ? l[got.mine] : -INFINITY;
     if (p.bias) {  // one that its bias takes out of service is as good as masked
-        const float b = chosen ? __ldg(p.bias + got.mine) : 0.0f;
+        const float b = chosen ? p.bias[got.mine] : 0.0f;
         if (!(b > -INFINITY)) lv = -INFINITY;
     }
     float s = 0.0f;
@@ -684,7 +674,7 @@ __global__ void __launch_bounds__(32 * kFastWarps, S <= 16 ? 8 : S <= 32 ? 6 : 3
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (32 * q + 4 * sub < p.E) f = __ldg(reinterpret_cast<const float4 *>(l + 32 * q + 4 * sub));
+        if (32 * q + 4 * sub < p.E) f = *reinterpret_cast<const float4 *>(l + 32 * q + 4 * sub);
         v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
     }
     const auto over = [&](auto f, float x) {  // of the token's lanes
@@ -722,7 +712,7 @@ __global__ void __launch_bounds__(32 * kFastWarps, S <= 16 ? 8 : S <= 32 ? 6 : 3
         for (int q = 0; q < Q; ++q) {
             const int e = 32 * q + 4 * sub;
             float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (e < p.E) b = __ldg(reinterpret_cast<const float4 *>(p.bias + e));
+            if (e < p.E) b = *reinterpret_cast<const float4 *>(p.bias + e);
             c[4 * q] += b.x, c[4 * q + 1] += b.y, c[4 * q + 2] += b.z, c[4 * q + 3] += b.w;
         }
 #pragma unroll
@@ -853,7 +843,7 @@ __global__ void __launch_bounds__(32 * kFastWarps, S <= 16 ? 8 : S <= 32 ? 6 : 3
         // the weights: the token's lanes are among themselves here
         const unsigned who = 0xffu << (lane & 24);
         const int e = sub < p.R ? mine[sub] : 0;
-        const float lv = sub < p.R ? __ldg(l + e) : -INFINITY;
+        const float lv = sub < p.R ? l[e] : -INFINITY;
         float s = 0.0f;
         if (p.renorm) {
             float m = lv;
