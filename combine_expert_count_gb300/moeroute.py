@@ -522,12 +522,27 @@ def moe_layer_few(shape, inter: int, x, topk_idx, topk_w, w13_q, w13_s, w2_q, w2
     _check(rc, "moe_layer_few")
 
 
-def _at(t, nbytes: int, name: str, device: int):
+# What buffers of such values are not given as: other values, which would be read, or
+# written, as something else.  Integers may hold the bits of any, but int64 ids are ids.
+_OTHER = {
+    "bf16": frozenset((torch.float16, torch.float32, torch.float64)),
+    "e4m3": frozenset((torch.float16, torch.float32, torch.float64)),
+    "fp32": frozenset((torch.float16, torch.float64)),
+    "int32": frozenset((torch.float16, torch.float32, torch.float64, torch.int64)),
+}
+_NOT_BF16, _NOT_E4M3, _NOT_FP32, _NOT_INT32 = _OTHER.values()
+
+
+def _at(t, nbytes: int, name: str, device: int, other=_NOT_BF16):
     """The address of a tensor on the current device, which the call's kernels run on;
-    no host memory.  _ptr's checks in the fewest steps: a small call is bound by them."""
+    no host memory, no type of ``other``.  _ptr's checks in the fewest steps: a small call
+    is bound by them."""
     if (t is not None and t.get_device() == device and t.nbytes >= nbytes
-            and t.is_contiguous()):
+            and t.is_contiguous() and t.dtype not in other):
         return t.data_ptr()
+    if t is not None and nbytes and t.dtype in other:
+        want = next(k for k, v in _OTHER.items() if v is other)
+        raise ValueError(f"{name}: {t.dtype}, where {want} values are expected")
     if t is not None and not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
     if t is not None and t.get_device() != device:
@@ -554,14 +569,15 @@ def moe_linear(shape, n: int, k: int, x, w, y, bias=None, res=None, act: str = "
     weights [n][k]; ``y`` is bf16, or fp32 where its dtype is torch.float32."""
     sh, d = _as_shape(shape), torch._C._cuda_getDevice()
     rows, f32 = sh.N * sh.T, y is not None and y.dtype == torch.float32
-    py = _at(y, rows * n * (4 if f32 else 2), "y", d)
+    py = _at(y, rows * n * (4 if f32 else 2), "y", d, _NOT_FP32 if f32 else _NOT_BF16)
     rc = (_lib or lib()).moe_linear(
         ctypes.byref(sh), n, k, _named(MOE_ACTS, act, "act"),
         _at(x, rows * k * 2, "x", d), _at(w, n * k * 2, "w", d),
         None if bias is None else _at(bias, 2 * n, "bias", d),
         None if res is None else _at(res, rows * n * 2, "res", d),
         None if f32 else py, py if f32 else None,
-        None if status is None else _at(status, 4, "status", d), _stream_on(stream, d))
+        None if status is None else _at(status, 4, "status", d, _NOT_INT32),
+        _stream_on(stream, d))
     if rc:
         _check(rc, "moe_linear")
 
@@ -577,7 +593,8 @@ def moe_linear_glu(shape, inter: int, k: int, x, w13, h, bias=None, act: str = "
         _at(x, rows * k * 2, "x", d), _at(w13, 4 * inter * k, "w13", d),
         None if bias is None else _at(bias, 4 * inter, "bias", d),
         _at(h, rows * inter * 2, "h", d),
-        None if status is None else _at(status, 4, "status", d), _stream_on(stream, d))
+        None if status is None else _at(status, 4, "status", d, _NOT_INT32),
+        _stream_on(stream, d))
     if rc:
         _check(rc, "moe_linear_glu")
 
@@ -594,9 +611,10 @@ def moe_topk(shape, logits, topk_idx, topk_w, bias=None, score: str = "softmax",
     nk = rows * sh.R * 4
     rc = (_lib or lib()).moe_topk(
         ctypes.byref(sh), _named(MOE_SCORES, score, "score"), groups, kept, best,
-        1 if renorm else 0, scale, _at(logits, rows * E * 4, "logits", d),
-        None if bias is None else _at(bias, E * 4, "bias", d),
-        _at(topk_idx, nk, "topk_idx", d), _at(topk_w, nk, "topk_w", d), _stream_on(stream, d))
+        1 if renorm else 0, scale, _at(logits, rows * E * 4, "logits", d, _NOT_FP32),
+        None if bias is None else _at(bias, E * 4, "bias", d, _NOT_FP32),
+        _at(topk_idx, nk, "topk_idx", d, _NOT_INT32), _at(topk_w, nk, "topk_w", d, _NOT_FP32),
+        _stream_on(stream, d))
     if rc:
         _check(rc, "moe_topk")
 
@@ -618,8 +636,9 @@ def moe_block_norm(shape, x, gamma, eps: float, res_out=None, y=None, q=None, s=
         None if res is None else at(res, nx, "res", d),
         None if gamma is None else at(gamma, row, "gamma", d),
         None if res_out is None else at(res_out, nx, "res_out", d),
-        None if y is None else at(y, nx, "y", d), None if q is None else at(q, nx // 2, "q", d),
-        None if s is None else at(s, nx // 64, "s", d), _stream_on(stream, d))
+        None if y is None else at(y, nx, "y", d),
+        None if q is None else at(q, nx // 2, "q", d, _NOT_E4M3),
+        None if s is None else at(s, nx // 64, "s", d, _NOT_FP32), _stream_on(stream, d))
     if rc:
         _check(rc, "moe_block_norm")
 
