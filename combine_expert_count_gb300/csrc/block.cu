@@ -1,14 +1,17 @@
 // block.cu -- moe_block_norm: the norm after a branch, its gate and scale, the
 // residual addition, the next norm and its block-128 e4m3 coding in one pass.
 //
-// A row stays in its CTA's registers, as it was read, through both sums of squares: HBM is
-// read and written once.  Measured with every input and output: 32767 rows of 7168 323 us
-// (6.6 TB/s), 2048 rows 27 with bf16 out only (4.3 TB/s: a batch of 2048 is 3.4 rounds of
-// CTAs, and each waits for its loads and two sums), one row 3.2.  At 82% of the warps it is
-// bound by loads in flight and by the sums' barriers, no longer by instructions (pairs of
-// floats and no division: 332 us; 351 before).  Slower: rows by bulk copies one to three ahead in
-// CTAs that stay (437 to 580 us), both sums in one round (425 to 444; v's square from x's,
-// the products' and the residual's sums), 896 threads with a chunk each (476).
+// A row stays with its CTA, as it was read, through both sums of squares: HBM is read and
+// written once.  It stays in registers, but for what the compiler spills: 24 bytes a thread
+// where 32 registers hold two chunks (the way of 7168), 320 where 64 hold eight (rows
+// wider than 32768).  Measured with every input and output: 32767 rows of 7168 308 us (6.9
+// TB/s, as much as a copy), 2048 rows 26 with bf16 out only (4.5 TB/s: a batch of 2048 is
+// 3.4 rounds of CTAs, and each waits for its loads and two sums), one row 3.2.  Vectors
+// come by plain loads: through the read-only path, which is not for what the kernel before
+// may write, the compiler held more of them at once and spilled 64 bytes (323 us).
+// Slower when this took 332 to 392: rows by bulk copies one to three ahead in CTAs that stay
+// (437 to 580 us), both sums in one round (425 to 444; v's square from x's, the products'
+// and the residual's sums), 896 threads with a chunk each (476).
 #include <cmath>
 
 #include "bf16.cuh"
@@ -215,9 +218,9 @@ static cudaError_t launch_block_norm(BlockNorm p, cudaStream_t st) {
     while (V < 8 && nch > most * V) V *= 2;
     const int nthr = ((nch + V - 1) / V + 31) / 32 * 32;
     // CTAs of rows wider than 4096 leave warps of an SM without work, and their loads wait:
-    // each brings a later row to L2.  us without and with it: 32767 rows of 7168 332 and 323, of
-    // 4096 182 and 185; 8192 of 4608 58.0 and 57.6, of 8192 99 and 96, of 12288 165 and 150; 2048
-    // of 7168 27.7 and 27.2.  Rows four times as far ahead, and farther: 330 to 420.
+    // each brings a later row to L2.  us without and with it: 32767 rows of 7168 325 and 308, of
+    // 4096 177 and 175; 8192 of 4608 57.1 and 55.8, of 8192 95 and 92, of 12288 164 and 150; 2048
+    // of 7168 25.2 and 24.2.  Rows four times as far ahead, and farther: 330 to 420.
     p.ahead = sms;
     const auto kern = nthr <= 512 ? (V == 1     ? k_block_norm<1, 512, false, false>
                                      : nch <= 512 ? k_block_norm<2, 512, false, false>

@@ -24,9 +24,9 @@ constexpr int kFewTile = 16384;  // of weights in a block
 // ring was, once all parts are done with theirs.
 constexpr int kLinearApart = 64;
 
-// What the kernels take, in ns, fitted to 1300 measured times of 176 sizes, each of which
-// went every way (an eighth off as a rule); what is chosen is 2% slower than the fastest
-// way on average, 30% at most.
+// What the kernels take, in ns, fitted to 1560 measured times of 176 sizes, each of which
+// went every way (a seventh off as a rule); what is chosen is 1.5% slower than the fastest
+// way on average, 27% at most.
 //   Few rows: 2.3 us and 24 ns a row that a CTA has (26 with fp32 results), 0.5 us for sums
 //   that cross the cluster; the bytes of a CTA's stages at 163 KB/us, or 0.28 us a stage, in
 //   quadrature with the operands at 7.1 MB/us; for each further round of CTAs 2.7 us and 22
@@ -36,9 +36,11 @@ constexpr int kLinearApart = 64;
 //   bytes at the pair's share of 15 MB/us; a further tile of the pair's no less than storing
 //   one does (1.9 us and 12.4 ns an output).  Rows of outputs that do not start on 16 bytes
 //   are stored in 1.28 times as long, of an odd number in 1.9 times.
-// us estimated and measured: 61 rows of gate/up of 768 by 2048 5.0 and 5.0; 64 x 256 x 7168
-// 4.7 and 5.2; 2048 x 256 x 7168 in fp32 13.5 and 14.3; 200 x 2048 x 2048 7.0 and 6.9; 509 x
-// 7168 x 7168 39.8 and 40.4; 8191 x 7168 x 7168 520 and 484.
+// us estimated and measured: 61 rows of gate/up of 768 by 2048 5.0 and 5.0, 2048 rows 13.6
+// and 14.4; 64 x 256 x 7168 5.2 and 5.2; 2048 x 256 x 7168 in fp32 13.4 and 14.4; 200 x 2048 x
+// 2048 7.1 and 7.0.  It is low for the largest tiles: 509 x 7168 x 7168 35.7 and 40.9, 8191 x
+// 7168 x 7168 447 and 483 (there the clock falls), 8191 x 256 x 7168 in fp32 30.4 and 36.5, 8191 x
+// 2048 x 768 with a residual, which it does not count, 26.0 and 30.1.
 // A CTA's shared memory without its ring, a stage's, and its stages.
 inline int few_fixed(int at, int parts) {
     const int rows = at / parts < 4 ? 4 : at / parts;

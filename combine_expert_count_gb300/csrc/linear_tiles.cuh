@@ -10,14 +10,15 @@
 // Pairs go through the tiles one after another; an accumulator in tensor memory is
 // stored by eight warps while the other one is filled.
 //
-// Measured: 8191 x 7168 x 7168 484 to 504 us (1.67 to 1.74 PFLOP/s, the tensor pipe is busy 83%
-// of the time), gate and up of 2048 by 7168 for 8191 rows 280 (1.72), 509 x 7168 x 7168 40.4.
-// What is left of the large ones is power (the clock falls) and the last round's tiles; the
-// small ones' bound is what the SMs take in, 14.5 TB/s together (509 rows: 488 MB, 34 us): a
-// second pair that got the weights by the same copies went no faster (39.8 for 39.3).  Tiles
-// of a short k are bound by their outputs, about 12 ns a column of a tile: 4346 x 3960 x 192
-// 22 us, 25 where rows start on 8 bytes, 30 on 4 and 42 on 2.  k shared by two pairs was no
-// faster than the clusters of the kernel for few rows.
+// Measured: 8191 x 7168 x 7168 483 to 504 us (1.67 to 1.74 PFLOP/s, the tensor pipe is busy 83%
+// of the time), gate and up of 2048 by 7168 for 8191 rows 278 (1.73), 509 x 7168 x 7168 40.9.
+// What is left of the large ones is power (the clock falls) and the last round's tiles.  The
+// small ones wait for what the SMs take in: 509 rows go as tiles 224 wide to 64 of the 76
+// pairs, whose 440 MB take 30 us at 14.5 TB/s; the first loads and the outputs take 6 more, and
+// about 5 are not accounted for.  A second pair that got the weights by the same copies went no
+// faster (39.8 for 39.3).  Tiles of a short k are bound by their outputs, about 12 ns a column
+// of a tile: 4346 x 3960 x 192 21 us, 24.5 where rows start on 8 bytes, 29 on 4 and 41 on 2.  k
+// shared by two pairs was no faster than the clusters of the kernel for few rows.
 #pragma once
 
 #include "act.cuh"

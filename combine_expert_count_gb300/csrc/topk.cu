@@ -8,8 +8,9 @@
 // token in 2000 at 256 experts).  A warp has a token, or, for up to eight of up to 512
 // experts, four.
 //
-// Measured: 32767 tokens, 8 of 128 experts 11.6 us (1.6 TB/s), of 256 16.8 (2.1 TB/s);
-// 2048 tokens, 8 of 256 4.3, with a bias and four of eight runs kept 9.7.  It is bound
+// Measured: 32767 tokens, 8 of 128 experts 11.6 us (1.6 TB/s), of 256 16.7 (2.1 TB/s), with
+// a bias and four of eight runs kept 37.5; 2048 tokens, 8 of 256 4.3, with a bias 7.0, and
+// four of eight runs kept 8.5, 32 of 1024 24.  It is bound
 // by instructions: at 128 experts about 150 a token and lane of eight, most of them in
 // the sorting networks (19 exchanges for eight keys, 12 for each further eight and each
 // doubling of the lanes); one token after another by whole warps took 26 us.  Few
@@ -360,7 +361,7 @@ __device__ __forceinline__ uint32_t kept_runs(const Router &p, const float *l, c
     if (p.per >= 4 && p.per <= 128 && (p.per & (p.per - 1)) == 0) {
         // a run is p.per / 4 neighbouring lanes' quads: their best two by exchanges.  The
         // way below asks all lanes for each run: 2048 tokens, 256 experts in eight runs
-        // 24.0 us that way, 9.5 this
+        // 24.0 us that way, 8.5 this
         float worths[C];
         run_values(p, v, key, top, inv_sum, scored, worths);
 #pragma unroll
@@ -887,9 +888,9 @@ static cudaError_t launch(K kern, int tokens, int warps, const Router &p, cudaSt
 
 static cudaError_t launch_topk(const Router &p, cudaStream_t st) {
     // us with a warp and with eight lanes a token, 256 experts: one token 3.5 and 3.2, 2048
-    // 6.6 and 4.3, 32767 32 and 17; with a bias and four of eight runs 8 tokens 4.6 and
-    // 6.1, 2048 9.7 and 12.2, 8192 16 and 23, 32767 53 and 38: there some tokens go the
-    // warp's way after the other
+    // 6.4 and 4.3, 32767 36 and 17; with a bias and four of eight runs 8 tokens 4.4 and
+    // 6.2, 2048 8.4 and 10.7, 8192 16 and 20.5, 12288 22.2 and 21.7, 16384 28 and 24.5,
+    // 32767 52 and 37.5: there some tokens go the warp's way after the other
     if (p.R <= kFastMost && p.E >= 32 && p.E <= 512 && p.E % 4 == 0 &&
         (p.groups == p.kept || p.per % 32 == 0) && (!p.bias || p.rows > 96 * sm_count())) {
         const auto kern = p.E <= 128   ? k_topk_fast<16>
